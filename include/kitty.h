@@ -297,6 +297,124 @@ int kitty_decode_attention_noalloc(const kitty_cfg* cfg, const void* q, const vo
                                    const int32_t* tail_len, float sm_scale, void* out,
                                    int32_t out_dtype, int32_t B, int32_t* d_status, void* stream);
 
+/* ---------------------------------------------------------------- positions
+ * Per-head RMS norm and position rotation of queries and keys, as models apply them
+ * before attention.  Per token at position p and head row x[128]:
+ *   norm   (weight given)  n = x / sqrt(mean(x^2) + eps) * weight
+ *   rotate                 pair j < rot_dim / 2 of n, the channels (j, j + rot_dim/2)
+ *                          (KITTY_ROPE_HALF) or (2j, 2j + 1)
+ *                          (KITTY_ROPE_INTERLEAVED), turns by t = p * f_j:
+ *                          (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t)
+ * Channels from rot_dim on are normed only.  All in fp32, rounded once to the
+ * 16-bit type; angles are exact to 2^-32 of a turn at every int32 position
+ * (negative ones too), given the table below. */
+#define KITTY_ROPE_HALF 0
+#define KITTY_ROPE_INTERLEAVED 1
+
+typedef struct {
+  int32_t rot_dim;      /* rotated channels: 0, 16, 32, ..., 128 */
+  int32_t layout;       /* KITTY_ROPE_HALF or KITTY_ROPE_INTERLEAVED */
+  float amplitude;      /* factor on the rotated channels (1 unless the scaling has one) */
+  float eps;            /* the norm's epsilon, >= 0 */
+  const uint64_t* turns;  /* device [rot_dim / 2], kitty_rope_turns; 8-byte aligned */
+  const void* q_weight; /* device [128] 16-bit (in_dtype); NULL: queries are not normed */
+  const void* k_weight; /* the same for keys */
+} kitty_rope;
+
+/* Frequencies of the pairs: f_j = base^(-2j/rot_dim), stretched for contexts
+ * longer than the trained one (`factor` times as long). */
+#define KITTY_ROPE_PLAIN 0  /* as they are */
+#define KITTY_ROPE_LINEAR 1 /* f / factor (position interpolation) */
+#define KITTY_ROPE_NTK 2    /* base * factor^(rot_dim / (rot_dim - 2)) for base */
+#define KITTY_ROPE_YARN 3   /* with D(n) = rot_dim ln(trained / (2 pi n)) / (2 ln base), the pair that
+                               turns n times over the trained length: pairs below floor(D(fast))
+                               keep f, pairs above ceil(D(slow)) take f / factor, a linear ramp
+                               between (bounds clamped to [0, rot_dim - 1]);
+                               amplitude 0.1 ln(factor) + 1 */
+#define KITTY_ROPE_BANDS 4  /* wavelengths 2 pi / f above trained / slow take f / factor, those below
+                               trained / fast keep f, between them
+                               u = (trained f / (2 pi) - slow) / (fast - slow) mixes
+                               (1 - u) f / factor + u f */
+typedef struct {
+  int32_t kind;         /* KITTY_ROPE_PLAIN ... KITTY_ROPE_BANDS */
+  int32_t trained;      /* trained context length (YARN, BANDS), >= 1 */
+  double factor;        /* >= 1 */
+  double fast, slow;    /* turns over the trained length, fast > slow > 0 (YARN: 32 and 1;
+                           BANDS: 4 and 1, where they are not set by the model) */
+} kitty_rope_scaling;
+
+/* Host: rot_dim / 2 frequencies (radians a position) and the amplitude that goes
+ * with them.  scaling may be NULL (plain); base > 1. */
+int kitty_rope_frequencies(int32_t rot_dim, double base, const kitty_rope_scaling* scaling,
+                           double* inv_freq, double* amplitude);
+
+/* Host: the table of kitty_rope.turns for any n frequencies (radians a position, finite):
+ * each as a fraction of a turn, f / 2 pi modulo 1, times 2^64.  The caller copies it to
+ * the device. */
+int kitty_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/* Norm and rotation of n_tokens tokens' queries and keys in one pass.
+ *   q          device [n_tokens][Hq][128] 16-bit, q_stride elements from token to token
+ *              (>= 128 Hq, a multiple of 8: a slice of a joint projection will do);
+ *              k likewise [n_tokens][Hkv][128].  Either may be NULL (not both)
+ *   positions  device int32 [n_tokens]
+ *   q_out, k_out  the same shapes, with strides of their own; may be q and k (in place),
+ *              otherwise no overlap
+ * Rows 16-byte aligned. */
+int kitty_norm_rope(const kitty_cfg* cfg, const kitty_rope* rope, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const int32_t* positions, int32_t n_tokens,
+                    void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                    void* stream);
+
+/* kitty_append_token with norm and rotation on the way: the token's position is
+ * pos_base[b] + 32 * num_pages[b] + tail_len[b] (before the append); its normed and rotated
+ * key goes into the tail (and, when the tail fills, is quantized with it), its value goes
+ * in as it is, and its normed and rotated query row to q_out.
+ *   q, k_new, v_new, q_out  as in kitty_norm_rope, one token a sequence; q may be NULL
+ *   pos_base   device int32 [B] or NULL (0): positions before this cache's first token,
+ *              e.g. a shared prefix
+ *   counted    0: tail_len, num_pages and block_table are advanced as by
+ *              kitty_append_token.  1: they count the new token already and are left as
+ *              they are (layers that share one set of lengths: the first layer's append
+ *              advances them, the others pass 1); a flush shows as tail_len 0 with a page
+ *              id in flush_page_ids
+ * Other arguments, layouts and status codes as for kitty_append_token; a num_pages
+ * outside [0, max_pages] sets KITTY_ST_BAD_LEN.  A sequence that is refused keeps its
+ * tail, lengths and q_out row. */
+int kitty_append_rope(const kitty_cfg* cfg, const kitty_rope* rope, const void* q, int64_t q_stride,
+                      const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                      void* q_out, int64_t q_out_stride, void* tail_k, void* tail_v,
+                      int32_t* tail_len, float* run_sum, float* run_sumsq, int32_t* run_count,
+                      const int32_t* flush_page_ids, int32_t* block_table, int32_t max_pages,
+                      int32_t* num_pages, void* pool, int32_t pool_pages, const int32_t* pos_base,
+                      int32_t counted, int32_t B, int32_t* d_status, void* stream);
+
+/* Norm, rotation and append into the 16-bit paged cache (layout and conventions of
+ * kitty_f16kv_append below), one token or a ragged run of tokens a sequence.
+ *   q, k_new, v_new, q_out  as in kitty_norm_rope, n_tokens rows; q may be NULL
+ *   seq_start  device int32 [B + 1], rising from 0: sequence b appends tokens
+ *              seq_start[b] .. seq_start[b+1] - 1 (none is fine); rows from seq_start[B] on are
+ *              padding, neither read into the cache nor written to q_out.  NULL:
+ *              n_tokens = B, one token each
+ *   Token i of a sequence's n goes to position ctx_len[b] + i of its pages, and turns by
+ *   that plus pos_base[b] (NULL: 0).
+ *   new_page_ids  device int32 [n_tokens]: entry t is the page for token t where that token
+ *              begins a page (slot 0), else ignored; entered in the block table
+ *   counted    0: ctx_len[b] advances by n.  1: ctx_len and block_table hold the new tokens
+ *              already and are left as they are; new_page_ids is ignored
+ * Tokens of a page id out of range are skipped (KITTY_ST_BAD_PAGE) and their sequence is not
+ * advanced; a sequence without room for its n tokens (KITTY_ST_TABLE_FULL, or
+ * KITTY_ST_BAD_LEN for a length outside the table) appends nothing; starts out of order:
+ * KITTY_ST_BAD_SEQ. */
+int kitty_f16kv_append_rope(const kitty_cfg* cfg, const kitty_rope* rope, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, int32_t n_tokens, void* q_out,
+                            int64_t q_out_stride, void* pool, int32_t pool_pages,
+                            int32_t* block_table, int32_t max_pages, int32_t* ctx_len,
+                            const int32_t* new_page_ids, const int32_t* seq_start,
+                            const int32_t* pos_base, int32_t counted, int32_t B, int32_t* d_status,
+                            void* stream);
+
 /* ---------------------------------------------------------------- 16-bit paged baseline
  * The unquantized paged KV cache that Kitty's memory budget and throughput are
  * compared against (paper: Abstract, "up to 8x larger batches and 2.1x-4.1x

@@ -13,7 +13,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libkitty.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-CU = ["quantize.cu", "decode.cu", "fp16kv.cu"]
+CU = ["quantize.cu", "decode.cu", "fp16kv.cu", "rope.cu"]
+HEADERS = ["kitty_common.cuh", "quant_tile.cuh", "host_common.h", "rope.cuh", "grid_dep.cuh"]
 CPP = ["host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -26,7 +27,7 @@ def _nvcc():
 
 
 def _sources():
-    return [os.path.join(CSRC, f) for f in CU + CPP + ["kitty_common.cuh", "quant_tile.cuh", "host_common.h"]] + [
+    return [os.path.join(CSRC, f) for f in CU + CPP + HEADERS] + [
         os.path.join(INCLUDE, "kitty.h")]
 
 

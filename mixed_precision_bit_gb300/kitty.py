@@ -21,6 +21,9 @@ ST = dict(OK=0, EMPTY=1, RANGE=2, NONFINITE=3, BAD_PAGE=4, BAD_LEN=5, TAIL_FULL=
           BAD_FLUSH=7, TABLE_FULL=8, BAD_SEQ=9, TIMEOUT=10)
 F16, BF16, F32 = 0, 1, 2
 RANK_PAGE, RANK_RUNNING, RANK_SEQUENCE = 0, 1, 2
+D = 128  # channels of a head
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
 
 
 class KittyError(RuntimeError):
@@ -61,6 +64,17 @@ class Config:
                     self.decode_max_pages, self.decode_wait_polls, self.v_bit)
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("eps", ctypes.c_float), ("turns", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("trained", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
+
+
 _lib = None
 EXPORTS = ("kitty_abi_version", "kitty_page_bytes", "kitty_avg_bits", "kitty_alloc_create",
            "kitty_alloc_pages", "kitty_free_pages", "kitty_alloc_free_count",
@@ -68,7 +82,8 @@ EXPORTS = ("kitty_abi_version", "kitty_page_bytes", "kitty_avg_bits", "kitty_all
            "kitty_decode_workspace_bytes", "kitty_decode_attention", "kitty_decode_plan",
            "kitty_decode_attention_noalloc", "kitty_append_decode", "kitty_f16kv_page_bytes",
            "kitty_f16kv_write_pages", "kitty_f16kv_append", "kitty_f16kv_workspace_bytes",
-           "kitty_f16kv_decode")
+           "kitty_f16kv_decode", "kitty_rope_frequencies", "kitty_rope_turns", "kitty_norm_rope",
+           "kitty_append_rope", "kitty_f16kv_append_rope")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -82,7 +97,7 @@ def load():
     if _lib is None:
         path = _build.build()
         L = ctypes.CDLL(path)
-        P, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         C = ctypes.POINTER(_Cfg)
         sig = {
             "kitty_abi_version": (ctypes.c_int, []),
@@ -109,6 +124,17 @@ def load():
             "kitty_f16kv_write_pages": (ctypes.c_int, [C, P, P, i32, P, P, i32, P, P]),
             "kitty_f16kv_append": (ctypes.c_int, [C, P, P, P, i32, P, i32, P, P, i32, P, P]),
             "kitty_f16kv_workspace_bytes": (ctypes.c_int, [C, i32, i32, ctypes.POINTER(sz)]),
+            "kitty_rope_frequencies": (ctypes.c_int, [i32, ctypes.c_double, ctypes.POINTER(_RopeScaling),
+                                                      P, ctypes.POINTER(ctypes.c_double)]),
+            "kitty_rope_turns": (ctypes.c_int, [P, i32, P]),
+            "kitty_norm_rope": (ctypes.c_int, [C, ctypes.POINTER(_Rope), P, i64, P, i64, P, i32, P,
+                                               i64, P, i64, P]),
+            "kitty_append_rope": (ctypes.c_int, [C, ctypes.POINTER(_Rope), P, i64, P, i64, P, i64, P,
+                                                 i64, P, P, P, P, P, P, P, P, i32, P, P, i32, P, i32,
+                                                 i32, P, P]),
+            "kitty_f16kv_append_rope": (ctypes.c_int, [C, ctypes.POINTER(_Rope), P, i64, P, i64, P,
+                                                       i64, i32, P, i64, P, i32, P, i32, P, P, P, P,
+                                                       i32, i32, P, P]),
             "kitty_f16kv_decode": (ctypes.c_int, [C, P, P, i32, P, i32, P, ctypes.c_float, P, i32,
                                                   P, sz, i32, P, P]),
         }
@@ -276,6 +302,157 @@ def append_decode(cfg: Config, k_new, v_new, q, tail_k, tail_v, tail_len, run_su
         _ptr(block_table), block_table.shape[1], _ptr(num_pages), _ptr(pool), pool_pages,
         float(sm_scale), _ptr(out), out_dtype, _ptr(workspace), ws_bytes, B, _ptr(status),
         _stream(stream)))
+
+
+# ------------------------------------------------------------------ positions
+def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN,
+                     factor: float = 1.0, trained: int = 0, fast: float = None, slow: float = 1.0):
+    """(frequencies, amplitude): radians a position of each of the rot_dim / 2 pairs, in 64
+    bits, and the factor on the rotated channels, stretched by `kind` (ROPE_*) to `factor`
+    times the `trained` length (kitty_rope_frequencies)."""
+    import numpy as np
+    if fast is None:
+        fast = 32.0 if kind == ROPE_YARN else 4.0
+    f = np.zeros(max(rot_dim // 2, 1), np.float64)
+    amp = ctypes.c_double()
+    sc = _RopeScaling(kind, trained, factor, fast, slow)
+    _chk("kitty_rope_frequencies", load().kitty_rope_frequencies(
+        rot_dim, base, ctypes.byref(sc), f.ctypes.data, ctypes.byref(amp)))
+    return f[:rot_dim // 2], amp.value
+
+
+class Rope:
+    """A position rotation with the norms before it (kitty_rope): the frequencies' table on
+    the device, the pairs' layout, and the norms' weights (16-bit [128]; None: not normed).
+    inv_freq: radians a position of each pair (rope_frequencies, or a model's own); empty
+    for norms alone."""
+
+    def __init__(self, inv_freq, layout: int = ROPE_HALF, amplitude: float = 1.0, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, device="cuda"):
+        import numpy as np
+        import torch
+        f = np.ascontiguousarray(inv_freq, np.float64)
+        turns = np.zeros(f.size, np.uint64)
+        _chk("kitty_rope_turns", load().kitty_rope_turns(f.ctypes.data, f.size, turns.ctypes.data))
+        for w in (q_weight, k_weight):
+            if w is not None and (w.numel() != D or w.element_size() != 2):
+                raise ValueError("kitty: norm weights are 16-bit [%d]" % D)
+        self.rot_dim, self.layout, self.amplitude, self.eps = 2 * f.size, layout, amplitude, eps
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self._c = _Rope(self.rot_dim, layout, amplitude, eps, _ptr(self.turns), _ptr(q_weight),
+                        _ptr(k_weight))
+
+    def c(self):
+        return self._c
+
+
+def _rows(t, heads: int):
+    """(device address, elements from token to token) of rows [n, heads, 128]: 16-bit, each
+    token's heads dense, any stride between tokens."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.element_size() != 2:
+        raise ValueError("kitty: expected 16-bit rows [n, %d, %d] (got %s, %s)"
+                         % (heads, D, tuple(t.shape), t.dtype))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
+        raise ValueError("kitty: the heads of a token must be contiguous (strides %s)" % (t.stride(),))
+    if t.shape[0] <= 1:  # the stride between tokens of one token says nothing
+        s0 = heads * D
+    return t.data_ptr(), s0
+
+
+def _on_current_device(*tensors):
+    """Every tensor in the current CUDA device's memory: the launch goes to its stream."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("kitty: tensor arguments must be in device memory (got %s)" % t.device)
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError("kitty: a tensor is on cuda:%d, the current device is cuda:%d"
+                             % (t.get_device(), dev))
+
+
+def _ints(name: str, t, n: int):
+    """Address of a dense int32 array of at least n entries."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() < n:
+        raise ValueError("kitty: %s must be int32 with %d entries (got %s, %s)"
+                         % (name, n, tuple(t.shape), t.dtype))
+    return _ptr(t)
+
+
+def _table(t, B: int):
+    """(address, entries of a row) of a block table [>= B, max_pages]."""
+    if t.dim() != 2 or t.shape[0] < B:
+        raise ValueError("kitty: the block table must be [%d, max_pages] (got %s)" % (B, tuple(t.shape)))
+    return _ints("block_table", t, 0), t.shape[1]
+
+
+def norm_rope(cfg: Config, rope: Rope, q, k, positions, q_out, k_out, stream=None):
+    """Per-head norms and the position rotation of queries q [n, Hq, 128] and keys k
+    [n, Hkv, 128] at positions [n] into q_out and k_out (which may be q and k); q or k may
+    be None.  Rows may be slices of a joint projection (any token stride)."""
+    _on_current_device(q, k, positions, q_out, k_out, rope.turns)
+    n = positions.numel()
+    a = []
+    for x, y, heads in ((q, q_out, cfg.num_q_heads), (k, k_out, cfg.num_kv_heads)):
+        if (x is None) != (y is None) or (x is not None and (x.shape[0] != n or y.shape[0] != n)):
+            raise ValueError("kitty: %d positions need as many rows in and out" % n)
+        a.append(_rows(x, heads) + _rows(y, heads))
+    _chk("kitty_norm_rope", load().kitty_norm_rope(
+        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), a[0][0], a[0][1], a[1][0], a[1][1],
+        _ints("positions", positions, n), n, a[0][2], a[0][3], a[1][2], a[1][3], _stream(stream)))
+
+
+def append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, tail_k, tail_v, tail_len, run_sum,
+                run_sumsq, run_count, flush_page_ids, block_table, num_pages, pool,
+                pool_pages: int, pos_base=None, counted: bool = False, status=None, stream=None):
+    """append_token with norm and rotation on the way (kitty_append_rope): the rotated query
+    rows go to q_out (q and q_out may be None), the rotated key into the tail."""
+    B = tail_len.numel()
+    _on_current_device(q, k_new, v_new, q_out, tail_k, tail_v, tail_len, run_sum, run_sumsq,
+                       run_count, flush_page_ids, block_table, num_pages, pool, pos_base, status,
+                       rope.turns)
+    (qp, qs), (op, os_) = _rows(q, cfg.num_q_heads), _rows(q_out, cfg.num_q_heads)
+    (kp, ks), (vp, vs) = _rows(k_new, cfg.num_kv_heads), _rows(v_new, cfg.num_kv_heads)
+    for x in (q, k_new, v_new, q_out):
+        if x is not None and x.shape[0] != B:
+            raise ValueError("kitty: %d sequences need as many rows (got %s)" % (B, tuple(x.shape)))
+    _chk("kitty_append_rope", load().kitty_append_rope(
+        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), qp, qs, kp, ks, vp, vs, op, os_, _ptr(tail_k),
+        _ptr(tail_v), _ptr(tail_len), _ptr(run_sum), _ptr(run_sumsq), _ptr(run_count),
+        _ints("flush_page_ids", flush_page_ids, B), *_table(block_table, B),
+        _ints("num_pages", num_pages, B), _ptr(pool), pool_pages, _ints("pos_base", pos_base, B),
+        int(counted), B, _ptr(status), _stream(stream)))
+
+
+def f16kv_append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, pool, pool_pages: int,
+                      block_table, ctx_len, new_page_ids, seq_start=None, pos_base=None,
+                      counted: bool = False, status=None, stream=None):
+    """Norm, rotation and append into the 16-bit paged cache (kitty_f16kv_append_rope): one
+    token a sequence, or the runs that seq_start [B + 1] marks; rows behind the last run
+    are left alone."""
+    B, n = ctx_len.numel(), k_new.shape[0]
+    _on_current_device(q, k_new, v_new, q_out, pool, block_table, ctx_len, new_page_ids, seq_start,
+                       pos_base, status, rope.turns)
+    (qp, qs), (op, os_) = _rows(q, cfg.num_q_heads), _rows(q_out, cfg.num_q_heads)
+    (kp, ks), (vp, vs) = _rows(k_new, cfg.num_kv_heads), _rows(v_new, cfg.num_kv_heads)
+    for x in (q, v_new, q_out):
+        if x is not None and x.shape[0] != n:
+            raise ValueError("kitty: %d tokens need as many rows (got %s)" % (n, tuple(x.shape)))
+    _chk("kitty_f16kv_append_rope", load().kitty_f16kv_append_rope(
+        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), qp, qs, kp, ks, vp, vs, n, op, os_, _ptr(pool),
+        pool_pages, *_table(block_table, B), _ptr(ctx_len),
+        _ints("new_page_ids", new_page_ids, n), _ints("seq_start", seq_start, B + 1),
+        _ints("pos_base", pos_base, B), int(counted), B, _ptr(status), _stream(stream)))
 
 
 # ------------------------------------------------------------------ 16-bit paged baseline
