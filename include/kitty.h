@@ -297,6 +297,39 @@ int kitty_decode_attention_noalloc(const kitty_cfg* cfg, const void* q, const vo
                                    const int32_t* tail_len, float sm_scale, void* out,
                                    int32_t out_dtype, int32_t B, int32_t* d_status, void* stream);
 
+/* ---------------------------------------------------------------- shared prefix
+ * kitty_decode_attention for a batch whose sequences share a prefix: the prefix's pages
+ * are attended once for the whole batch, each sequence's own pages and tail as by
+ * kitty_decode_attention, and the two merged in one softmax:
+ *   out[b][hq] = softmax_t(sm_scale * q.k_t) . v_t over the first prefix_pages[b] pages of
+ *   prefix_table, then the num_pages[b] pages of block_table[b] and the tail.
+ *   prefix_table  device int32 [n_prefix]: the prefix's pages, in the same pool
+ *   prefix_pages  device int32 [B] in [0, n_prefix] (a sequence that forked off earlier
+ *                 shares fewer pages; 0: none), or NULL: all share all n_prefix pages.  A
+ *                 value outside sets KITTY_ST_BAD_LEN and counts as 0
+ *   q             16-byte aligned
+ *   workspace     device, >= kitty_shared_workspace_bytes(cfg, B, n_prefix, max_pages),
+ *                 16-byte aligned; calls that may overlap need one each
+ * Other arguments, layouts and status codes as for kitty_decode_attention.  A prefix page
+ * id out of range sets KITTY_ST_BAD_PAGE and its tokens are left out.  A sequence is not
+ * affected by what prefix pages hold that it does not share.  A prefix page with a stored
+ * step so large that a step times a code may leave fp16's range (a step above 65504 / 2^bits;
+ * channels or groups that span more than half the range of the input rule) sets
+ * KITTY_ST_RANGE, and the outputs of the sequences that share it are then undefined.
+ * Launches, in stream order: the decode kernel, the prefix kernel, the merge; all three can
+ * be captured. */
+int kitty_shared_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_prefix,
+                                 int32_t max_pages, size_t* bytes);
+int kitty_decode_attention_shared(const kitty_cfg* cfg, const void* q, const void* pool,
+                                  int32_t pool_pages, const int32_t* prefix_table,
+                                  int32_t n_prefix, const int32_t* prefix_pages,
+                                  const int32_t* block_table, int32_t max_pages,
+                                  const int32_t* num_pages, const void* tail_k,
+                                  const void* tail_v, const int32_t* tail_len, float sm_scale,
+                                  void* out, int32_t out_dtype, void* workspace,
+                                  size_t workspace_bytes, int32_t B, int32_t* d_status,
+                                  void* stream);
+
 /* ---------------------------------------------------------------- positions
  * Per-head RMS norm and position rotation of queries and keys, as models apply them
  * before attention.  Per token at position p and head row x[128]:
@@ -465,6 +498,18 @@ int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const void* pool, in
  * takes the tail tokens. */
 int kitty_decode_plan(const kitty_cfg* cfg, int32_t B, int32_t max_pages, int32_t* splits,
                       int32_t* pages_per_split);
+
+/* kitty_f16kv_decode for a batch whose sequences share a prefix of full pages: the
+ * arguments of kitty_decode_attention_shared and of kitty_f16kv_decode; ctx_len[b] counts a
+ * sequence's own tokens, behind the prefix. */
+int kitty_f16kv_shared_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_prefix,
+                                       int32_t max_pages, size_t* bytes);
+int kitty_f16kv_decode_shared(const kitty_cfg* cfg, const void* q, const void* pool,
+                              int32_t pool_pages, const int32_t* prefix_table, int32_t n_prefix,
+                              const int32_t* prefix_pages, const int32_t* block_table,
+                              int32_t max_pages, const int32_t* ctx_len, float sm_scale, void* out,
+                              int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                              int32_t B, int32_t* d_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -44,6 +44,7 @@
 #include "kitty_common.cuh"
 #include "quant_tile.cuh"
 #include "host_common.h"
+#include "partials.h"
 
 #include <algorithm>
 #include <atomic>
@@ -83,6 +84,7 @@ static_assert(sizeof(QuantSmem) <= (size_t)kDWarps * stages_for(2) * 3072 &&
 constexpr int kQx = kD + 2;
 constexpr uint32_t kWaitLimit = 1u << 22;  // polls of one barrier phase (~0.1-1 s)
 constexpr int kPartial = kD + 4;           // split partial: m, l, 2 unused, o[128] (16-byte aligned)
+static_assert(kPartial == kPartialFloats, "the layout that decode_partials hands out");
 constexpr int kMaxSplits = 256;            // splits per sequence, at most
 // Running-max floor (log2 units): finite, so masked scores (-inf) give p = 0 exactly.
 constexpr float kNegBig = -1.0e30f;
@@ -1726,6 +1728,14 @@ void plan(const kitty_cfg* cfg, int B, int M, int blob, Schedule* sc) {
   }
 }
 
+// The decode kernel leaves partials when there is more than one split: a schedule of one
+// gets a second split without pages.
+void at_least_two(Schedule* sc) {
+  if (sc->splits > 1) return;
+  sc->starts[2] = sc->starts[1];
+  sc->splits = 2;
+}
+
 size_t workspace_bytes(const kitty_cfg* cfg, int B, const Schedule& sc) {
   return sc.splits > 1 ? (size_t)B * cfg->num_q_heads * sc.splits * kPartial * sizeof(float) : 0;
 }
@@ -1762,7 +1772,7 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
               const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
               const void* tail_k, const void* tail_v, const int32_t* tail_len, float sm_scale,
               void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes_in, int32_t B,
-              int32_t* d_status, void* stream, const AppendParams& ap) {
+              int32_t* d_status, void* stream, const AppendParams& ap, int* partial_splits = nullptr) {
   int rc = check_cfg(cfg, kMaxGroup);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
@@ -1779,6 +1789,7 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
   DecodeParams p = {};
   Schedule sc;
   plan(cfg, B, max_pages, blob, &sc);
+  if (partial_splits != nullptr) at_least_two(&sc);
   const size_t need = workspace_bytes(cfg, B, sc);
   if (workspace_bytes_in < need || (need > 0 && (!workspace || !aligned16(workspace))))
     return KITTY_ERR_WORKSPACE;
@@ -1822,6 +1833,10 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
                                     : launch_decode_nx<KITTY_F16, 4, 2>(nx, grid, smem, s, p))
                           : launch_decode_nx<KITTY_F16, 2, 2>(nx, grid, smem, s, p));
   if (e != cudaSuccess) return KITTY_ERR_CUDA;
+  if (partial_splits != nullptr) {
+    *partial_splits = sc.splits;
+    return KITTY_OK;
+  }
   // the merge step follows the decode grid as a programmatic dependent
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1898,6 +1913,24 @@ extern "C" int kitty_append_decode(const kitty_cfg* cfg, const void* k_new, cons
   return attention(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k, tail_v,
                    tail_len, sm_scale, out, out_dtype, workspace, workspace_bytes, B, d_status,
                    stream, ap);
+}
+
+// ------------------------------------------------------------------ partials alone
+size_t kitty::decode_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
+  Schedule sc;
+  plan(cfg, B, max_pages, (int)blob_bytes(cfg->n_hi, cfg->lo_bit, v_bits(cfg)), &sc);
+  at_least_two(&sc);
+  return workspace_bytes(cfg, B, sc);
+}
+
+int kitty::decode_partials(const kitty_cfg* cfg, const void* q, const void* pool, int32_t pool_pages,
+                           const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
+                           const void* tail_k, const void* tail_v, const int32_t* tail_len,
+                           float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
+                           int32_t B, int32_t* d_status, void* stream, int* splits) {
+  const AppendParams none = {};
+  return attention(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k, tail_v,
+                   tail_len, sm_scale, out, out_dtype, ws, ws_bytes, B, d_status, stream, none, splits);
 }
 
 // ------------------------------------------------------------------ no-allocation variant

@@ -21,6 +21,7 @@
 // Splits are merged by a second kernel in split order.
 #include "kitty_common.cuh"
 #include "host_common.h"
+#include "partials.h"
 
 #include <algorithm>
 #include <atomic>
@@ -37,6 +38,7 @@ constexpr int kRowPad = kRowB + 16;           // staged row stride
 constexpr int kFBlob = 2 * kPage * kRowB;     // 16384: K then V of one (page, kv head)
 constexpr int kFStage = 2 * kHalf * kRowPad;  // 8704: one staged half page (K rows, V rows)
 constexpr int kFPartial = kD + 4;             // split partial: m, l, 2 unused, o[128]
+static_assert(kFPartial == kPartialFloats, "the layout that f16kv_partials hands out");
 constexpr uint32_t kFWaitLimit = 1u << 22;
 constexpr int kFMaxSplits = 64;
 
@@ -453,12 +455,15 @@ extern "C" int kitty_f16kv_workspace_bytes(const kitty_cfg* cfg, int32_t B, int3
   return KITTY_OK;
 }
 
-extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const void* pool,
-                                  int32_t pool_pages, const int32_t* block_table,
-                                  int32_t max_pages, const int32_t* ctx_len, float sm_scale,
-                                  void* out, int32_t out_dtype, void* workspace,
-                                  size_t workspace_bytes, int32_t B, int32_t* d_status,
-                                  void* stream) {
+namespace {
+
+// Checks and launch; with partial_splits, the partials alone (at least two a row: a plan
+// of one split gets a second one without pages).
+int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t pool_pages,
+                    const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
+                    float sm_scale, void* out, int32_t out_dtype, void* workspace,
+                    size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream,
+                    int* partial_splits) {
   const int rc = check_cfg(cfg, 4);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
@@ -471,6 +476,7 @@ extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const voi
     return KITTY_ERR_INVALID_ARG;
   F16Params p = {};
   f16kv_plan(B * cfg->num_kv_heads, max_pages, &p.splits, &p.pps);
+  if (partial_splits != nullptr) *partial_splits = p.splits = std::max(p.splits, 2);
   const size_t need =
       p.splits > 1 ? (size_t)B * cfg->num_q_heads * p.splits * kFPartial * sizeof(float) : 0;
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
@@ -494,6 +500,32 @@ extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const voi
   const cudaError_t e = cfg->in_dtype == KITTY_BF16 ? launch_f16kv<KITTY_BF16>(grid, s, p)
                                                     : launch_f16kv<KITTY_F16>(grid, s, p);
   if (e != cudaSuccess) return KITTY_ERR_CUDA;
-  if (p.splits > 1) f16kv_combine_kernel<<<(unsigned)B * cfg->num_q_heads, 128, 0, s>>>(p);
+  if (p.splits > 1 && partial_splits == nullptr) f16kv_combine_kernel<<<(unsigned)B * cfg->num_q_heads, 128, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const void* pool,
+                                  int32_t pool_pages, const int32_t* block_table,
+                                  int32_t max_pages, const int32_t* ctx_len, float sm_scale,
+                                  void* out, int32_t out_dtype, void* workspace,
+                                  size_t workspace_bytes, int32_t B, int32_t* d_status,
+                                  void* stream) {
+  return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
+                         out_dtype, workspace, workspace_bytes, B, d_status, stream, nullptr);
+}
+
+size_t kitty::f16kv_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
+  int splits = 1, pps = 1;
+  f16kv_plan(B * cfg->num_kv_heads, max_pages, &splits, &pps);
+  return (size_t)B * cfg->num_q_heads * std::max(splits, 2) * kFPartial * sizeof(float);
+}
+
+int kitty::f16kv_partials(const kitty_cfg* cfg, const void* q, const void* pool, int32_t pool_pages,
+                          const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
+                          float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
+                          int32_t B, int32_t* d_status, void* stream, int* splits) {
+  return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
+                         out_dtype, ws, ws_bytes, B, d_status, stream, splits);
 }

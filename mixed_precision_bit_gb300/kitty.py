@@ -83,7 +83,9 @@ EXPORTS = ("kitty_abi_version", "kitty_page_bytes", "kitty_avg_bits", "kitty_all
            "kitty_decode_attention_noalloc", "kitty_append_decode", "kitty_f16kv_page_bytes",
            "kitty_f16kv_write_pages", "kitty_f16kv_append", "kitty_f16kv_workspace_bytes",
            "kitty_f16kv_decode", "kitty_rope_frequencies", "kitty_rope_turns", "kitty_norm_rope",
-           "kitty_append_rope", "kitty_f16kv_append_rope")
+           "kitty_append_rope", "kitty_f16kv_append_rope", "kitty_shared_workspace_bytes",
+           "kitty_decode_attention_shared", "kitty_f16kv_shared_workspace_bytes",
+           "kitty_f16kv_decode_shared")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -135,6 +137,14 @@ def load():
             "kitty_f16kv_append_rope": (ctypes.c_int, [C, ctypes.POINTER(_Rope), P, i64, P, i64, P,
                                                        i64, i32, P, i64, P, i32, P, i32, P, P, P, P,
                                                        i32, i32, P, P]),
+            "kitty_shared_workspace_bytes": (ctypes.c_int, [C, i32, i32, i32, ctypes.POINTER(sz)]),
+            "kitty_decode_attention_shared": (ctypes.c_int, [C, P, P, i32, P, i32, P, P, i32, P, P, P,
+                                                             P, ctypes.c_float, P, i32, P, sz, i32, P,
+                                                             P]),
+            "kitty_f16kv_shared_workspace_bytes": (ctypes.c_int, [C, i32, i32, i32,
+                                                                  ctypes.POINTER(sz)]),
+            "kitty_f16kv_decode_shared": (ctypes.c_int, [C, P, P, i32, P, i32, P, P, i32, P,
+                                                         ctypes.c_float, P, i32, P, sz, i32, P, P]),
             "kitty_f16kv_decode": (ctypes.c_int, [C, P, P, i32, P, i32, P, ctypes.c_float, P, i32,
                                                   P, sz, i32, P, P]),
         }
@@ -496,3 +506,64 @@ def f16kv_decode(cfg: Config, q, pool, pool_pages: int, block_table, ctx_len, sm
         ctypes.byref(cfg.c()), _ptr(q), _ptr(pool), pool_pages, _ptr(block_table),
         block_table.shape[1], _ptr(ctx_len), float(sm_scale), _ptr(out), out_dtype,
         _ptr(workspace), ws_bytes, B, _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ shared prefix
+def _out_dtype(out):
+    import torch
+    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}[out.dtype]
+
+
+def _shared_bytes(name, cfg, B, n_prefix, max_pages):
+    n = ctypes.c_size_t()
+    _chk(name, getattr(load(), name)(ctypes.byref(cfg.c()), B, n_prefix, max_pages, ctypes.byref(n)))
+    return n.value
+
+
+def shared_workspace_bytes(cfg: Config, B: int, n_prefix: int, max_pages: int) -> int:
+    return _shared_bytes("kitty_shared_workspace_bytes", cfg, B, n_prefix, max_pages)
+
+
+def f16kv_shared_workspace_bytes(cfg: Config, B: int, n_prefix: int, max_pages: int) -> int:
+    return _shared_bytes("kitty_f16kv_shared_workspace_bytes", cfg, B, n_prefix, max_pages)
+
+
+def _attended(cfg, q, out, B):
+    if q.shape != (B, cfg.num_q_heads, D) or q.element_size() != 2 or out.shape != q.shape:
+        raise ValueError("kitty: q (16-bit) and out must be [%d, %d, %d] (got %s, %s)"
+                         % (B, cfg.num_q_heads, D, tuple(q.shape), tuple(out.shape)))
+
+
+def decode_attention_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, prefix_pages,
+                            block_table, num_pages, tail_k, tail_v, tail_len, sm_scale: float, out,
+                            workspace=None, status=None, stream=None):
+    """decode_attention of a batch that shares a prefix (kitty_decode_attention_shared):
+    sequence b attends the first prefix_pages[b] pages of prefix_table (prefix_pages None: all
+    of them), then its own pages and tail."""
+    B = num_pages.numel()
+    _on_current_device(q, pool, prefix_table, prefix_pages, block_table, num_pages, tail_k, tail_v,
+                       tail_len, out, workspace, status)
+    _attended(cfg, q, out, B)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _chk("kitty_decode_attention_shared", load().kitty_decode_attention_shared(
+        ctypes.byref(cfg.c()), _ptr(q), _ptr(pool), pool_pages, _ints("prefix_table", prefix_table, 0),
+        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B), *_table(block_table, B),
+        _ptr(num_pages), _ptr(tail_k), _ptr(tail_v), _ints("tail_len", tail_len, B), float(sm_scale),
+        _ptr(out), _out_dtype(out), _ptr(workspace), ws_bytes, B, _ptr(status), _stream(stream)))
+
+
+def f16kv_decode_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, prefix_pages,
+                        block_table, ctx_len, sm_scale: float, out, workspace=None, status=None,
+                        stream=None):
+    """f16kv_decode of a batch that shares a prefix (kitty_f16kv_decode_shared); ctx_len counts
+    a sequence's own tokens."""
+    B = ctx_len.numel()
+    _on_current_device(q, pool, prefix_table, prefix_pages, block_table, ctx_len, out, workspace,
+                       status)
+    _attended(cfg, q, out, B)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _chk("kitty_f16kv_decode_shared", load().kitty_f16kv_decode_shared(
+        ctypes.byref(cfg.c()), _ptr(q), _ptr(pool), pool_pages, _ints("prefix_table", prefix_table, 0),
+        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B), *_table(block_table, B),
+        _ptr(ctx_len), float(sm_scale), _ptr(out), _out_dtype(out), _ptr(workspace), ws_bytes, B,
+        _ptr(status), _stream(stream)))

@@ -1,0 +1,77 @@
+"""Refusals of the shared-prefix calls, checked before anything is launched, and their
+workspace sizes."""
+
+import ctypes
+
+import pytest
+
+from mixed_precision_bit_gb300 import kitty as K
+
+A = 1 << 20  # a device address that is never used
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return K.load()
+
+
+def _cfg(**kw):
+    return K.Config(**{**dict(num_kv_heads=2, num_q_heads=8), **kw})
+
+
+def _packed(lib, cfg=None, **kw):
+    a = dict(q=A, pool=A, pp=4, pt=A, npre=3, pre=A, bt=A, mp=2, np=A, tk=A, tv=A, tl=A, sm=0.1, out=A, od=0,
+             ws=A, wb=1 << 30, B=2, st=None, stream=None)
+    a.update(kw)
+    return lib.kitty_decode_attention_shared(ctypes.byref((cfg or _cfg()).c()), *a.values())
+
+
+def _plain(lib, cfg=None, **kw):
+    a = dict(q=A, pool=A, pp=4, pt=A, npre=3, pre=A, bt=A, mp=2, ln=A, sm=0.1, out=A, od=0, ws=A, wb=1 << 30,
+             B=2, st=None, stream=None)
+    a.update(kw)
+    return lib.kitty_f16kv_decode_shared(ctypes.byref((cfg or _cfg()).c()), *a.values())
+
+
+def test_refusals(lib):
+    for call, extra in ((_packed, [dict(np=None), dict(tk=None), dict(tl=None), dict(tv=A + 8)]),
+                        (_plain, [dict(ln=None)])):
+        assert call(lib, B=0) == 0
+        for kw in [dict(B=-1), dict(npre=-1), dict(mp=-1), dict(pp=-1), dict(q=None), dict(out=None), dict(pool=None),
+                   dict(pool=A + 8), dict(pt=None), dict(bt=None), dict(od=3), dict(sm=float("nan")),
+                   dict(sm=float("inf")), dict(q=A + 8)] + extra:
+            assert call(lib, **kw) == -1, kw
+        for kw in (dict(ws=None), dict(ws=A + 4), dict(wb=0), dict(wb=100)):
+            assert call(lib, **kw) == -4, kw
+        assert call(lib, cfg=_cfg(head_dim=64)) == -2
+        assert call(lib, B=70000, wb=1 << 60) == -2
+    assert _packed(lib, cfg=_cfg(num_kv_heads=1, num_q_heads=33)) == -2
+    assert _plain(lib, cfg=_cfg(num_kv_heads=1, num_q_heads=5)) == -2
+
+
+def test_workspace_bytes(lib):
+    for size in (K.shared_workspace_bytes, K.f16kv_shared_workspace_bytes):
+        cfg = _cfg()
+        assert size(cfg, 0, 10, 10) == 0
+        rows = 5 * 8 * 132 * 4
+        n0 = size(cfg, 5, 0, 10)                      # no prefix: the own partials
+        assert n0 >= 2 * rows and n0 % rows == 0
+        n1 = size(cfg, 5, 100, 10)
+        assert n1 > n0 and (n1 - n0) % rows == 0
+        for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, -1)):
+            with pytest.raises(K.KittyError) as e:
+                size(cfg, *bad)
+            assert e.value.code == -1
+
+
+def test_binding_checks_shapes():
+    import torch
+    cfg = _cfg()
+    out = torch.zeros(2, 8, 128)
+    with pytest.raises(ValueError):
+        K._attended(cfg, torch.zeros(2, 7, 128, dtype=torch.int16), out, 2)
+    with pytest.raises(ValueError):
+        K._attended(cfg, torch.zeros(2, 8, 128), out, 2)
+    with pytest.raises(ValueError):
+        K._table(torch.zeros(1, 4, dtype=torch.int32), 2)
+    K._attended(cfg, torch.zeros(2, 8, 128, dtype=torch.int16), out, 2)
