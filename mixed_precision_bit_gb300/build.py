@@ -13,9 +13,9 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libkitty.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-CU = ["quantize.cu", "decode.cu", "fp16kv.cu", "rope.cu", "shared.cu"]
+CU = ["quantize.cu", "decode.cu", "fp16kv.cu", "rope.cu", "shared.cu", "prefix.cu"]
 HEADERS = ["kitty_common.cuh", "quant_tile.cuh", "host_common.h", "rope.cuh", "grid_dep.cuh",
-           "partials.h"]
+           "partials.h", "prefix.h", "tcgen05.cuh"]
 CPP = ["host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,792 @@
+// Attention of a whole batch's queries to the pages that its sequences share, on the
+// fifth-generation tensor cores (sm_103a).
+//
+// Rows.  All query heads of a kv head over all sequences attend the same Keys and Values:
+// R = B * Hq / Hkv rows.  One block takes up to 256 of them, as two tiles of 128 (the two
+// "lanes" below), and a contiguous split of the prefix; with R <= 128 both lanes hold the
+// same 128 rows and take alternate tiles of the split.  Per tile of kTok tokens and lane:
+//   S = Q K^T          tcgen05.mma, 128 x kTok x 128, fp32 in tensor memory
+//   p = 2^(s - m)      one thread a row: its scores from tensor memory, the running maximum
+//                      and sum in registers, p back over S as the next product's operand
+//   O += P V           tcgen05.mma with P in tensor memory, fp32 in tensor memory
+// The maximum m only moves when a score passes it by more than 2^8 (p then stays <= 256, well
+// inside fp16), so O is rescaled a few times at the start and hardly ever later.
+// Warps: 4 a lane for the softmax, one issuing products, the rest loading.  While one
+// lane's softmax runs, the tensor cores work on the other's products.
+//
+// Packed pages (tiles of three pages).  A loading warp takes one page's Keys or Values of
+// each tile, staged by bulk copies, and writes operands to shared memory in fp16:
+//   Keys    step * code, exact (a step has 7 significant bits, a code 2 or 4); the page's
+//           channel minima as one more row, so that Q K^T also gives q.M, which the
+//           softmax adds to the page's 32 scores;
+//   Values  step * code, exact, transposed; each token's four group minima as four more
+//           channels, which the end adds to the channels of their group.
+// So the only roundings are p to fp16 and, for 8-bit boosted Keys, step * code to fp16.
+//
+// 16-bit pages (tiles of four pages) come by tiled TMA loads, swizzled, the Values as they
+// lie (N contiguous).  For bf16 p is a (high, rest) pair: one bf16 would leave an error of
+// 2^-9 of p, above what the decode keeps.
+//
+// Masks.  Sequence b sees its first prefix_pages[b] pages.  Its rows' probabilities are 0 for
+// later pages, and the products with those pages' Values leave its rows alone (the
+// product's lane mask), so nothing in them can reach it.
+#include "prefix.h"
+
+#include <algorithm>
+#include <atomic>
+
+#include "grid_dep.cuh"
+#include "host_common.h"
+#include "kitty_common.cuh"
+#include "partials.h"
+#include "tcgen05.cuh"
+
+namespace kitty {
+namespace {
+
+constexpr int kRows = 256;                // rows of a block: two lanes of 128
+constexpr int kQBytes = kRows * kD * 2;   // the queries' operand: [channel half][row][128 bytes]
+constexpr int kQHalf = kRows * 128;
+constexpr int kStages = 2;                // of Keys and of Values
+constexpr int kFlags = 8;                 // tiles whose page flags are kept
+constexpr uint32_t kPrefixWaitPolls = 1u << 22;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;
+constexpr float kFloor = -1.0e30f;        // a row without a score yet
+constexpr float kSlack = 8.f;             // log2 units the maximum may lag behind
+
+// Packed pages: Key planes of W bits, Values of V bits.
+template <int W_, int V_>
+struct PackedFmt {
+  static constexpr bool kPacked = true, kBf16 = false, kPair = false;
+  static constexpr int W = W_, V = V_, kPages = 3, kTok = 96;
+  static constexpr int kS = 112;          // columns of S: 96 scores, 3 of q.M (16 is the granule)
+  static constexpr int kO = 144;          // columns of O: 128 channels, 4 group minima
+  static constexpr int kKHalf = kS * 128, kKBytes = 2 * kKHalf;
+  static constexpr int kSlab = kO * 64;   // a page's Values: [channel][64 bytes]
+  static constexpr int kVBytes = kPages * kSlab;
+  static constexpr int kLoadWarps = 2 * kPages;
+  static constexpr int kRaw = W == 2 ? 4 : 2;                // staged page parts a warp
+  static constexpr int kRawK = 512 * W + 128 * 4 * W + 512 + 128;  // at n_hi = 128
+  static constexpr int kRawV = 512 * V + 512;
+  static constexpr int kRawBytes = kPages * kRaw * (kRawK + kRawV);
+};
+
+// 16-bit pages.
+template <bool BF>
+struct PlainFmt {
+  static constexpr bool kPacked = false, kBf16 = BF, kPair = BF;
+  static constexpr int kPages = 4, kTok = 128, kS = 128, kO = 128;
+  static constexpr int kKHalf = kTok * 128, kKBytes = 2 * kKHalf, kVBytes = kKBytes;
+  static constexpr int kSlab = 0, kLoadWarps = 2, kRawBytes = 0;
+};
+
+template <class F>
+__host__ __device__ constexpr int threads_of() { return 32 * (kLoadWarp + F::kLoadWarps); }
+template <class F>
+__host__ __device__ constexpr int smem_of() { return 1024 + kQBytes + kStages * (F::kKBytes + F::kVBytes) + F::kRawBytes; }
+
+struct Bars {
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+  uint64_t sfull[2], pready[2], ofull[2], drain;
+  uint64_t raw[6][4];
+};
+
+struct Shared {
+  Bars bars;
+  uint32_t tmem;
+  int abort;
+  int maxpages, minpages[2];
+  int pages[kRows];                // pages that each row sees (padding rows: all)
+  uint8_t valid[kFlags][4];        // page ids in range, by tile
+};
+
+// Whole warp: waits for a phase, at most `polls` polls; false when it, or another warp of
+// the block, has given up.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  bool done = false;
+  for (uint32_t i = 0;; ++i) {
+    done = done || mbar_try(a, parity);
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    const bool stop = i >= polls || *abort != 0;
+    if (__any_sync(0xFFFFFFFFu, stop)) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ float ex2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) { return h2_bits(__hadd2(bits_h2(a), bits_h2(b))); }
+__device__ __forceinline__ uint32_t h2max(uint32_t a, uint32_t b) { return h2_bits(__hmax2(bits_h2(a), bits_h2(b))); }
+
+// Both halves' codes of class K of a plane word as fp16 integers.  2-bit planes: class
+// K = token or channel block 0..3, at bits 2K + 2; 4-bit planes: K = 0, 1, at bits 4K + 2.  A
+// code under the exponent of 1024 reads 1024 + code * 2^shift; one fused multiply-add
+// takes both off, exactly.
+template <int BITS, int K>
+__device__ __forceinline__ uint32_t codes(uint32_t x) {
+  constexpr int shift = BITS * K + 2;
+  constexpr uint32_t mask = (((1u << BITS) - 1u) << shift) * 0x00010001u;
+  const uint32_t y = (x & mask) | 0x64006400u;
+  const __half2 inv = __float2half2_rn(1.0f / (1 << shift));
+  const __half2 off = __float2half2_rn(-1024.0f / (1 << shift));
+  return h2_bits(__hfma2(bits_h2(y), inv, off));
+}
+
+// A page's Key part (staged at raw, as in the page up to the channel list) to rows
+// 32 page .. of the stage, and its minima to row kTok + page.  Lane (r, qq) holds tokens r,
+// r + 8, r + 16, r + 24 of the channels 16j + 8h + 2qq + {0, 1}: pairs of channels, and the
+// eight rows of a warp's store lie in different swizzled 16-byte columns.
+template <class F>
+__device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page, int n_hi, int32_t* d_status) {
+  constexpr int W = F::W;
+  const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
+  const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
+  const uint32_t row = stage + (32 * page + r) * 128 + 4 * qq;
+  uint32_t top = 0;  // largest step pair
+  uint32_t plane[4 * W];  // this lane's words: one (W = 2) or two a j
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const uint4 v = lds128(raw + 16 * W * lane + 16 * i);
+    plane[4 * i] = v.x;
+    plane[4 * i + 1] = v.y;
+    plane[4 * i + 2] = v.z;
+    plane[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t w[2] = {plane[W / 2 * j], plane[W / 2 * j + W / 2 - 1]};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t S = lds32(ks + 32 * j + 16 * h + 4 * qq);
+      top = h2max(top, S);
+      const uint32_t at = row + (j >> 2) * F::kKHalf + (((2 * (j & 3) + h) ^ r) << 4);
+      if (W == 2) {
+        const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
+        sts32(at, h2mul(codes<2, 0>(x), S));
+        sts32(at + 1024, h2mul(codes<2, 1>(x), S));
+        sts32(at + 2048, h2mul(codes<2, 2>(x), S));
+        sts32(at + 3072, h2mul(codes<2, 3>(x), S));
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t x = h ? __funnelshift_r(w[mt], w[mt], 8) : w[mt];
+          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), S));
+          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), S));
+        }
+      }
+    }
+  }
+  {  // minima of channels 4 lane .. 4 lane + 3
+    const int j = lane >> 2, h = (lane >> 1) & 1, q0 = 2 * (lane & 1), m = F::kTok + page;
+    const uint32_t a = lds32(km + 2 * (((q0 * 8 + j) * 2 + h) * 2)), b = lds32(km + 2 * ((((q0 + 1) * 8 + j) * 2 + h) * 2));
+    const uint32_t at = stage + (lane >> 4) * F::kKHalf + m * 128 + ((((lane & 15) >> 1) ^ (m & 7)) << 4) + 8 * (lane & 1);
+    sts32(at, a);
+    sts32(at + 4, b);
+  }
+  // a step times a code (boosted: times 2^W at most) must stay in fp16
+  const float2 t = __half22float2(bits_h2(top));
+  if (!(fmaxf(t.x, t.y) * (float)(1 << W) <= 65504.f)) set_status(d_status, KITTY_ST_RANGE);
+  if (n_hi == 0) return;
+  // boosted channels: add step / 2^W * low code to what the base plane gave
+  __syncwarp();
+  const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
+  const int nx = n_hi / 16;
+  for (int js = 0; js < nx; ++js) {
+    uint32_t w[2];
+    if (W == 2) {
+      w[0] = lds32(raw + 512 * W + 4 * (lane * nx + js));
+    } else {
+      w[0] = lds32(raw + 512 * W + 4 * (lane * 2 * nx + 2 * js));
+      w[1] = lds32(raw + 512 * W + 4 * (lane * 2 * nx + 2 * js + 1));
+    }
+    const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t c0 = (ids >> (16 * h)) & 127u, c1 = (ids >> (16 * h + 8)) & 127u;
+      const uint32_t S = h2mul(lds16(ks + 2 * c0) | (lds16(ks + 2 * c1) << 16), part);
+      const uint32_t base = stage + (32 * page + r) * 128;
+      const uint32_t a0 = base + (c0 >> 6) * F::kKHalf + ((((c0 >> 3) & 7) ^ r) << 4) + 2 * (c0 & 7);
+      const uint32_t a1 = base + (c1 >> 6) * F::kKHalf + ((((c1 >> 3) & 7) ^ r) << 4) + 2 * (c1 & 7);
+      auto add = [&](int tau, uint32_t code) {
+        const uint32_t v = h2add(h2mul(code, S), lds16(a0 + 1024 * tau) | (lds16(a1 + 1024 * tau) << 16));
+        sts16(a0 + 1024 * tau, v);
+        sts16(a1 + 1024 * tau, v >> 16);
+      };
+      if (W == 2) {
+        const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
+        add(0, codes<2, 0>(x));
+        add(1, codes<2, 1>(x));
+        add(2, codes<2, 2>(x));
+        add(3, codes<2, 3>(x));
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint32_t x = h ? __funnelshift_r(w[mt], w[mt], 8) : w[mt];
+          add(2 * mt, codes<4, 0>(x));
+          add(2 * mt + 1, codes<4, 1>(x));
+        }
+      }
+    }
+  }
+}
+
+// A page's Value part (staged at raw: plane, steps, minima) to its slab, channels as rows of
+// 32 tokens, the four groups' minima as rows 128 .. 131.
+template <class F>
+__device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t* d_status) {
+  constexpr int V = F::V;
+  const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
+  const uint32_t vs = raw + 512 * V, vm = vs + 256;
+  const uint32_t sw = (r >> 1) & 3;
+  uint32_t top = 0;
+  uint32_t plane[4 * V];  // this lane's words: one (V = 2) or two a (G, kt)
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint4 v = lds128(raw + 16 * V * lane + 16 * i);
+    plane[4 * i] = v.x;
+    plane[4 * i + 1] = v.y;
+    plane[4 * i + 2] = v.z;
+    plane[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int G = 0; G < 4; ++G) {
+    const uint4 s4 = lds128(vs + 64 * G + 16 * qq);
+    const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
+    const uint32_t row = slab + (32 * G + r) * 64 + 4 * qq;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      const uint32_t w[2] = {plane[V / 2 * (2 * G + kt)], plane[V / 2 * (2 * G + kt) + V / 2 - 1]};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t s = S[2 * kt + h], at = row + (((2 * kt + h) ^ sw) << 4);
+        top = h2max(top, s);
+        if (V == 2) {
+          const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
+          sts32(at, h2mul(codes<2, 0>(x), s));
+          sts32(at + 512, h2mul(codes<2, 1>(x), s));
+          sts32(at + 1024, h2mul(codes<2, 2>(x), s));
+          sts32(at + 1536, h2mul(codes<2, 3>(x), s));
+        } else {
+#pragma unroll
+          for (int mc = 0; mc < 2; ++mc) {
+            const uint32_t x = h ? __funnelshift_r(w[mc], w[mc], 8) : w[mc];
+            sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
+            sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
+          }
+        }
+      }
+    }
+  }
+  if (r < 4) {  // group r's minima of the tokens of column qq
+    const uint4 m4 = lds128(vm + 64 * r + 16 * qq);
+    const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sts32(slab + (kD + r) * 64 + ((i ^ sw) << 4) + 4 * qq, m[i]);
+  }
+  const float2 t = __half22float2(bits_h2(top));
+  if (!(fmaxf(t.x, t.y) * (float)(1 << V) <= 65504.f)) set_status(d_status, KITTY_ST_RANGE);
+}
+
+// Eight queries' channels (16 bytes) in the operand's type; a negative scale is taken as
+// its magnitude and the negated query.
+template <class F>
+__device__ __forceinline__ uint4 query16(uint4 v, int in_dtype, bool negate) {
+  uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (F::kPacked && in_dtype == KITTY_BF16)
+      x[i] = h2_bits(__floats2half2_rn(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u)));
+    if (negate) x[i] ^= 0x80008000u;
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+template <class F>
+__global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const PrefixArgs p,
+                                                                    const __grid_constant__ CUtensorMap map) {
+  extern __shared__ uint8_t dyn[];
+  __shared__ Shared sh;
+  grid_trigger();
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int R = p.B * p.g, units = (R + kRows - 1) / kRows;
+  const int kvh = blockIdx.x / units, unit = blockIdx.x - kvh * units, split = blockIdx.y;
+  const bool both = R > 128;  // two lanes of rows; else the lanes share the rows and alternate
+  volatile int* abort = &sh.abort;
+
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t kst = base + kQBytes, vst = kst + kStages * F::kKBytes, raws = vst + kStages * F::kVBytes;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.bars.kfull[i], F::kPacked ? F::kPages : 1);
+      mbar_init(&sh.bars.vfull[i], F::kPacked ? F::kPages : 1);
+      mbar_init(&sh.bars.kempty[i], 1);
+      mbar_init(&sh.bars.vempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.bars.sfull[i], 1);
+      mbar_init(&sh.bars.pready[i], 128);
+      mbar_init(&sh.bars.ofull[i], 1);
+    }
+    mbar_init(&sh.bars.drain, 1);
+    for (int i = 0; i < 6; ++i)
+      for (int k = 0; k < 4; ++k) mbar_init(&sh.bars.raw[i][k], 1);
+    fence_mbar_init();
+    sh.abort = 0;
+    sh.maxpages = 0;
+    sh.minpages[0] = sh.minpages[1] = p.n_prefix;
+  }
+  __syncthreads();
+  // ---- the rows: what each sees of the prefix, its partials' place, its query
+  const int row = tid;                                         // < kRows: a softmax thread
+  const int in_unit = unit * kRows + (both ? row : (row & 127));  // row of the kv head
+  int my_pages = p.n_prefix;
+  size_t part_row = 0;
+  const bool real = row < kRows && in_unit < R;
+  if (real) {
+    const int b = in_unit / p.g;
+    part_row = (size_t)b * p.Hq + (size_t)kvh * p.g + (in_unit - b * p.g);
+    if (p.prefix_pages != nullptr) {
+      my_pages = p.prefix_pages[b];
+      if (my_pages < 0 || my_pages > p.n_prefix) {
+        set_status(p.d_status, KITTY_ST_BAD_LEN);
+        my_pages = 0;
+      }
+    }
+    atomicMax(&sh.maxpages, my_pages);
+    atomicMin(&sh.minpages[row >> 7], my_pages);
+  }
+  if (row < kRows) sh.pages[row] = my_pages;
+  __syncthreads();
+  const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
+  const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
+  const int page_end = min(sh.maxpages, p.n_prefix);
+  const int n = max(0, min(t1, (page_end + F::kPages - 1) / F::kPages) - t0);  // tiles of this block
+  const int steps = both ? 2 * n : n;  // step s: lane s & 1, tile s / 2 or s
+  const int slot0 = both ? split : 2 * split + (row >> 7);
+  float* part = p.ws + (part_row * p.slots + slot0) * kPartialFloats;
+  if (n == 0) {
+    if (real) part[0] = -INFINITY;
+    if (tid == 0) grid_wait();
+    return;
+  }
+  if (wid == kMmaWarp) tmem_alloc(smem_u32(&sh.tmem), 512);
+  // the queries: 16 threads a row
+  for (int i = tid; i < kRows * 16; i += threads_of<F>()) {
+    const int rr = i >> 4, c = i & 15;
+    const int x = unit * kRows + (both ? rr : (rr & 127));
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (x < R) {
+      const int b = x / p.g;
+      v = *reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.Hq + (size_t)kvh * p.g + (x - b * p.g)) * kD + 8 * c);
+    }
+    sts128(base + (c >> 3) * kQHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), query16<F>(v, p.in_dtype, p.sm_log2 < 0.f));
+  }
+  fence_async_shared();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  int loads = 0;  // 16-bit pages: tiles that this warp has requested
+  auto s_col = [&](int a) { return tmem + (uint32_t)(a * F::kS); };
+  auto o_col = [&](int a) { return tmem + (uint32_t)(2 * F::kS + a * F::kO); };
+
+  if (wid < kSoftmaxWarps) {
+    // =========================================================== softmax
+    const int a = wid >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
+    const uint32_t S = s_col(a) + lanes, O = o_col(a) + lanes;
+    const float sc = fabsf(p.sm_log2);
+    float m = kFloor, l = 0.f;
+    bool ok = true;
+    int i = 0;
+    for (int s = a; s < steps; s += 2, ++i) {
+      if (!wait_phase(&sh.bars.sfull[a], i & 1, p.wait_polls, abort)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int tile = both ? s >> 1 : s, page0 = (t0 + tile) * F::kPages;
+      uint32_t bias[4] = {0, 0, 0, 0};
+      if (F::kPacked) tmem_ld4(S + F::kTok, bias);
+      bool on[F::kPages];
+      float mx = kFloor;
+#pragma unroll
+      for (int g = 0; g < F::kPages; ++g) {
+        on[g] = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
+        uint32_t x[32];
+        tmem_ld32(S + 32 * g, x);
+        tmem_wait_ld(x);
+        if (F::kPacked && g == 0) pin(bias);
+        float pm = __uint_as_float(x[0]);
+#pragma unroll
+        for (int k = 1; k < 32; ++k) pm = fmaxf(pm, __uint_as_float(x[k]));
+        if (on[g]) mx = fmaxf(mx, (pm + __uint_as_float(bias[g])) * sc);
+      }
+      if (i == 0) {
+        m = mx;
+      } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+        const float nm = fmaxf(m, mx), f = ex2a(m - nm);
+#pragma unroll
+        for (int c = 0; c < F::kO; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(O + c, x);
+          tmem_wait_ld(x);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+          tmem_st16(O + c, x);
+        }
+        l *= f;
+        m = nm;
+      }
+#pragma unroll
+      for (int g = 0; g < F::kPages; ++g) {
+        uint32_t x[32];
+        tmem_ld32(S + 32 * g, x);
+        tmem_wait_ld(x);
+        const float off = fmaf(__uint_as_float(bias[g]), sc, -m);
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float e0 = on[g] ? ex2a(fmaf(__uint_as_float(x[2 * k]), sc, off)) : 0.f;
+          const float e1 = on[g] ? ex2a(fmaf(__uint_as_float(x[2 * k + 1]), sc, off)) : 0.f;
+          l += e0 + e1;
+          if (F::kBf16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+            hi[k] = *reinterpret_cast<const uint32_t*>(&h);
+            const float2 hf = __bfloat1622float2(h);
+            const __nv_bfloat162 r = __floats2bfloat162_rn(e0 - hf.x, e1 - hf.y);
+            lo[k] = *reinterpret_cast<const uint32_t*>(&r);
+          } else {
+            hi[k] = h2_bits(__floats2half2_rn(e0, e1));
+          }
+        }
+        // over the page's own scores, which this thread has taken
+        tmem_st16(S + 32 * g, hi);
+        if (F::kPair) tmem_st16(S + 32 * g + 16, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_s(smem_u32(&sh.bars.pready[a]));
+    }
+    // ---- this lane's partials
+    if (ok && i > 0) ok = wait_phase(&sh.bars.ofull[a], 0, p.wait_polls, abort);
+    if (ok && i > 0) {
+      tc_fence_after();
+      uint32_t vmin[4] = {0, 0, 0, 0};
+      if (F::kPacked) tmem_ld4(O + kD, vmin);
+#pragma unroll
+      for (int c = 0; c < kD; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(O + c, x);
+        tmem_wait_ld(x);
+        if (F::kPacked && c == 0) pin(vmin);
+        const float add = __uint_as_float(vmin[c / 32]);
+        if (real && l != 0.f) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + 4 + c + k) =
+                make_float4(__uint_as_float(x[k]) + add, __uint_as_float(x[k + 1]) + add,
+                            __uint_as_float(x[k + 2]) + add, __uint_as_float(x[k + 3]) + add);
+        }
+      }
+      tc_fence_before();
+    }
+    if (real) {
+      const bool some = ok && i > 0 && l != 0.f;
+      part[0] = some ? m : -INFINITY;
+      part[1] = l;
+    }
+    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
+  } else if (wid == kMmaWarp) {
+    // =========================================================== products
+    constexpr uint32_t qk = mma_desc(F::kBf16, false, F::kS), pv = mma_desc(F::kBf16, !F::kPacked, F::kO);
+    bool started[2] = {false, false};
+    auto last_use = [&](int s) { return !both || (s & 1); };
+    auto scores = [&](int s) -> bool {
+      const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
+      if (!wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) {
+          const uint32_t qa = base + (k >> 2) * kQHalf + a * (128 * 128) + 32 * (k & 3);
+          const uint32_t kb = kst + st * F::kKBytes + (k >> 2) * F::kKHalf + 32 * (k & 3);
+          mma_ss(s_col(a), smem_desc(qa, 16, 1024, kSwizzle128), smem_desc(kb, 16, 1024, kSwizzle128), qk, k > 0);
+        }
+        mma_commit(smem_u32(&sh.bars.sfull[a]));
+        if (last_use(s)) mma_commit(smem_u32(&sh.bars.kempty[st]));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = scores(0) && (steps < 2 || scores(1));
+    for (int s = 0; ok && s < steps; ++s) {
+      const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
+      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
+           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
+      if (!ok) break;
+      tc_fence_after();
+      for (int g = 0; g < F::kPages; ++g) {
+        const int page = (t0 + tile) * F::kPages + g;
+        if (page >= page_end || sh.valid[tile % kFlags][g] == 0) continue;
+        uint32_t off[4] = {0, 0, 0, 0};
+        if (page >= sh.minpages[a]) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) off[w] = __ballot_sync(0xFFFFFFFFu, sh.pages[128 * a + 32 * w + lane] <= page);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t pa = s_col(a) + 32 * g + 8 * k;
+            const uint64_t vb = F::kPacked
+                ? smem_desc(vst + st * F::kVBytes + g * F::kSlab + 32 * k, 16, 512, kSwizzle64)
+                : smem_desc(vst + st * F::kVBytes + (32 * g + 16 * k) * 128, F::kKHalf, 1024, kSwizzle128);
+            mma_ts(o_col(a), pa, vb, pv, started[a] || k > 0, off);
+            if (F::kPair) mma_ts(o_col(a), pa + 16, vb, pv, true, off);
+          }
+        }
+        started[a] = true;
+      }
+      if (lane == 0) {
+        if (last_use(s)) mma_commit(smem_u32(&sh.bars.vempty[st]));
+        if (s + 2 >= steps) mma_commit(smem_u32(&sh.bars.ofull[a]));
+      }
+      __syncwarp();
+      if (s + 2 < steps) ok = scores(s + 2);
+    }
+    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
+  } else if constexpr (F::kPacked) {
+    // =========================================================== packed pages
+    const int d = wid - kLoadWarp, g = d % F::kPages;
+    const bool values = d >= F::kPages;
+    const uint32_t part_bytes = values ? F::kRawV : 512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi;
+    const size_t part_off = values ? (size_t)(512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi) : 0;
+    const uint32_t raw0 = raws + (values ? F::kPages * F::kRaw * F::kRawK + g * F::kRaw * F::kRawV : g * F::kRaw * F::kRawK);
+    const uint32_t raw_stride = values ? F::kRawV : F::kRawK;
+    int ids = -1, ids_at = -1000;  // lane l: the id of this warp's page of tile ids_at + l
+    auto id_of = [&](int tile) {
+      if (tile - ids_at >= 32 || tile < ids_at) {
+        ids_at = tile;
+        const int page = (t0 + tile + lane) * F::kPages + g;
+        ids = page < page_end ? p.table[page] : -1;
+      }
+      return __shfl_sync(0xFFFFFFFFu, ids, tile - ids_at);
+    };
+    uint32_t staged = 0;  // bit: the slot holds (or awaits) a page
+    auto fetch = [&](int tile) {
+      const int id = id_of(tile), slot = tile % F::kRaw;
+      const bool in = id >= 0 && id < p.pool_pages;
+      if (lane == 0) {
+        if (in) {
+          const uint32_t bar = smem_u32(&sh.bars.raw[d][slot]);
+          mbar_arrive_expect_tx_s(bar, part_bytes);
+          bulk_g2s_s(raw0 + slot * raw_stride, p.pool + ((size_t)id * p.Hkv + kvh) * p.blob + part_off, part_bytes, bar);
+        } else if ((t0 + tile) * F::kPages + g < page_end) {
+          set_status(p.d_status, KITTY_ST_BAD_PAGE);
+        }
+      }
+      staged = in ? staged | (1u << slot) : staged & ~(1u << slot);
+    };
+    uint32_t phases = 0;  // bit: phase parity that the slot's barrier completes next
+    bool ok = true;
+    for (int tile = 0; tile < min(n, F::kRaw); ++tile) fetch(tile);
+    for (int tile = 0; tile < n; ++tile) {
+      const int slot = tile % F::kRaw, st = tile % kStages;
+      const bool in = (staged >> slot) & 1u;
+      if (in) {
+        ok = wait_phase(&sh.bars.raw[d][slot], (phases >> slot) & 1u, p.wait_polls, abort);
+        if (!ok) break;
+        phases ^= 1u << slot;
+        staged &= ~(1u << slot);
+      }
+      ok = wait_phase(values ? &sh.bars.vempty[st] : &sh.bars.kempty[st], ((tile / kStages) & 1) ^ 1, p.wait_polls, abort);
+      if (!ok) break;
+      if (in) {
+        const uint32_t raw = raw0 + slot * raw_stride;
+        if (values) put_values<F>(raw, vst + st * F::kVBytes + g * F::kSlab, p.d_status);
+        else put_keys<F>(raw, kst + st * F::kKBytes, g, p.n_hi, p.d_status);
+      }
+      if (!values && lane == 0) sh.valid[tile % kFlags][g] = in;
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
+      if (tile + F::kRaw < n) fetch(tile + F::kRaw);
+    }
+    if (!ok && lane == 0) {
+      set_status(p.d_status, KITTY_ST_TIMEOUT);
+      for (int k = 0; k < F::kRaw; ++k)  // this warp's copies in flight
+        if ((staged >> k) & 1u) mbar_wait_bounded(&sh.bars.raw[d][k], (phases >> k) & 1u, kPrefixWaitPolls);
+    }
+    __syncwarp();
+  } else {
+    // =========================================================== 16-bit pages
+    const bool values = wid == kLoadWarp + 1;
+    uint64_t *full = values ? sh.bars.vfull : sh.bars.kfull, *empty = values ? sh.bars.vempty : sh.bars.kempty;
+    const uint32_t st0 = values ? vst : kst;
+    bool ok = true;
+    int tile = 0;  // loads issued
+    for (; tile < n; ++tile) {
+      const int st = tile % kStages;
+      ok = wait_phase(&empty[st], ((tile / kStages) & 1) ^ 1, p.wait_polls, abort);
+      if (!ok) break;
+      const int page = (t0 + tile) * F::kPages + lane;
+      const int id = lane < F::kPages && page < page_end ? p.table[page] : -1;
+      const bool in = id >= 0 && id < p.pool_pages;
+      const int count = __popc(__ballot_sync(0xFFFFFFFFu, in));
+      const uint32_t bar = smem_u32(&full[st]);
+      if (lane < F::kPages) {
+        if (!values) sh.valid[tile % kFlags][lane] = in;
+        if (!in && page < page_end) set_status(p.d_status, KITTY_ST_BAD_PAGE);
+      }
+      __syncwarp();  // the flags, before the arrival that publishes them
+      if (lane == 0) mbar_arrive_expect_tx_s(bar, (uint32_t)(count * kPage * kD * 2));
+      __syncwarp();
+      if (in) {
+        const int y = (id * p.Hkv + kvh) * 2 * kPage + (values ? kPage : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          tma_load_2d(st0 + st * F::kKBytes + h * F::kKHalf + lane * kPage * 128, &map, 64 * h, y, bar);
+      }
+    }
+    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
+    __syncwarp();
+    loads = tile;
+  }
+  __syncthreads();
+  // after a wait that ran out: nothing may be in flight when the block's memory is given back
+  if (*abort != 0 && lane == 0) {
+    if (wid == kMmaWarp) {
+      mma_commit(smem_u32(&sh.bars.drain));
+      mbar_wait_bounded(&sh.bars.drain, 0, kPrefixWaitPolls);
+    } else if (!F::kPacked && wid >= kLoadWarp) {
+      for (int k = max(0, loads - kStages); k < loads; ++k)
+        mbar_wait_bounded(wid == kLoadWarp ? &sh.bars.kfull[k % kStages] : &sh.bars.vfull[k % kStages],
+                          (k / kStages) & 1, kPrefixWaitPolls);
+    }
+  }
+  __syncwarp();
+  if (wid == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0) grid_wait();  // whoever waits for this grid has waited for the one before, too
+}
+
+// Splits of the prefix: one block an SM; a block costs its tiles and a start and end worth
+// about kBlockTiles tiles; each split adds a partial a row, written and read.
+PrefixPlan plan_for(int Hkv, int rows, int tiles, int sms) {
+  PrefixPlan pl = {Hkv * ((rows + kRows - 1) / kRows), 1, 1};
+  const double tile = rows > 128 ? 1.0 : 0.5, kBlockTiles = 4.0;
+  const double per_split = (double)Hkv * rows * 1056.0 / 6.0e6;  // us, against 1.3 us a tile
+  double best = 1e30;
+  for (int s = 1; s <= std::min(tiles, 64); ++s) {
+    const int waves = (pl.units * s + sms - 1) / sms, per = (tiles + s - 1) / s;
+    const double cost = waves * (per * tile + kBlockTiles) * 1.3 + s * per_split;
+    if (cost < best - 1e-9) {
+      best = cost;
+      pl.splits = s;
+    }
+  }
+  pl.slots = rows > 128 ? pl.splits : 2 * pl.splits;
+  return pl;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The 16-bit pool as rows of 128 channels; boxes of 32 rows by 64 channels, swizzled.
+bool pool_map(CUtensorMap* map, const void* pool, uint64_t rows) {
+  static std::atomic<EncodeTiled> encode{nullptr};
+  EncodeTiled f = encode.load();
+  if (f == nullptr) {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return false;
+    f = reinterpret_cast<EncodeTiled>(sym);
+    encode.store(f);
+  }
+  const cuuint64_t dims[2] = {kD, rows}, strides[1] = {kD * 2};
+  const cuuint32_t box[2] = {64, kPage}, ones[2] = {1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(pool), dims, strides, box, ones,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class F>
+int launch(const PrefixArgs& a, const PrefixPlan& pl, const CUtensorMap& map, cudaStream_t s) {
+  static_assert(smem_of<F>() <= 227 * 1024 - 1024, "fits beside the static part");
+  static_assert(2 * (F::kS + F::kO) <= 512, "fits tensor memory");
+  static std::atomic<uint64_t> opted_in{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KITTY_ERR_CUDA;
+  const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit == 0 || (opted_in.load() & bit) == 0) {
+    if (cudaFuncSetAttribute(prefix_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<F>()) != cudaSuccess)
+      return KITTY_ERR_CUDA;
+    opted_in.fetch_or(bit);
+  }
+  const cudaError_t e = launch_dependent(prefix_kernel<F>, dim3((unsigned)pl.units, (unsigned)pl.splits),
+                                         threads_of<F>(), (size_t)smem_of<F>(), s, a, map);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
+}
+
+}  // namespace
+
+PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix) {
+  if (n_prefix <= 0 || B <= 0) return {0, 0, 0};
+  const int pages = packed ? PackedFmt<2, 2>::kPages : PlainFmt<true>::kPages;
+  return plan_for(cfg->num_kv_heads, B * (cfg->num_q_heads / cfg->num_kv_heads), (n_prefix + pages - 1) / pages, sm_count());
+}
+
+int prefix_launch(const kitty_cfg* cfg, bool packed, const PrefixArgs& args, const PrefixPlan& pl, cudaStream_t s) {
+  CUtensorMap map = {};
+  if (packed) {
+    if (cfg->lo_bit == 2) return launch<PackedFmt<2, 2>>(args, pl, map, s);
+    return v_bits(cfg) == 2 ? launch<PackedFmt<4, 2>>(args, pl, map, s) : launch<PackedFmt<4, 4>>(args, pl, map, s);
+  }
+  const uint64_t rows = (uint64_t)args.pool_pages * args.Hkv * 2 * kPage;
+  if (rows == 0) return KITTY_ERR_INVALID_ARG;
+  if (rows > 0x7FFFFFFFull) return KITTY_ERR_UNSUPPORTED;  // a row's coordinate is an int32
+  if (!pool_map(&map, args.pool, rows)) return KITTY_ERR_CUDA;
+  return cfg->in_dtype == KITTY_BF16 ? launch<PlainFmt<true>>(args, pl, map, s) : launch<PlainFmt<false>>(args, pl, map, s);
+}
+
+}  // namespace kitty
