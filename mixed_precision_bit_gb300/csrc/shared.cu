@@ -27,38 +27,95 @@ struct MergeParams {
   const float *a, *b;  // partials of the prefix and of the own pages, row-major
   void* out;
   int32_t* d_status;
-  int na, nb, rows, out_dtype;
+  int na, nb, rows, out_dtype, wide;  // wide: out is 16-byte aligned
 };
 
-// One warp a row: the partials of both lists in order, four channels a lane.
+// WARPS warps a row (4 / WARPS rows a block).  Every warp reads the row's maxima, one slot a
+// lane, and weighs them; then warp w sums slots w, w + WARPS, ... of the unscaled outputs,
+// four channels a lane, kAhead loads in flight, and the warps' sums meet in shared memory.
+// A slot that attended nothing (m = -inf) has weight 0 and its outputs are not used.
+constexpr int kAhead = 8;
+
+template <int WARPS>
 __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
+  __shared__ float4 part[4][32];
   grid_wait();
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= p.rows) return;
-  const float* a = p.a + (size_t)row * p.na * kPartialFloats;
-  const float* b = p.b + (size_t)row * p.nb * kPartialFloats;
-  float ms = -INFINITY;
-  for (int s = 0; s < p.na; ++s) ms = fmaxf(ms, a[s * kPartialFloats]);
-  for (int s = 0; s < p.nb; ++s) ms = fmaxf(ms, b[s * kPartialFloats]);
-  float L = 0.f;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, w = wid % WARPS;
+  const int row = blockIdx.x * (4 / WARPS) + wid / WARPS;
+  const bool in = row < p.rows;
+  const int n = in ? p.na + p.nb : 0;
+  const float* a = p.a + (size_t)(in ? row : 0) * p.na * kPartialFloats;
+  const float* b = p.b + (size_t)(in ? row : 0) * p.nb * kPartialFloats;
+  auto slot = [&](int s) { return s < p.na ? a + (size_t)s * kPartialFloats : b + (size_t)(s - p.na) * kPartialFloats; };
+  float ms = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ms != -INFINITY) {
-    for (int s = 0; s < p.na + p.nb; ++s) {
-      const float* x = s < p.na ? a + s * kPartialFloats : b + (s - p.na) * kPartialFloats;
-      if (x[0] == -INFINITY) continue;
-      const float e = exp2_fast(x[0] - ms);
-      const float4 o = reinterpret_cast<const float4*>(x + 4)[lane];
-      L += x[1] * e;
-      O.x += o.x * e;
-      O.y += o.y * e;
-      O.z += o.z * e;
-      O.w += o.w * e;
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    // this round's maxima and sums, one slot a lane, and the first outputs, all in flight
+    const int mine = s0 + lane;
+    const float2 ml = mine < n ? *reinterpret_cast<const float2*>(slot(mine)) : make_float2(-INFINITY, 0.f);
+    float mr = fmaxf(ml.x, ms);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xFFFFFFFFu, mr, d));
+    if (mr == -INFINITY) continue;
+    const float f = ms == -INFINITY ? 0.f : exp2_fast(ms - mr);
+    const float e = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - mr);
+    float l = e == 0.f ? 0.f : ml.y * e;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    L = L * f + l;
+    O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+    ms = mr;
+    const int m = min(32, n - s0);
+    for (int k0 = w; k0 < m; k0 += WARPS * kAhead) {
+      float4 o[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int s = k0 + k * WARPS;
+        o[k] = s < m ? reinterpret_cast<const float4*>(slot(s0 + s) + 4)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int s = k0 + k * WARPS;
+        const float es = __shfl_sync(0xFFFFFFFFu, e, s & 31);
+        if (s < m && es != 0.f) {
+          O.x = fmaf(o[k].x, es, O.x);
+          O.y = fmaf(o[k].y, es, O.y);
+          O.z = fmaf(o[k].z, es, O.z);
+          O.w = fmaf(o[k].w, es, O.w);
+        }
+      }
     }
   }
+  if (WARPS > 1) {
+    part[wid][lane] = O;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) {
+      const float4 x = part[wid + k][lane];
+      O = make_float4(O.x + x.x, O.y + x.y, O.z + x.z, O.w + x.w);
+    }
+  }
+  if (!in) return;
   const bool ok = L != 0.f;
   if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_EMPTY);
   const float r[4] = {ok ? O.x / L : 0.f, ok ? O.y / L : 0.f, ok ? O.z / L : 0.f, ok ? O.w / L : 0.f};
   const size_t i = (size_t)row * kD + 4 * lane;
+  if (p.wide) {  // the outputs are 16-byte aligned
+    if (p.out_dtype == KITTY_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + i) = make_float4(r[0], r[1], r[2], r[3]);
+    } else {
+      uint2 h;
+      if (p.out_dtype == KITTY_BF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(r[0], r[1]), y = __floats2bfloat162_rn(r[2], r[3]);
+        h = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      } else {
+        h = make_uint2(h2_bits(__floats2half2_rn(r[0], r[1])), h2_bits(__floats2half2_rn(r[2], r[3])));
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + i) = h;
+    }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (p.out_dtype == KITTY_F32) static_cast<float*>(p.out)[i + k] = r[k];
@@ -106,7 +163,7 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
   const PrefixPlan plan = prefix_plan(cfg, packed, B, n_prefix);
   const size_t mine = prefix_bytes(cfg, packed, B, n_prefix);
   float* own_ws = static_cast<float*>(ws) + mine / sizeof(float);
-  MergeParams m = {static_cast<float*>(ws), own_ws, out, d_status, plan.slots, 0, B * cfg->num_q_heads, out_dtype};
+  MergeParams m = {static_cast<float*>(ws), own_ws, out, d_status, plan.slots, 0, B * cfg->num_q_heads, out_dtype, aligned16(out)};
   rc = own(own_ws, ws_bytes - mine, &m.nb);
   if (rc != KITTY_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -134,7 +191,10 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
     rc = prefix_launch(cfg, packed, p, plan, s);
     if (rc != KITTY_OK) return rc;
   }
-  const cudaError_t e = launch_dependent(merge_kernel, dim3((unsigned)((m.rows + 3) / 4)), 128, 0, s, m);
+  // few partials a row: a warp a row; more (measured at 10 to 32): four warps
+  const cudaError_t e = m.na + m.nb <= kAhead
+      ? launch_dependent(merge_kernel<1>, dim3((unsigned)((m.rows + 3) / 4)), 128, 0, s, m)
+      : launch_dependent(merge_kernel<4>, dim3((unsigned)m.rows), 128, 0, s, m);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
 }
 
