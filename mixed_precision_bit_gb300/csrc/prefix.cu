@@ -89,7 +89,7 @@ __host__ __device__ constexpr int smem_of() { return 1024 + kQBytes + kStages * 
 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t sfull[2], pready[2], ofull[2], drain;
+  uint64_t sfull[2], pready[2], ofull[2], qready, drain;
   uint64_t raw[6][4];
 };
 
@@ -97,9 +97,10 @@ struct Shared {
   Bars bars;
   uint32_t tmem;
   int abort;
-  int maxpages, minpages[2];
-  int pages[kRows];                // pages that each row sees (padding rows: all)
+  int maxpages;
+  int row[kRows];                  // partials' row (sequence, query head); -1: padding
   uint8_t valid[kFlags][4];        // page ids in range, by tile
+  alignas(16) uint32_t off[2][4][4];  // by lane and page: rows that do not see it, 32 a word
 };
 
 // Whole warp: waits for a phase, at most `polls` polls; false when it, or another warp of
@@ -112,6 +113,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
     if (__all_sync(0xFFFFFFFFu, done)) return true;
     const bool stop = i >= polls || *abort != 0;
     if (__any_sync(0xFFFFFFFFu, stop)) break;
+  }
+  *abort = 1;
+  return false;
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try(a, parity)) return true;
+    if (i >= polls || *abort != 0) break;
   }
   *abort = 1;
   return false;
@@ -149,7 +161,6 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 }
 
 __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
-__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) { return h2_bits(__hadd2(bits_h2(a), bits_h2(b))); }
 __device__ __forceinline__ uint32_t h2max(uint32_t a, uint32_t b) { return h2_bits(__hmax2(bits_h2(a), bits_h2(b))); }
 
 // Both halves' codes of class K of a plane word as fp16 integers.  2-bit planes: class
@@ -176,8 +187,8 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
   const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
   const uint32_t row = stage + (32 * page + r) * 128 + 4 * qq;
-  uint32_t top = 0;  // largest step pair
-  uint32_t plane[4 * W];  // this lane's words: one (W = 2) or two a j
+  // this lane's words of the base plane, one (W = 2) or two a j, and its steps
+  uint32_t plane[4 * W], S[16], top = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     const uint4 v = lds128(raw + 16 * W * lane + 16 * i);
@@ -187,77 +198,89 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
     plane[4 * i + 3] = v.w;
   }
 #pragma unroll
+  for (int i = 0; i < 16; ++i) S[i] = lds32(ks + 16 * i + 4 * qq);
+  // minima of channels 4 lane .. 4 lane + 3
+  const int mj = lane >> 2, mh = (lane >> 1) & 1, mq = 2 * (lane & 1), mrow = F::kTok + page;
+  const uint32_t m0 = lds32(km + 4 * ((mq * 8 + mj) * 2 + mh)), m1 = lds32(km + 4 * (((mq + 1) * 8 + mj) * 2 + mh));
+#pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t w[2] = {plane[W / 2 * j], plane[W / 2 * j + W / 2 - 1]};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t S = lds32(ks + 32 * j + 16 * h + 4 * qq);
-      top = h2max(top, S);
+      const uint32_t s = S[2 * j + h];
+      top = h2max(top, s);
       const uint32_t at = row + (j >> 2) * F::kKHalf + (((2 * (j & 3) + h) ^ r) << 4);
       if (W == 2) {
         const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
-        sts32(at, h2mul(codes<2, 0>(x), S));
-        sts32(at + 1024, h2mul(codes<2, 1>(x), S));
-        sts32(at + 2048, h2mul(codes<2, 2>(x), S));
-        sts32(at + 3072, h2mul(codes<2, 3>(x), S));
+        sts32(at, h2mul(codes<2, 0>(x), s));
+        sts32(at + 1024, h2mul(codes<2, 1>(x), s));
+        sts32(at + 2048, h2mul(codes<2, 2>(x), s));
+        sts32(at + 3072, h2mul(codes<2, 3>(x), s));
       } else {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           const uint32_t x = h ? __funnelshift_r(w[mt], w[mt], 8) : w[mt];
-          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), S));
-          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), S));
+          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), s));
+          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), s));
         }
       }
     }
   }
-  {  // minima of channels 4 lane .. 4 lane + 3
-    const int j = lane >> 2, h = (lane >> 1) & 1, q0 = 2 * (lane & 1), m = F::kTok + page;
-    const uint32_t a = lds32(km + 2 * (((q0 * 8 + j) * 2 + h) * 2)), b = lds32(km + 2 * ((((q0 + 1) * 8 + j) * 2 + h) * 2));
-    const uint32_t at = stage + (lane >> 4) * F::kKHalf + m * 128 + ((((lane & 15) >> 1) ^ (m & 7)) << 4) + 8 * (lane & 1);
-    sts32(at, a);
-    sts32(at + 4, b);
+  {
+    const uint32_t at = stage + (lane >> 4) * F::kKHalf + mrow * 128 + ((((lane & 15) >> 1) ^ (mrow & 7)) << 4) + 8 * (lane & 1);
+    sts32(at, m0);
+    sts32(at + 4, m1);
   }
   // a step times a code (boosted: times 2^W at most) must stay in fp16
   const float2 t = __half22float2(bits_h2(top));
   if (!(fmaxf(t.x, t.y) * (float)(1 << W) <= 65504.f)) set_status(d_status, KITTY_ST_RANGE);
   if (n_hi == 0) return;
-  // boosted channels: add step / 2^W * low code to what the base plane gave
+  // Boosted channels again, from both planes: step * high + step / 2^W * low.  This lane's
+  // columns of the extra plane are pairs too, of any two channels (c0, c1): their words of the
+  // base plane lie in the lanes of the same tokens.
   __syncwarp();
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
+  const uint32_t base = stage + (32 * page + r) * 128, lo_plane = raw + 512 * W + 2 * W * nx * lane;
   for (int js = 0; js < nx; ++js) {
-    uint32_t w[2];
-    if (W == 2) {
-      w[0] = lds32(raw + 512 * W + 4 * (lane * nx + js));
-    } else {
-      w[0] = lds32(raw + 512 * W + 4 * (lane * 2 * nx + 2 * js));
-      w[1] = lds32(raw + 512 * W + 4 * (lane * 2 * nx + 2 * js + 1));
-    }
     const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
+    uint32_t lo[2];
+    lo[0] = lds32(lo_plane + 2 * W * js);
+    lo[1] = W == 4 ? lds32(lo_plane + 2 * W * js + 4) : 0;
+    uint32_t at[4], st[4], hi[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = (ids >> (8 * i)) & 127u;
+      st[i] = lds16(ks + 2 * c);
+      const uint32_t from = raw + 16 * W * (4 * r + ((c >> 1) & 3)) + 2 * W * (c >> 4);
+      const uint32_t turn = 16 * (c & 1) + 8 * ((c >> 3) & 1);
+#pragma unroll
+      for (int mt = 0; mt < W / 2; ++mt) {
+        const uint32_t x = lds32(from + 4 * mt);
+        hi[i][mt] = __funnelshift_r(x, x, turn);  // the channel's codes in the low half
+      }
+      at[i] = base + (c >> 6) * F::kKHalf + ((((c >> 3) & 7) ^ r) << 4) + 2 * (c & 7);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t c0 = (ids >> (16 * h)) & 127u, c1 = (ids >> (16 * h + 8)) & 127u;
-      const uint32_t S = h2mul(lds16(ks + 2 * c0) | (lds16(ks + 2 * c1) << 16), part);
-      const uint32_t base = stage + (32 * page + r) * 128;
-      const uint32_t a0 = base + (c0 >> 6) * F::kKHalf + ((((c0 >> 3) & 7) ^ r) << 4) + 2 * (c0 & 7);
-      const uint32_t a1 = base + (c1 >> 6) * F::kKHalf + ((((c1 >> 3) & 7) ^ r) << 4) + 2 * (c1 & 7);
-      auto add = [&](int tau, uint32_t code) {
-        const uint32_t v = h2add(h2mul(code, S), lds16(a0 + 1024 * tau) | (lds16(a1 + 1024 * tau) << 16));
-        sts16(a0 + 1024 * tau, v);
-        sts16(a1 + 1024 * tau, v >> 16);
+      const uint32_t s = st[2 * h] | (st[2 * h + 1] << 16), sl = h2mul(s, part);
+      auto put = [&](int tau, uint32_t ch, uint32_t cl) {
+        const uint32_t v = h2_bits(__hfma2(bits_h2(ch), bits_h2(s), bits_h2(h2mul(cl, sl))));
+        sts16(at[2 * h] + 1024 * tau, v);
+        sts16(at[2 * h + 1] + 1024 * tau, v >> 16);
       };
-      if (W == 2) {
-        const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
-        add(0, codes<2, 0>(x));
-        add(1, codes<2, 1>(x));
-        add(2, codes<2, 2>(x));
-        add(3, codes<2, 3>(x));
-      } else {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t x = h ? __funnelshift_r(w[mt], w[mt], 8) : w[mt];
-          add(2 * mt, codes<4, 0>(x));
-          add(2 * mt + 1, codes<4, 1>(x));
+      for (int mt = 0; mt < W / 2; ++mt) {
+        const uint32_t xh = __byte_perm(hi[2 * h][mt], hi[2 * h + 1][mt], 0x5410);
+        const uint32_t xl = h ? __funnelshift_r(lo[mt], lo[mt], 8) : lo[mt];
+        if (W == 2) {
+          put(0, codes<2, 0>(xh), codes<2, 0>(xl));
+          put(1, codes<2, 1>(xh), codes<2, 1>(xl));
+          put(2, codes<2, 2>(xh), codes<2, 2>(xl));
+          put(3, codes<2, 3>(xh), codes<2, 3>(xl));
+        } else {
+          put(2 * mt, codes<4, 0>(xh), codes<4, 0>(xl));
+          put(2 * mt + 1, codes<4, 1>(xh), codes<4, 1>(xl));
         }
       }
     }
@@ -274,6 +297,10 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
   const uint32_t sw = (r >> 1) & 3;
   uint32_t top = 0;
   uint32_t plane[4 * V];  // this lane's words: one (V = 2) or two a (G, kt)
+  uint4 steps[4];
+#pragma unroll
+  for (int G = 0; G < 4; ++G) steps[G] = lds128(vs + 64 * G + 16 * qq);
+  const uint4 m4 = lds128(vm + 64 * (r & 3) + 16 * qq);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const uint4 v = lds128(raw + 16 * V * lane + 16 * i);
@@ -284,8 +311,7 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
   }
 #pragma unroll
   for (int G = 0; G < 4; ++G) {
-    const uint4 s4 = lds128(vs + 64 * G + 16 * qq);
-    const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
+    const uint32_t S[4] = {steps[G].x, steps[G].y, steps[G].z, steps[G].w};
     const uint32_t row = slab + (32 * G + r) * 64 + 4 * qq;
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
@@ -312,7 +338,6 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
     }
   }
   if (r < 4) {  // group r's minima of the tokens of column qq
-    const uint4 m4 = lds128(vm + 64 * r + 16 * qq);
     const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) sts32(slab + (kD + r) * 64 + ((i ^ sw) << 4) + 4 * qq, m[i]);
@@ -362,64 +387,46 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       mbar_init(&sh.bars.pready[i], 128);
       mbar_init(&sh.bars.ofull[i], 1);
     }
+    mbar_init(&sh.bars.qready, kRows);
     mbar_init(&sh.bars.drain, 1);
     for (int i = 0; i < 6; ++i)
       for (int k = 0; k < 4; ++k) mbar_init(&sh.bars.raw[i][k], 1);
     fence_mbar_init();
     sh.abort = 0;
     sh.maxpages = 0;
-    sh.minpages[0] = sh.minpages[1] = p.n_prefix;
   }
-  __syncthreads();
-  // ---- the rows: what each sees of the prefix, its partials' place, its query
-  const int row = tid;                                         // < kRows: a softmax thread
-  const int in_unit = unit * kRows + (both ? row : (row & 127));  // row of the kv head
-  int my_pages = p.n_prefix;
+  // ---- the rows: what each sees of the prefix, its partials' place
+  const int in_unit = unit * kRows + (both ? tid : (tid & 127));  // row of the kv head
+  const bool real = tid < kRows && in_unit < R;
+  int my_pages = p.n_prefix, b = 0;
   size_t part_row = 0;
-  const bool real = row < kRows && in_unit < R;
   if (real) {
-    const int b = in_unit / p.g;
+    b = in_unit / p.g;
     part_row = (size_t)b * p.Hq + (size_t)kvh * p.g + (in_unit - b * p.g);
-    if (p.prefix_pages != nullptr) {
-      my_pages = p.prefix_pages[b];
+    if (p.prefix_pages != nullptr) my_pages = p.prefix_pages[b];
+  }
+  if (tid < kRows) sh.row[tid] = real ? (int)part_row : -1;
+  if (wid == kMmaWarp) tmem_alloc(smem_u32(&sh.tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int page_end = p.n_prefix;  // pages that some row of the block sees
+  if (p.prefix_pages != nullptr) {
+    if (real) {
       if (my_pages < 0 || my_pages > p.n_prefix) {
         set_status(p.d_status, KITTY_ST_BAD_LEN);
         my_pages = 0;
       }
+      atomicMax(&sh.maxpages, my_pages);
     }
-    atomicMax(&sh.maxpages, my_pages);
-    atomicMin(&sh.minpages[row >> 7], my_pages);
+    __syncthreads();
+    page_end = sh.maxpages;
   }
-  if (row < kRows) sh.pages[row] = my_pages;
-  __syncthreads();
   const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
   const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
-  const int page_end = min(sh.maxpages, p.n_prefix);
   const int n = max(0, min(t1, (page_end + F::kPages - 1) / F::kPages) - t0);  // tiles of this block
   const int steps = both ? 2 * n : n;  // step s: lane s & 1, tile s / 2 or s
-  const int slot0 = both ? split : 2 * split + (row >> 7);
-  float* part = p.ws + (part_row * p.slots + slot0) * kPartialFloats;
-  if (n == 0) {
-    if (real) part[0] = -INFINITY;
-    if (tid == 0) grid_wait();
-    return;
-  }
-  if (wid == kMmaWarp) tmem_alloc(smem_u32(&sh.tmem), 512);
-  // the queries: 16 threads a row
-  for (int i = tid; i < kRows * 16; i += threads_of<F>()) {
-    const int rr = i >> 4, c = i & 15;
-    const int x = unit * kRows + (both ? rr : (rr & 127));
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (x < R) {
-      const int b = x / p.g;
-      v = *reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.Hq + (size_t)kvh * p.g + (x - b * p.g)) * kD + 8 * c);
-    }
-    sts128(base + (c >> 3) * kQHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), query16<F>(v, p.in_dtype, p.sm_log2 < 0.f));
-  }
-  fence_async_shared();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  const int slot0 = both ? split : 2 * split + (tid >> 7);
   const uint32_t tmem = sh.tmem;
   int loads = 0;  // 16-bit pages: tiles that this warp has requested
   auto s_col = [&](int a) { return tmem + (uint32_t)(a * F::kS); };
@@ -431,6 +438,22 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
     const uint32_t S = s_col(a) + lanes, O = o_col(a) + lanes;
     const float sc = fabsf(p.sm_log2);
+    if (n > 0) {  // the lane's queries: 16 threads a row, 8 rows at a time
+      const int c = lane & 15, at = (c >> 3) * kQHalf;
+      uint4 v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int x = sh.row[32 * wid + 2 * k + (lane >> 4)];
+        v[k] = x >= 0 ? *reinterpret_cast<const uint4*>(p.q + (size_t)x * kD + 8 * c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int rr = 32 * wid + 2 * k + (lane >> 4);
+        sts128(base + at + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), query16<F>(v[k], p.in_dtype, p.sm_log2 < 0.f));
+      }
+      fence_async_shared();
+      mbar_arrive_s(smem_u32(&sh.bars.qready));
+    }
     float m = kFloor, l = 0.f;
     bool ok = true;
     int i = 0;
@@ -448,6 +471,8 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
 #pragma unroll
       for (int g = 0; g < F::kPages; ++g) {
         on[g] = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
+        const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on[g]);
+        if (lane == 0) sh.off[a][g][wid & 3] = off;
         uint32_t x[32];
         tmem_ld32(S + 32 * g, x);
         tmem_wait_ld(x);
@@ -503,12 +528,16 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       tc_fence_before();
       mbar_arrive_s(smem_u32(&sh.bars.pready[a]));
     }
-    // ---- this lane's partials
+    // ---- this lane's partials: 32 channels at a time through the lane's own queries' memory
+    // (its products have read them), so that a row's 128 bytes are written together
     if (ok && i > 0) ok = wait_phase(&sh.bars.ofull[a], 0, p.wait_polls, abort);
+    const bool some = ok && i > 0 && l != 0.f;
     if (ok && i > 0) {
       tc_fence_after();
       uint32_t vmin[4] = {0, 0, 0, 0};
       if (F::kPacked) tmem_ld4(O + kD, vmin);
+      const uint32_t buf = base + 32 * wid * 128;  // 4096 bytes: 32 rows of 128, swizzled
+      const int sub = lane >> 3, c4 = lane & 7;
 #pragma unroll
       for (int c = 0; c < kD; c += 32) {
         uint32_t x[32];
@@ -516,80 +545,79 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
         tmem_wait_ld(x);
         if (F::kPacked && c == 0) pin(vmin);
         const float add = __uint_as_float(vmin[c / 32]);
-        if (real && l != 0.f) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(part + 4 + c + k) =
-                make_float4(__uint_as_float(x[k]) + add, __uint_as_float(x[k + 1]) + add,
-                            __uint_as_float(x[k + 2]) + add, __uint_as_float(x[k + 3]) + add);
+        for (int k = 0; k < 8; ++k) {
+          uint4 v;
+          v.x = __float_as_uint(__uint_as_float(x[4 * k]) + add);
+          v.y = __float_as_uint(__uint_as_float(x[4 * k + 1]) + add);
+          v.z = __float_as_uint(__uint_as_float(x[4 * k + 2]) + add);
+          v.w = __float_as_uint(__uint_as_float(x[4 * k + 3]) + add);
+          sts128(buf + lane * 128 + ((k ^ (lane & 7)) << 4), v);
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + sub, x = sh.row[32 * wid + rr];
+          const uint4 v = lds128(buf + rr * 128 + ((c4 ^ (rr & 7)) << 4));
+          if (x >= 0)
+            *reinterpret_cast<uint4*>(p.ws + ((size_t)x * p.slots + slot0) * kPartialFloats + 4 + c + 4 * c4) = v;
+        }
+        __syncwarp();
       }
       tc_fence_before();
     }
-    if (real) {
-      const bool some = ok && i > 0 && l != 0.f;
-      part[0] = some ? m : -INFINITY;
-      part[1] = l;
-    }
+    if (real)
+      *reinterpret_cast<float2*>(p.ws + (part_row * p.slots + slot0) * kPartialFloats) = make_float2(some ? m : -INFINITY, l);
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
   } else if (wid == kMmaWarp) {
     // =========================================================== products
     constexpr uint32_t qk = mma_desc(F::kBf16, false, F::kS), pv = mma_desc(F::kBf16, !F::kPacked, F::kO);
-    bool started[2] = {false, false};
-    auto last_use = [&](int s) { return !both || (s & 1); };
-    auto scores = [&](int s) -> bool {
-      const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
-      if (!wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
-      tc_fence_after();
-      if (lane == 0) {
+    if (lane == 0 && n > 0) {
+      const uint64_t qdesc = smem_desc(base, 16, 1024, kSwizzle128), kdesc = smem_desc(kst, 16, 1024, kSwizzle128);
+      const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
+      bool started[2] = {false, false};
+      auto last_use = [&](int s) { return !both || (s & 1); };
+      auto scores = [&](int s) -> bool {
+        const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
+        if (!wait_one(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
+        tc_fence_after();
+        const uint64_t qa = qdesc + a * (128 * 128 / 16), kb = kdesc + st * (F::kKBytes / 16);
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) {
-          const uint32_t qa = base + (k >> 2) * kQHalf + a * (128 * 128) + 32 * (k & 3);
-          const uint32_t kb = kst + st * F::kKBytes + (k >> 2) * F::kKHalf + 32 * (k & 3);
-          mma_ss(s_col(a), smem_desc(qa, 16, 1024, kSwizzle128), smem_desc(kb, 16, 1024, kSwizzle128), qk, k > 0);
-        }
+        for (int k = 0; k < kD / 16; ++k)
+          mma_ss(s_col(a), qa + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
         mma_commit(smem_u32(&sh.bars.sfull[a]));
         if (last_use(s)) mma_commit(smem_u32(&sh.bars.kempty[st]));
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = scores(0) && (steps < 2 || scores(1));
-    for (int s = 0; ok && s < steps; ++s) {
-      const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
-      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
-           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
-      if (!ok) break;
-      tc_fence_after();
-      for (int g = 0; g < F::kPages; ++g) {
-        const int page = (t0 + tile) * F::kPages + g;
-        if (page >= page_end || sh.valid[tile % kFlags][g] == 0) continue;
-        uint32_t off[4] = {0, 0, 0, 0};
-        if (page >= sh.minpages[a]) {
+        return true;
+      };
+      bool ok = wait_one(&sh.bars.qready, 0, p.wait_polls, abort) && scores(0) && (steps < 2 || scores(1));
+      for (int s = 0; ok && s < steps; ++s) {
+        const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
+        ok = wait_one(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
+             wait_one(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vb = vdesc + st * (F::kVBytes / 16);
 #pragma unroll
-          for (int w = 0; w < 4; ++w) off[w] = __ballot_sync(0xFFFFFFFFu, sh.pages[128 * a + 32 * w + lane] <= page);
-        }
-        if (lane == 0) {
+        for (int g = 0; g < F::kPages; ++g) {
+          const uint4 o4 = *reinterpret_cast<const uint4*>(sh.off[a][g]);
+          if ((o4.x & o4.y & o4.z & o4.w) == 0xFFFFFFFFu) continue;  // no row sees it (or no page)
+          const uint32_t off[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t pa = s_col(a) + 32 * g + 8 * k;
-            const uint64_t vb = F::kPacked
-                ? smem_desc(vst + st * F::kVBytes + g * F::kSlab + 32 * k, 16, 512, kSwizzle64)
-                : smem_desc(vst + st * F::kVBytes + (32 * g + 16 * k) * 128, F::kKHalf, 1024, kSwizzle128);
-            mma_ts(o_col(a), pa, vb, pv, started[a] || k > 0, off);
-            if (F::kPair) mma_ts(o_col(a), pa + 16, vb, pv, true, off);
+            const uint64_t vk = vb + (F::kPacked ? (g * F::kSlab + 32 * k) / 16 : (32 * g + 16 * k) * 128 / 16);
+            mma_ts(o_col(a), pa, vk, pv, started[a] || k > 0, off);
+            if (F::kPair) mma_ts(o_col(a), pa + 16, vk, pv, true, off);
           }
+          started[a] = true;
         }
-        started[a] = true;
-      }
-      if (lane == 0) {
         if (last_use(s)) mma_commit(smem_u32(&sh.bars.vempty[st]));
         if (s + 2 >= steps) mma_commit(smem_u32(&sh.bars.ofull[a]));
+        else ok = scores(s + 2);
       }
-      __syncwarp();
-      if (s + 2 < steps) ok = scores(s + 2);
+      if (!ok) set_status(p.d_status, KITTY_ST_TIMEOUT);
     }
-    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
+    __syncwarp();
   } else if constexpr (F::kPacked) {
     // =========================================================== packed pages
     const int d = wid - kLoadWarp, g = d % F::kPages;
