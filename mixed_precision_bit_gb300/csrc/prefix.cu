@@ -20,12 +20,15 @@
 //           channel minima as one more row, so that Q K^T also gives q.M, which the
 //           softmax adds to the page's 32 scores;
 //   Values  step * code, exact, transposed; each token's four group minima as four more
-//           channels, which the end adds to the channels of their group.
-// So the only roundings are p to fp16 and, for 8-bit boosted Keys, step * code to fp16.
+//           channels, which the end adds to the channels of their group; and a channel of
+//           ones, whose column of O is the sum of the rounded p.
+// So the only roundings are p to fp16 and, for 8-bit boosted Keys, step * code to fp16; and
+// with the sum taken over the rounded p, theirs shift an output by at most 2^-11 of
+// sum p |v - out|.
 //
 // 16-bit pages (tiles of four pages) come by tiled TMA loads, swizzled, the Values as they
-// lie (N contiguous).  For bf16 p is a (high, rest) pair: one bf16 would leave an error of
-// 2^-9 of p, above what the decode keeps.
+// lie (N contiguous).  There is no room for a channel of ones beside 128 scores, and one bf16
+// p would leave an error of 2^-9: p is a (high, rest) pair, its sum taken in registers.
 //
 // Masks.  Sequence b sees its first prefix_pages[b] pages.  Its rows' probabilities are 0 for
 // later pages, and the products with those pages' Values leave its rows alone (the
@@ -62,7 +65,7 @@ struct PackedFmt {
   static constexpr bool kPacked = true, kBf16 = false, kPair = false;
   static constexpr int W = W_, V = V_, kPages = 3, kTok = 96;
   static constexpr int kS = 112;          // columns of S: 96 scores, 3 of q.M (16 is the granule)
-  static constexpr int kO = 144;          // columns of O: 128 channels, 4 group minima
+  static constexpr int kO = 144;          // columns of O: 128 channels, 4 group minima, the sum of p
   static constexpr int kKHalf = kS * 128, kKBytes = 2 * kKHalf;
   static constexpr int kSlab = kO * 64;   // a page's Values: [channel][64 bytes]
   static constexpr int kVBytes = kPages * kSlab;
@@ -76,7 +79,7 @@ struct PackedFmt {
 // 16-bit pages.
 template <bool BF>
 struct PlainFmt {
-  static constexpr bool kPacked = false, kBf16 = BF, kPair = BF;
+  static constexpr bool kPacked = false, kBf16 = BF, kPair = true;
   static constexpr int kPages = 4, kTok = 128, kS = 128, kO = 128;
   static constexpr int kKHalf = kTok * 128, kKBytes = 2 * kKHalf, kVBytes = kKBytes;
   static constexpr int kSlab = 0, kLoadWarps = 2, kRawBytes = 0;
@@ -97,7 +100,8 @@ struct Shared {
   Bars bars;
   uint32_t tmem;
   int abort;
-  int maxpages;
+  int maxpages, minpages;          // that a row of the block sees
+  int bad;                         // a page id out of range so far
   int row[kRows];                  // partials' row (sequence, query head); -1: padding
   uint8_t valid[kFlags][4];        // page ids in range, by tile
   alignas(16) uint32_t off[2][4][4];  // by lane and page: rows that do not see it, 32 a word
@@ -113,17 +117,6 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
     if (__all_sync(0xFFFFFFFFu, done)) return true;
     const bool stop = i >= polls || *abort != 0;
     if (__any_sync(0xFFFFFFFFu, stop)) break;
-  }
-  *abort = 1;
-  return false;
-}
-
-// The same for one thread.
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try(a, parity)) return true;
-    if (i >= polls || *abort != 0) break;
   }
   *abort = 1;
   return false;
@@ -187,41 +180,42 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
   const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
   const uint32_t row = stage + (32 * page + r) * 128 + 4 * qq;
-  // this lane's words of the base plane, one (W = 2) or two a j, and its steps
-  uint32_t plane[4 * W], S[16], top = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const uint4 v = lds128(raw + 16 * W * lane + 16 * i);
-    plane[4 * i] = v.x;
-    plane[4 * i + 1] = v.y;
-    plane[4 * i + 2] = v.z;
-    plane[4 * i + 3] = v.w;
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) S[i] = lds32(ks + 16 * i + 4 * qq);
+  uint32_t top = 0;  // largest step pair
   // minima of channels 4 lane .. 4 lane + 3
   const int mj = lane >> 2, mh = (lane >> 1) & 1, mq = 2 * (lane & 1), mrow = F::kTok + page;
   const uint32_t m0 = lds32(km + 4 * ((mq * 8 + mj) * 2 + mh)), m1 = lds32(km + 4 * (((mq + 1) * 8 + mj) * 2 + mh));
-#pragma unroll
+  // Rolled, here and below: six loading warps, the softmax and the products share one
+  // instruction cache, and unrolled bodies made every warp of the block wait for code
+  // (measured: the first page took 4000 to 8700 cycles, each later one 2200 to 3300).
+  uint32_t w[2], s0, s1;
+  auto load = [&](int j) {  // this lane's words of channels 16 j .., and the steps of its pairs
+    w[0] = lds32(raw + 16 * W * lane + 2 * W * j);
+    w[1] = W == 4 ? lds32(raw + 16 * W * lane + 2 * W * j + 4) : 0;
+    s0 = lds32(ks + 32 * j + 4 * qq);
+    s1 = lds32(ks + 32 * j + 16 + 4 * qq);
+  };
+  load(0);
+#pragma unroll 1
   for (int j = 0; j < 8; ++j) {
-    const uint32_t w[2] = {plane[W / 2 * j], plane[W / 2 * j + W / 2 - 1]};
+    const uint32_t x0 = w[0], x1 = w[1], st[2] = {s0, s1};
+    if (j < 7) load(j + 1);
+    const uint32_t half = row + (j >> 2) * F::kKHalf, chunk = 2 * (j & 3);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t s = S[2 * j + h];
-      top = h2max(top, s);
-      const uint32_t at = row + (j >> 2) * F::kKHalf + (((2 * (j & 3) + h) ^ r) << 4);
+      top = h2max(top, st[h]);
+      const uint32_t at = half + (((chunk + h) ^ r) << 4);
       if (W == 2) {
-        const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
-        sts32(at, h2mul(codes<2, 0>(x), s));
-        sts32(at + 1024, h2mul(codes<2, 1>(x), s));
-        sts32(at + 2048, h2mul(codes<2, 2>(x), s));
-        sts32(at + 3072, h2mul(codes<2, 3>(x), s));
+        const uint32_t x = h ? __funnelshift_r(x0, x0, 8) : x0;
+        sts32(at, h2mul(codes<2, 0>(x), st[h]));
+        sts32(at + 1024, h2mul(codes<2, 1>(x), st[h]));
+        sts32(at + 2048, h2mul(codes<2, 2>(x), st[h]));
+        sts32(at + 3072, h2mul(codes<2, 3>(x), st[h]));
       } else {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t x = h ? __funnelshift_r(w[mt], w[mt], 8) : w[mt];
-          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), s));
-          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), s));
+          const uint32_t y = mt ? x1 : x0, x = h ? __funnelshift_r(y, y, 8) : y;
+          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), st[h]));
+          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), st[h]));
         }
       }
     }
@@ -242,6 +236,7 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
   const uint32_t base = stage + (32 * page + r) * 128, lo_plane = raw + 512 * W + 2 * W * nx * lane;
+#pragma unroll 1
   for (int js = 0; js < nx; ++js) {
     const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
     uint32_t lo[2];
@@ -296,32 +291,23 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
   const uint32_t vs = raw + 512 * V, vm = vs + 256;
   const uint32_t sw = (r >> 1) & 3;
   uint32_t top = 0;
-  uint32_t plane[4 * V];  // this lane's words: one (V = 2) or two a (G, kt)
-  uint4 steps[4];
-#pragma unroll
-  for (int G = 0; G < 4; ++G) steps[G] = lds128(vs + 64 * G + 16 * qq);
   const uint4 m4 = lds128(vm + 64 * (r & 3) + 16 * qq);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const uint4 v = lds128(raw + 16 * V * lane + 16 * i);
-    plane[4 * i] = v.x;
-    plane[4 * i + 1] = v.y;
-    plane[4 * i + 2] = v.z;
-    plane[4 * i + 3] = v.w;
-  }
-#pragma unroll
+#pragma unroll 1
   for (int G = 0; G < 4; ++G) {
-    const uint32_t S[4] = {steps[G].x, steps[G].y, steps[G].z, steps[G].w};
+    const uint4 s4 = lds128(vs + 64 * G + 16 * qq);
+    const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
+    uint32_t w[2 * (V / 2)];  // one (V = 2) or two a kt
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = lds32(raw + 16 * V * lane + 4 * V * G + 4 * i);
     const uint32_t row = slab + (32 * G + r) * 64 + 4 * qq;
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      const uint32_t w[2] = {plane[V / 2 * (2 * G + kt)], plane[V / 2 * (2 * G + kt) + V / 2 - 1]};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t s = S[2 * kt + h], at = row + (((2 * kt + h) ^ sw) << 4);
         top = h2max(top, s);
         if (V == 2) {
-          const uint32_t x = h ? __funnelshift_r(w[0], w[0], 8) : w[0];
+          const uint32_t x = h ? __funnelshift_r(w[kt], w[kt], 8) : w[kt];
           sts32(at, h2mul(codes<2, 0>(x), s));
           sts32(at + 512, h2mul(codes<2, 1>(x), s));
           sts32(at + 1024, h2mul(codes<2, 2>(x), s));
@@ -329,7 +315,7 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
         } else {
 #pragma unroll
           for (int mc = 0; mc < 2; ++mc) {
-            const uint32_t x = h ? __funnelshift_r(w[mc], w[mc], 8) : w[mc];
+            const uint32_t y = w[V / 2 * kt + (V == 4 ? mc : 0)], x = h ? __funnelshift_r(y, y, 8) : y;
             sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
             sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
           }
@@ -360,13 +346,83 @@ __device__ __forceinline__ uint4 query16(uint4 v, int in_dtype, bool negate) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
+__device__ __forceinline__ uint64_t pair64(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two probabilities in the operand's type; kPair: (high, rest).
+template <class F>
+__device__ __forceinline__ uint32_t pack_probs(float e0, float e1, uint32_t& rest) {
+  if (!F::kBf16) {
+    const __half2 h = __floats2half2_rn(e0, e1);
+    if (F::kPair) {
+      const float2 f = __half22float2(h);
+      rest = h2_bits(__floats2half2_rn(e0 - f.x, e1 - f.y));
+    }
+    return h2_bits(h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+  const uint32_t hi = *reinterpret_cast<const uint32_t*>(&h);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xFFFF0000u));
+  rest = *reinterpret_cast<const uint32_t*>(&r);
+  return hi;
+}
+
+// The maximum of some row of the warp has passed the slack at page g of a tile: O (when some
+// tile has gone into it) and the tile's probabilities so far are scaled by the rows' f (1:
+// unchanged, bit for bit; else the probabilities are rounded once more).
+template <class F>
+__device__ __forceinline__ void rescale_row(uint32_t O, uint32_t S, int g, bool has_o, float f) {
+#pragma unroll 1
+  for (int c = has_o ? 0 : F::kO; c < F::kO; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(O + c, x);
+    tmem_wait_ld(x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+    tmem_st16(O + c, x);
+  }
+  tmem_wait_st();  // this thread's probabilities are written before they are read
+#pragma unroll 1
+  for (int j = 0; j < g; ++j) {
+    uint32_t x[16], y[16];
+    tmem_ld16(S + 32 * j, x);
+    tmem_wait_ld(x);
+    if (F::kPair) {
+      tmem_ld16(S + 32 * j + 16, y);
+      tmem_wait_ld(y);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (f == 1.f) break;  // rewritten as they are
+      float2 v;
+      if (F::kBf16) {
+        v.x = __uint_as_float(x[k] << 16) + (F::kPair ? __uint_as_float(y[k] << 16) : 0.f);
+        v.y = __uint_as_float(x[k] & 0xFFFF0000u) + (F::kPair ? __uint_as_float(y[k] & 0xFFFF0000u) : 0.f);
+      } else {
+        v = __half22float2(bits_h2(x[k]));
+        if (F::kPair) {
+          const float2 r = __half22float2(bits_h2(y[k]));
+          v = make_float2(v.x + r.x, v.y + r.y);
+        }
+      }
+      x[k] = pack_probs<F>(v.x * f, v.y * f, y[k]);
+    }
+    tmem_st16(S + 32 * j, x);
+    if (F::kPair) tmem_st16(S + 32 * j + 16, y);
+  }
+}
+
 template <class F>
 __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const PrefixArgs p,
                                                                     const __grid_constant__ CUtensorMap map) {
   extern __shared__ uint8_t dyn[];
   __shared__ Shared sh;
   grid_trigger();
-  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int wid = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // the compiler sees a warp-uniform role
   const int R = p.B * p.g, units = (R + kRows - 1) / kRows;
   const int kvh = blockIdx.x / units, unit = blockIdx.x - kvh * units, split = blockIdx.y;
   const bool both = R > 128;  // two lanes of rows; else the lanes share the rows and alternate
@@ -394,6 +450,8 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     fence_mbar_init();
     sh.abort = 0;
     sh.maxpages = 0;
+    sh.minpages = p.n_prefix;
+    sh.bad = 0;
   }
   // ---- the rows: what each sees of the prefix, its partials' place
   const int in_unit = unit * kRows + (both ? tid : (tid & 127));  // row of the kv head
@@ -410,7 +468,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int page_end = p.n_prefix;  // pages that some row of the block sees
+  int page_end = p.n_prefix, full_pages = p.n_prefix;  // pages that some row, every row, of the block sees
   if (p.prefix_pages != nullptr) {
     if (real) {
       if (my_pages < 0 || my_pages > p.n_prefix) {
@@ -418,16 +476,18 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
         my_pages = 0;
       }
       atomicMax(&sh.maxpages, my_pages);
+      atomicMin(&sh.minpages, my_pages);
     }
     __syncthreads();
-    page_end = sh.maxpages;
+    page_end = __shfl_sync(0xFFFFFFFFu, sh.maxpages, 0);
+    full_pages = __shfl_sync(0xFFFFFFFFu, sh.minpages, 0);
   }
   const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
   const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
   const int n = max(0, min(t1, (page_end + F::kPages - 1) / F::kPages) - t0);  // tiles of this block
   const int steps = both ? 2 * n : n;  // step s: lane s & 1, tile s / 2 or s
   const int slot0 = both ? split : 2 * split + (tid >> 7);
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
   int loads = 0;  // 16-bit pages: tiles that this warp has requested
   auto s_col = [&](int a) { return tmem + (uint32_t)(a * F::kS); };
   auto o_col = [&](int a) { return tmem + (uint32_t)(2 * F::kS + a * F::kO); };
@@ -438,6 +498,10 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
     const uint32_t S = s_col(a) + lanes, O = o_col(a) + lanes;
     const float sc = fabsf(p.sm_log2);
+    if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's minima
+      const uint32_t at = vst + (tid / (4 * F::kPages)) * F::kVBytes + (tid / 4 % F::kPages) * F::kSlab + (kD + 4) * 64;
+      sts128(at + 16 * (tid & 3), make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u));
+    }
     if (n > 0) {  // the lane's queries: 16 threads a row, 8 rows at a time
       const int c = lane & 15, at = (c >> 3) * kQHalf;
       uint4 v[16];
@@ -454,7 +518,9 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       fence_async_shared();
       mbar_arrive_s(smem_u32(&sh.bars.qready));
     }
-    float m = kFloor, l = 0.f;
+    float m = kFloor;
+    float2 sum = make_float2(0.f, 0.f);  // 16-bit pages: two partial sums of p
+    bool any = false;                    // this row has seen a page
     bool ok = true;
     int i = 0;
     for (int s = a; s < steps; s += 2, ++i) {
@@ -464,65 +530,61 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       }
       tc_fence_after();
       const int tile = both ? s >> 1 : s, page0 = (t0 + tile) * F::kPages;
-      uint32_t bias[4] = {0, 0, 0, 0};
-      if (F::kPacked) tmem_ld4(S + F::kTok, bias);
-      bool on[F::kPages];
-      float mx = kFloor;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < F::kPages; ++g) {
-        on[g] = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
-        const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on[g]);
-        if (lane == 0) sh.off[a][g][wid & 3] = off;
-        uint32_t x[32];
+        uint32_t x[32], bias = 0;
+        if (F::kPacked) tmem_ld1(S + F::kTok + g, bias);
         tmem_ld32(S + 32 * g, x);
+        // the rows that do not see this page, for the products' masks
+        const bool on = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
+        any = any || on;
+        const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on);
+        if (lane == 0) sh.off[a][g][wid & 3] = off;
         tmem_wait_ld(x);
-        if (F::kPacked && g == 0) pin(bias);
+        if (F::kPacked) pin(bias);
         float pm = __uint_as_float(x[0]);
 #pragma unroll
-        for (int k = 1; k < 32; ++k) pm = fmaxf(pm, __uint_as_float(x[k]));
-        if (on[g]) mx = fmaxf(mx, (pm + __uint_as_float(bias[g])) * sc);
-      }
-      if (i == 0) {
-        m = mx;
-      } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-        const float nm = fmaxf(m, mx), f = ex2a(m - nm);
-#pragma unroll
-        for (int c = 0; c < F::kO; c += 16) {
-          uint32_t x[16];
-          tmem_ld16(O + c, x);
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-          tmem_st16(O + c, x);
+        for (int k = 1; k < 31; k += 2) pm = fmaxf(fmaxf(pm, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+        pm = fmaxf(pm, __uint_as_float(x[31]));
+        const float mx = on ? fmaxf((pm + __uint_as_float(bias)) * sc, kFloor) : kFloor;
+        if ((i | g) == 0) {
+          m = mx;
+        } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+          // each row by its own maximum: what it gives does not depend on its neighbours'
+          const float nm = mx > m + kSlack ? mx : m, f = nm > m ? ex2a(m - nm) : 1.f;
+          rescale_row<F>(O, S, g, i > 0, f);
+          sum = make_float2(sum.x * f, sum.y * f);
+          m = nm;
         }
-        l *= f;
-        m = nm;
-      }
+        const float shift = fmaf(__uint_as_float(bias), sc, -m);
+        const uint64_t sc2 = f2pack(sc, sc), shift2 = f2pack(shift, shift);
+        uint64_t acc = f2pack(sum.x, sum.y);
+        uint32_t P[16], rest[16];
+        if (off == 0) {
 #pragma unroll
-      for (int g = 0; g < F::kPages; ++g) {
-        uint32_t x[32];
-        tmem_ld32(S + 32 * g, x);
-        tmem_wait_ld(x);
-        const float off = fmaf(__uint_as_float(bias[g]), sc, -m);
-        uint32_t hi[16], lo[16];
+          for (int k = 0; k < 16; ++k) {
+            uint64_t e2;
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(pair64(x[2 * k], x[2 * k + 1])), "l"(sc2), "l"(shift2));
+            float e0, e1;
+            f2unpack(e2, e0, e1);
+            e0 = ex2a(e0);
+            e1 = ex2a(e1);
+            if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
+            P[k] = pack_probs<F>(e0, e1, rest[k]);
+          }
+        } else {  // a mixed page: what a row does not see may hold anything
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float e0 = on[g] ? ex2a(fmaf(__uint_as_float(x[2 * k]), sc, off)) : 0.f;
-          const float e1 = on[g] ? ex2a(fmaf(__uint_as_float(x[2 * k + 1]), sc, off)) : 0.f;
-          l += e0 + e1;
-          if (F::kBf16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-            hi[k] = *reinterpret_cast<const uint32_t*>(&h);
-            const float2 hf = __bfloat1622float2(h);
-            const __nv_bfloat162 r = __floats2bfloat162_rn(e0 - hf.x, e1 - hf.y);
-            lo[k] = *reinterpret_cast<const uint32_t*>(&r);
-          } else {
-            hi[k] = h2_bits(__floats2half2_rn(e0, e1));
+          for (int k = 0; k < 16; ++k) {
+            const float e0 = on ? ex2a(fmaf(__uint_as_float(x[2 * k]), sc, shift)) : 0.f;
+            const float e1 = on ? ex2a(fmaf(__uint_as_float(x[2 * k + 1]), sc, shift)) : 0.f;
+            if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
+            P[k] = pack_probs<F>(e0, e1, rest[k]);
           }
         }
+        f2unpack(acc, sum.x, sum.y);
         // over the page's own scores, which this thread has taken
-        tmem_st16(S + 32 * g, hi);
-        if (F::kPair) tmem_st16(S + 32 * g + 16, lo);
+        tmem_st16(S + 32 * g, P);
+        if (F::kPair) tmem_st16(S + 32 * g + 16, rest);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -531,20 +593,25 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     // ---- this lane's partials: 32 channels at a time through the lane's own queries' memory
     // (its products have read them), so that a row's 128 bytes are written together
     if (ok && i > 0) ok = wait_phase(&sh.bars.ofull[a], 0, p.wait_polls, abort);
-    const bool some = ok && i > 0 && l != 0.f;
+    float total = sum.x + sum.y;
     if (ok && i > 0) {
       tc_fence_after();
-      uint32_t vmin[4] = {0, 0, 0, 0};
-      if (F::kPacked) tmem_ld4(O + kD, vmin);
+      if (F::kPacked) {
+        uint32_t t;
+        tmem_ld1(O + kD + 4, t);
+        tmem_wait_ld(t);
+        total = __uint_as_float(t);
+      }
       const uint32_t buf = base + 32 * wid * 128;  // 4096 bytes: 32 rows of 128, swizzled
       const int sub = lane >> 3, c4 = lane & 7;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
-        uint32_t x[32];
+        uint32_t x[32], vmin = 0;
+        if (F::kPacked) tmem_ld1(O + kD + c / 32, vmin);
         tmem_ld32(O + c, x);
         tmem_wait_ld(x);
-        if (F::kPacked && c == 0) pin(vmin);
-        const float add = __uint_as_float(vmin[c / 32]);
+        if (F::kPacked) pin(vmin);
+        const float add = __uint_as_float(vmin);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           uint4 v;
@@ -567,55 +634,85 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       tc_fence_before();
     }
     if (real)
-      *reinterpret_cast<float2*>(p.ws + (part_row * p.slots + slot0) * kPartialFloats) = make_float2(some ? m : -INFINITY, l);
+      *reinterpret_cast<float2*>(p.ws + (part_row * p.slots + slot0) * kPartialFloats) = make_float2(ok && any ? m : -INFINITY, total);
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
   } else if (wid == kMmaWarp) {
     // =========================================================== products
     constexpr uint32_t qk = mma_desc(F::kBf16, false, F::kS), pv = mma_desc(F::kBf16, !F::kPacked, F::kO);
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
+      // The whole warp runs this, one elected lane issues: descriptors stay in uniform registers.
       const uint64_t qdesc = smem_desc(base, 16, 1024, kSwizzle128), kdesc = smem_desc(kst, 16, 1024, kSwizzle128);
       const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
+      const int both_shift = both ? 1 : 0;
       bool started[2] = {false, false};
-      auto last_use = [&](int s) { return !both || (s & 1); };
-      auto scores = [&](int s) -> bool {
-        const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
-        if (!wait_one(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
+      // S of step s; `first`: no step before it has waited for its tile's Keys
+      auto scores = [&](int s, int a, bool first, bool last) -> bool {
+        const int tile = s >> both_shift, st = tile % kStages;
+        if (first && !wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
         tc_fence_after();
         const uint64_t qa = qdesc + a * (128 * 128 / 16), kb = kdesc + st * (F::kKBytes / 16);
+        const uint32_t d = s_col(a);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k)
-          mma_ss(s_col(a), qa + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
-        mma_commit(smem_u32(&sh.bars.sfull[a]));
-        if (last_use(s)) mma_commit(smem_u32(&sh.bars.kempty[st]));
+          for (int k = 0; k < kD / 16; ++k)
+            mma_ss(d, qa + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
+          mma_commit(smem_u32(&sh.bars.sfull[a]));
+          if (last) mma_commit(smem_u32(&sh.bars.kempty[st]));
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = wait_one(&sh.bars.qready, 0, p.wait_polls, abort) && scores(0) && (steps < 2 || scores(1));
-      for (int s = 0; ok && s < steps; ++s) {
-        const int a = s & 1, tile = both ? s >> 1 : s, st = tile % kStages;
-        ok = wait_one(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
-             wait_one(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
-        if (!ok) break;
+      // O += P V of step s, then the scores of the lane's next tile
+      auto step = [&](int s, int a) -> bool {
+        const bool first = !both || a == 0, last = !both || a == 1;  // of the tile's uses
+        const int tile = s >> both_shift, st = tile % kStages, page0 = (t0 + tile) * F::kPages;
+        if (first && !wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
+        if (!wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort)) return false;
         tc_fence_after();
         const uint64_t vb = vdesc + st * (F::kVBytes / 16);
+        const uint32_t d = o_col(a), pcol = s_col(a);
+        if (page0 + F::kPages <= full_pages && *static_cast<volatile int*>(&sh.bad) == 0) {
+          // every row of the block sees every page of the tile
+          if (elect_one()) {
 #pragma unroll
-        for (int g = 0; g < F::kPages; ++g) {
-          const uint4 o4 = *reinterpret_cast<const uint4*>(sh.off[a][g]);
-          if ((o4.x & o4.y & o4.z & o4.w) == 0xFFFFFFFFu) continue;  // no row sees it (or no page)
-          const uint32_t off[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t pa = s_col(a) + 32 * g + 8 * k;
-            const uint64_t vk = vb + (F::kPacked ? (g * F::kSlab + 32 * k) / 16 : (32 * g + 16 * k) * 128 / 16);
-            mma_ts(o_col(a), pa, vk, pv, started[a] || k > 0, off);
-            if (F::kPair) mma_ts(o_col(a), pa + 16, vk, pv, true, off);
+            for (int k = 0; k < 2 * F::kPages; ++k) {
+              const uint64_t vk = vb + (F::kPacked ? ((k >> 1) * F::kSlab + 32 * (k & 1)) / 16 : 16 * k * 128 / 16);
+              mma_ts(d, pcol + 16 * k - 8 * (k & 1), vk, pv, started[a] || k > 0);
+              if (F::kPair) mma_ts(d, pcol + 16 * k - 8 * (k & 1) + 16, vk, pv, true);
+            }
           }
           started[a] = true;
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < F::kPages; ++g) {
+            const uint4 o4 = *reinterpret_cast<const uint4*>(sh.off[a][g]);
+            if (__any_sync(0xFFFFFFFFu, (o4.x & o4.y & o4.z & o4.w) == 0xFFFFFFFFu)) continue;  // no row sees it, or no page
+            const uint32_t off[4] = {o4.x, o4.y, o4.z, o4.w};
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t pa = pcol + 32 * g + 8 * k;
+                const uint64_t vk = vb + (F::kPacked ? (g * F::kSlab + 32 * k) / 16 : (32 * g + 16 * k) * 128 / 16);
+                mma_ts_masked(d, pa, vk, pv, started[a] || k > 0, off);
+                if (F::kPair) mma_ts_masked(d, pa + 16, vk, pv, true, off);
+              }
+            }
+            __syncwarp();
+            started[a] = true;
+          }
         }
-        if (last_use(s)) mma_commit(smem_u32(&sh.bars.vempty[st]));
-        if (s + 2 >= steps) mma_commit(smem_u32(&sh.bars.ofull[a]));
-        else ok = scores(s + 2);
-      }
-      if (!ok) set_status(p.d_status, KITTY_ST_TIMEOUT);
+        const bool more = s + 2 < steps;
+        if (elect_one()) {
+          if (last) mma_commit(smem_u32(&sh.bars.vempty[st]));
+          if (!more) mma_commit(smem_u32(&sh.bars.ofull[a]));
+        }
+        __syncwarp();
+        return !more || scores(s + 2, a, first, last);
+      };
+      bool ok = wait_phase(&sh.bars.qready, 0, p.wait_polls, abort) && scores(0, 0, true, !both) &&
+                (steps < 2 || scores(1, 1, !both, true));
+      for (int s = 0; ok && s < steps; s += 2) ok = step(s, 0) && (s + 1 >= steps || step(s + 1, 1));
+      if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     }
     __syncwarp();
   } else if constexpr (F::kPacked) {
@@ -669,7 +766,10 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
         if (values) put_values<F>(raw, vst + st * F::kVBytes + g * F::kSlab, p.d_status);
         else put_keys<F>(raw, kst + st * F::kKBytes, g, p.n_hi, p.d_status);
       }
-      if (!values && lane == 0) sh.valid[tile % kFlags][g] = in;
+      if (!values && lane == 0) {
+        sh.valid[tile % kFlags][g] = in;
+        if (!in) sh.bad = 1;
+      }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
@@ -698,7 +798,10 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       const int count = __popc(__ballot_sync(0xFFFFFFFFu, in));
       const uint32_t bar = smem_u32(&full[st]);
       if (lane < F::kPages) {
-        if (!values) sh.valid[tile % kFlags][lane] = in;
+        if (!values) {
+          sh.valid[tile % kFlags][lane] = in;
+          if (!in) sh.bad = 1;
+        }
         if (!in && page < page_end) set_status(p.d_status, KITTY_ST_BAD_PAGE);
       }
       __syncwarp();  // the flags, before the arrival that publishes them
@@ -717,7 +820,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
   }
   __syncthreads();
   // after a wait that ran out: nothing may be in flight when the block's memory is given back
-  if (*abort != 0 && lane == 0) {
+  if (*abort != 0 && elect_one()) {
     if (wid == kMmaWarp) {
       mma_commit(smem_u32(&sh.bars.drain));
       mbar_wait_bounded(&sh.bars.drain, 0, kPrefixWaitPolls);
