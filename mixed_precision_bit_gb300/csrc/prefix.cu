@@ -9,9 +9,10 @@
 //   p = 2^(s - m)      one thread a row: its scores from tensor memory, the running maximum
 //                      and sum in registers, p back over S as the next product's operand
 //   O += P V           tcgen05.mma with P in tensor memory, fp32 in tensor memory
-// The maximum m only moves when a score passes it by more than 2^8 (p then stays <= 256, well
-// inside fp16), so O is rescaled a few times at the start and hardly ever later.
-// Warps: 4 a lane for the softmax, one issuing products, the rest loading.  While one
+// m is not the maximum itself: it is set 2^6 above the first page's, and moves only when a
+// score passes it by more than 2^8 (p then stays <= 256, well inside fp16), so that O is
+// hardly ever rescaled: a rescale costs the lane about a tile's time.
+// Warps: 4 a lane for the softmax, one a lane issuing products, the rest loading.  While one
 // lane's softmax runs, the tensor cores work on the other's products.
 //
 // Packed pages (tiles of three pages).  A loading warp takes one page's Keys or Values of
@@ -54,10 +55,11 @@ constexpr int kStages = 2;                // of Keys and of Values
 constexpr int kFlags = 8;                 // tiles whose page flags are kept
 constexpr uint32_t kPrefixWaitPolls = 1u << 22;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 9;
+constexpr int kMmaWarp = 8;               // and the next: one a lane
+constexpr int kLoadWarp = 10;
 constexpr float kFloor = -1.0e30f;        // a row without a score yet
-constexpr float kSlack = 8.f;             // log2 units the maximum may lag behind
+constexpr float kSlack = 8.f;             // log2 units the maximum may lag behind ..
+constexpr float kMargin = 6.f;            // .. or run ahead, when it is set
 
 // Packed pages: Key planes of W bits, Values of V bits.
 template <int W_, int V_>
@@ -69,11 +71,13 @@ struct PackedFmt {
   static constexpr int kKHalf = kS * 128, kKBytes = 2 * kKHalf;
   static constexpr int kSlab = kO * 64;   // a page's Values: [channel][64 bytes]
   static constexpr int kVBytes = kPages * kSlab;
-  static constexpr int kLoadWarps = 2 * kPages;
-  static constexpr int kRaw = W == 2 ? 4 : 2;                // staged page parts a warp
+  // two warps for a page's Keys (64 channels each), one for its Values; one idle, so that the
+  // block is five warpgroups
+  static constexpr int kLoadWarps = 3 * kPages + 1;
+  static constexpr int kRaw = W == 2 ? 2 : 1;                // staged page parts a warp
   static constexpr int kRawK = 512 * W + 128 * 4 * W + 512 + 128;  // at n_hi = 128
   static constexpr int kRawV = 512 * V + 512;
-  static constexpr int kRawBytes = kPages * kRaw * (kRawK + kRawV);
+  static constexpr int kRawBytes = kPages * kRaw * (2 * kRawK + kRawV);
 };
 
 // 16-bit pages.
@@ -92,8 +96,8 @@ __host__ __device__ constexpr int smem_of() { return 1024 + kQBytes + kStages * 
 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t sfull[2], pready[2], ofull[2], qready, drain;
-  uint64_t raw[6][4];
+  uint64_t sfull[2], pready[2], ofull[2], qready[2], drain[2], turn[2];
+  uint64_t raw[9][2];
 };
 
 struct Shared {
@@ -154,7 +158,6 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 }
 
 __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
-__device__ __forceinline__ uint32_t h2max(uint32_t a, uint32_t b) { return h2_bits(__hmax2(bits_h2(a), bits_h2(b))); }
 
 // Both halves' codes of class K of a plane word as fp16 integers.  2-bit planes: class
 // K = token or channel block 0..3, at bits 2K + 2; 4-bit planes: K = 0, 1, at bits 4K + 2.  A
@@ -170,75 +173,72 @@ __device__ __forceinline__ uint32_t codes(uint32_t x) {
   return h2_bits(__hfma2(bits_h2(y), inv, off));
 }
 
-// A page's Key part (staged at raw, as in the page up to the channel list) to rows
-// 32 page .. of the stage, and its minima to row kTok + page.  Lane (r, qq) holds tokens r,
-// r + 8, r + 16, r + 24 of the channels 16j + 8h + 2qq + {0, 1}: pairs of channels, and the
-// eight rows of a warp's store lie in different swizzled 16-byte columns.
+// A stored step so large that a step times a code may leave fp16.
+template <int BITS>
+__device__ __forceinline__ bool step_too_large(uint32_t pair) {
+  const float2 f = __half22float2(bits_h2(pair));
+  return !(fmaxf(f.x, f.y) * (float)(1 << BITS) <= 65504.f);
+}
+
+// Channels 64 half .. of a page's Key part (staged at raw, as in the page up to the channel
+// list) to rows 32 page .. of the stage, and their minima to row kTok + page.  Lane (r, qq)
+// holds tokens r, r + 8, r + 16, r + 24 of the channels 16j + 8h + 2qq + {0, 1}: pairs of
+// channels, and the eight rows of a warp's store lie in different swizzled 16-byte columns.
 template <class F>
-__device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page, int n_hi, int32_t* d_status) {
+__device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page, int half, int n_hi, int32_t* d_status) {
   constexpr int W = F::W;
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
   const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
-  const uint32_t row = stage + (32 * page + r) * 128 + 4 * qq;
-  uint32_t top = 0;  // largest step pair
-  // minima of channels 4 lane .. 4 lane + 3
-  const int mj = lane >> 2, mh = (lane >> 1) & 1, mq = 2 * (lane & 1), mrow = F::kTok + page;
-  const uint32_t m0 = lds32(km + 4 * ((mq * 8 + mj) * 2 + mh)), m1 = lds32(km + 4 * (((mq + 1) * 8 + mj) * 2 + mh));
-  // Rolled, here and below: six loading warps, the softmax and the products share one
-  // instruction cache, and unrolled bodies made every warp of the block wait for code
-  // (measured: the first page took 4000 to 8700 cycles, each later one 2200 to 3300).
-  uint32_t w[2], s0, s1;
-  auto load = [&](int j) {  // this lane's words of channels 16 j .., and the steps of its pairs
-    w[0] = lds32(raw + 16 * W * lane + 2 * W * j);
-    w[1] = W == 4 ? lds32(raw + 16 * W * lane + 2 * W * j + 4) : 0;
-    s0 = lds32(ks + 32 * j + 4 * qq);
-    s1 = lds32(ks + 32 * j + 16 + 4 * qq);
-  };
-  load(0);
-#pragma unroll 1
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t x0 = w[0], x1 = w[1], st[2] = {s0, s1};
-    if (j < 7) load(j + 1);
-    const uint32_t half = row + (j >> 2) * F::kKHalf, chunk = 2 * (j & 3);
+  const uint32_t dst = stage + half * F::kKHalf, row = dst + (32 * page + r) * 128 + 16 * r;  // + swizzle
+  uint32_t w[2 * W];  // this lane's words of the half: one (W = 2) or two a j
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) {
+    const uint4 v = lds128(raw + 16 * W * lane + 8 * W * half + 16 * i);
+    w[4 * i] = v.x;
+    w[4 * i + 1] = v.y;
+    w[4 * i + 2] = v.z;
+    w[4 * i + 3] = v.w;
+  }
+  const uint32_t sq = ks + 128 * half + 4 * qq;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      top = h2max(top, st[h]);
-      const uint32_t at = half + (((chunk + h) ^ r) << 4);
-      if (W == 2) {
-        const uint32_t x = h ? __funnelshift_r(x0, x0, 8) : x0;
-        sts32(at, h2mul(codes<2, 0>(x), st[h]));
-        sts32(at + 1024, h2mul(codes<2, 1>(x), st[h]));
-        sts32(at + 2048, h2mul(codes<2, 2>(x), st[h]));
-        sts32(at + 3072, h2mul(codes<2, 3>(x), st[h]));
-      } else {
+      const uint32_t S = lds32(sq + 32 * j + 16 * h);
+      const uint32_t at = (row ^ (16 * (2 * j + h))) + 4 * qq;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t y = mt ? x1 : x0, x = h ? __funnelshift_r(y, y, 8) : y;
-          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), st[h]));
-          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), st[h]));
+      for (int mt = 0; mt < W / 2; ++mt) {
+        const uint32_t y = w[W / 2 * j + mt], x = h ? __funnelshift_r(y, y, 8) : y;
+        if (W == 2) {
+          sts32(at, h2mul(codes<2, 0>(x), S));
+          sts32(at + 1024, h2mul(codes<2, 1>(x), S));
+          sts32(at + 2048, h2mul(codes<2, 2>(x), S));
+          sts32(at + 3072, h2mul(codes<2, 3>(x), S));
+        } else {
+          sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), S));
+          sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), S));
         }
       }
     }
   }
-  {
-    const uint32_t at = stage + (lane >> 4) * F::kKHalf + mrow * 128 + ((((lane & 15) >> 1) ^ (mrow & 7)) << 4) + 8 * (lane & 1);
-    sts32(at, m0);
-    sts32(at + 4, m1);
+  {  // minima of channels 64 half + 2 lane, + 1; their steps' range (boosted: times 2^W at most)
+    const int c = 64 * half + 2 * lane, m = F::kTok + page;
+    const uint32_t v = lds32(km + 4 * ((((c >> 1) & 3) * 8 + (c >> 4)) * 2 + ((c >> 3) & 1)));
+    sts32(dst + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) + 4 * (lane & 3), v);
+    if (step_too_large<W>(lds32(ks + 2 * c))) set_status(d_status, KITTY_ST_RANGE);
   }
-  // a step times a code (boosted: times 2^W at most) must stay in fp16
-  const float2 t = __half22float2(bits_h2(top));
-  if (!(fmaxf(t.x, t.y) * (float)(1 << W) <= 65504.f)) set_status(d_status, KITTY_ST_RANGE);
-  if (n_hi == 0) return;
-  // Boosted channels again, from both planes: step * high + step / 2^W * low.  This lane's
-  // columns of the extra plane are pairs too, of any two channels (c0, c1): their words of the
-  // base plane lie in the lanes of the same tokens.
-  __syncwarp();
+  // Boosted channels of this half again, from both planes: step * high + step / 2^W * low.
+  // This lane's columns of the extra plane are pairs too, of any two channels (c0 < c1): their
+  // words of the base plane lie in the lanes of the same tokens.
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
-  const uint32_t base = stage + (32 * page + r) * 128, lo_plane = raw + 512 * W + 2 * W * nx * lane;
+  const uint32_t lo_plane = raw + 512 * W + 2 * W * nx * lane, hi_plane = raw + 64 * W * r;
+  __syncwarp();
 #pragma unroll 1
   for (int js = 0; js < nx; ++js) {
     const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
+    const uint32_t outside = (half ? ~ids : ids) & 0x40404040u;  // channels of the other half
+    if (__all_sync(0xFFFFFFFFu, outside == 0x40404040u)) continue;  // the list ascends: most groups lie in one half
     uint32_t lo[2];
     lo[0] = lds32(lo_plane + 2 * W * js);
     lo[1] = W == 4 ? lds32(lo_plane + 2 * W * js + 4) : 0;
@@ -247,22 +247,22 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
     for (int i = 0; i < 4; ++i) {
       const uint32_t c = (ids >> (8 * i)) & 127u;
       st[i] = lds16(ks + 2 * c);
-      const uint32_t from = raw + 16 * W * (4 * r + ((c >> 1) & 3)) + 2 * W * (c >> 4);
-      const uint32_t turn = 16 * (c & 1) + 8 * ((c >> 3) & 1);
+      const uint32_t from = hi_plane + 8 * W * (c & 6) + 2 * W * (c >> 4);
 #pragma unroll
       for (int mt = 0; mt < W / 2; ++mt) {
         const uint32_t x = lds32(from + 4 * mt);
-        hi[i][mt] = __funnelshift_r(x, x, turn);  // the channel's codes in the low half
+        hi[i][mt] = __funnelshift_r(x, x, (c & 8) + 16 * (c & 1));  // the channel's codes in the low half
       }
-      at[i] = base + (c >> 6) * F::kKHalf + ((((c >> 3) & 7) ^ r) << 4) + 2 * (c & 7);
+      at[i] = row ^ ((2 * c) & 0x7Eu);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t s = st[2 * h] | (st[2 * h + 1] << 16), sl = h2mul(s, part);
+      const uint32_t s = __byte_perm(st[2 * h], st[2 * h + 1], 0x5410), sl = h2mul(s, part);
+      const bool in0 = !((outside >> (16 * h)) & 0x40u), in1 = !((outside >> (16 * h + 8)) & 0x40u);
       auto put = [&](int tau, uint32_t ch, uint32_t cl) {
         const uint32_t v = h2_bits(__hfma2(bits_h2(ch), bits_h2(s), bits_h2(h2mul(cl, sl))));
-        sts16(at[2 * h] + 1024 * tau, v);
-        sts16(at[2 * h + 1] + 1024 * tau, v >> 16);
+        if (in0) sts16(at[2 * h] + 1024 * tau, v);
+        if (in1) sts16(at[2 * h + 1] + 1024 * tau, v >> 16);
       };
 #pragma unroll
       for (int mt = 0; mt < W / 2; ++mt) {
@@ -283,39 +283,37 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
 }
 
 // A page's Value part (staged at raw: plane, steps, minima) to its slab, channels as rows of
-// 32 tokens, the four groups' minima as rows 128 .. 131.
+// 32 tokens, the four groups' minima as rows 128 .. 131.  (Rolled over the groups: loading
+// warps, softmax and products share one instruction cache; with everything unrolled the
+// first page of a block took 4000 to 8700 cycles, each later one 2200 to 3300.)
 template <class F>
 __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t* d_status) {
   constexpr int V = F::V;
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
   const uint32_t vs = raw + 512 * V, vm = vs + 256;
   const uint32_t sw = (r >> 1) & 3;
-  uint32_t top = 0;
-  const uint4 m4 = lds128(vm + 64 * (r & 3) + 16 * qq);
 #pragma unroll 1
   for (int G = 0; G < 4; ++G) {
     const uint4 s4 = lds128(vs + 64 * G + 16 * qq);
     const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
-    uint32_t w[2 * (V / 2)];  // one (V = 2) or two a kt
+    uint32_t w[V];  // one (V = 2) or two a kt
 #pragma unroll
     for (int i = 0; i < V; ++i) w[i] = lds32(raw + 16 * V * lane + 4 * V * G + 4 * i);
-    const uint32_t row = slab + (32 * G + r) * 64 + 4 * qq;
+    const uint32_t row = slab + (32 * G + r) * 64 + 16 * sw;
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t s = S[2 * kt + h], at = row + (((2 * kt + h) ^ sw) << 4);
-        top = h2max(top, s);
-        if (V == 2) {
-          const uint32_t x = h ? __funnelshift_r(w[kt], w[kt], 8) : w[kt];
-          sts32(at, h2mul(codes<2, 0>(x), s));
-          sts32(at + 512, h2mul(codes<2, 1>(x), s));
-          sts32(at + 1024, h2mul(codes<2, 2>(x), s));
-          sts32(at + 1536, h2mul(codes<2, 3>(x), s));
-        } else {
+        const uint32_t s = S[2 * kt + h], at = (row ^ (16 * (2 * kt + h))) + 4 * qq;
 #pragma unroll
-          for (int mc = 0; mc < 2; ++mc) {
-            const uint32_t y = w[V / 2 * kt + (V == 4 ? mc : 0)], x = h ? __funnelshift_r(y, y, 8) : y;
+        for (int mc = 0; mc < V / 2; ++mc) {
+          const uint32_t y = w[V / 2 * kt + mc], x = h ? __funnelshift_r(y, y, 8) : y;
+          if (V == 2) {
+            sts32(at, h2mul(codes<2, 0>(x), s));
+            sts32(at + 512, h2mul(codes<2, 1>(x), s));
+            sts32(at + 1024, h2mul(codes<2, 2>(x), s));
+            sts32(at + 1536, h2mul(codes<2, 3>(x), s));
+          } else {
             sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
             sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
           }
@@ -324,12 +322,13 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
     }
   }
   if (r < 4) {  // group r's minima of the tokens of column qq
+    const uint4 m4 = lds128(vm + 64 * r + 16 * qq);
     const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) sts32(slab + (kD + r) * 64 + ((i ^ sw) << 4) + 4 * qq, m[i]);
   }
-  const float2 t = __half22float2(bits_h2(top));
-  if (!(fmaxf(t.x, t.y) * (float)(1 << V) <= 65504.f)) set_status(d_status, KITTY_ST_RANGE);
+  if (step_too_large<V>(lds32(vs + 4 * lane)) || step_too_large<V>(lds32(vs + 128 + 4 * lane)))
+    set_status(d_status, KITTY_ST_RANGE);
 }
 
 // Eight queries' channels (16 bytes) in the operand's type; a negative scale is taken as
@@ -433,20 +432,21 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.bars.kfull[i], F::kPacked ? F::kPages : 1);
+      mbar_init(&sh.bars.kfull[i], F::kPacked ? 2 * F::kPages : 1);
       mbar_init(&sh.bars.vfull[i], F::kPacked ? F::kPages : 1);
-      mbar_init(&sh.bars.kempty[i], 1);
-      mbar_init(&sh.bars.vempty[i], 1);
+      mbar_init(&sh.bars.kempty[i], both ? 2 : 1);
+      mbar_init(&sh.bars.vempty[i], both ? 2 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.bars.sfull[i], 1);
       mbar_init(&sh.bars.pready[i], 128);
       mbar_init(&sh.bars.ofull[i], 1);
+      mbar_init(&sh.bars.qready[i], 128);
+      mbar_init(&sh.bars.drain[i], 1);
+      mbar_init(&sh.bars.turn[i], 1);
     }
-    mbar_init(&sh.bars.qready, kRows);
-    mbar_init(&sh.bars.drain, 1);
-    for (int i = 0; i < 6; ++i)
-      for (int k = 0; k < 4; ++k) mbar_init(&sh.bars.raw[i][k], 1);
+    for (int i = 0; i < 9; ++i)
+      for (int k = 0; k < 2; ++k) mbar_init(&sh.bars.raw[i][k], 1);
     fence_mbar_init();
     sh.abort = 0;
     sh.maxpages = 0;
@@ -464,6 +464,11 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     if (p.prefix_pages != nullptr) my_pages = p.prefix_pages[b];
   }
   if (tid < kRows) sh.row[tid] = real ? (int)part_row : -1;
+  if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's minima
+    const uint32_t at = vst + (tid / (4 * F::kPages)) * F::kVBytes + (tid / 4 % F::kPages) * F::kSlab + (kD + 4) * 64;
+    sts128(at + 16 * (tid & 3), make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u));
+    fence_async_shared();
+  }
   if (wid == kMmaWarp) tmem_alloc(smem_u32(&sh.tmem), 512);
   tc_fence_before();
   __syncthreads();
@@ -492,16 +497,17 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
   auto s_col = [&](int a) { return tmem + (uint32_t)(a * F::kS); };
   auto o_col = [&](int a) { return tmem + (uint32_t)(2 * F::kS + a * F::kO); };
 
+  // five warpgroups at 96 registers: the two of the softmax take 128, the others 64
+  if (F::kPacked) {
+    if (wid < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  }
   if (wid < kSoftmaxWarps) {
     // =========================================================== softmax
     const int a = wid >> 2;
     const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
     const uint32_t S = s_col(a) + lanes, O = o_col(a) + lanes;
     const float sc = fabsf(p.sm_log2);
-    if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's minima
-      const uint32_t at = vst + (tid / (4 * F::kPages)) * F::kVBytes + (tid / 4 % F::kPages) * F::kSlab + (kD + 4) * 64;
-      sts128(at + 16 * (tid & 3), make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u));
-    }
     if (n > 0) {  // the lane's queries: 16 threads a row, 8 rows at a time
       const int c = lane & 15, at = (c >> 3) * kQHalf;
       uint4 v[16];
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
         sts128(base + at + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), query16<F>(v[k], p.in_dtype, p.sm_log2 < 0.f));
       }
       fence_async_shared();
-      mbar_arrive_s(smem_u32(&sh.bars.qready));
+      mbar_arrive_s(smem_u32(&sh.bars.qready[wid >> 2]));
     }
     float m = kFloor;
     float2 sum = make_float2(0.f, 0.f);  // 16-bit pages: two partial sums of p
@@ -530,58 +536,68 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       }
       tc_fence_after();
       const int tile = both ? s >> 1 : s, page0 = (t0 + tile) * F::kPages;
-#pragma unroll 1
+      uint32_t x[2][32], bias[2] = {0, 0};
+      auto load = [&](int g) {
+        if (F::kPacked) tmem_ld1(S + F::kTok + g, bias[g & 1]);
+        tmem_ld32(S + 32 * g, x[g & 1]);
+      };
+      load(0);
+#pragma unroll
       for (int g = 0; g < F::kPages; ++g) {
-        uint32_t x[32], bias = 0;
-        if (F::kPacked) tmem_ld1(S + F::kTok + g, bias);
-        tmem_ld32(S + 32 * g, x);
+        uint32_t (&v)[32] = x[g & 1];
+        uint32_t& bg = bias[g & 1];
         // the rows that do not see this page, for the products' masks
         const bool on = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
         any = any || on;
         const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on);
         if (lane == 0) sh.off[a][g][wid & 3] = off;
-        tmem_wait_ld(x);
-        if (F::kPacked) pin(bias);
-        float pm = __uint_as_float(x[0]);
+        tmem_wait_ld(v);
+        if (F::kPacked) pin(bg);
+        if (g + 1 < F::kPages) load(g + 1);
+        auto seen_max = [&]() {  // this row's maximum on the page, scaled
+          float pm = __uint_as_float(v[0]);
 #pragma unroll
-        for (int k = 1; k < 31; k += 2) pm = fmaxf(fmaxf(pm, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
-        pm = fmaxf(pm, __uint_as_float(x[31]));
-        const float mx = on ? fmaxf((pm + __uint_as_float(bias)) * sc, kFloor) : kFloor;
-        if ((i | g) == 0) {
-          m = mx;
-        } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-          // each row by its own maximum: what it gives does not depend on its neighbours'
-          const float nm = mx > m + kSlack ? mx : m, f = nm > m ? ex2a(m - nm) : 1.f;
-          rescale_row<F>(O, S, g, i > 0, f);
-          sum = make_float2(sum.x * f, sum.y * f);
-          m = nm;
-        }
-        const float shift = fmaf(__uint_as_float(bias), sc, -m);
-        const uint64_t sc2 = f2pack(sc, sc), shift2 = f2pack(shift, shift);
-        uint64_t acc = f2pack(sum.x, sum.y);
+          for (int k = 1; k < 31; k += 2) pm = fmaxf(fmaxf(pm, __uint_as_float(v[k])), __uint_as_float(v[k + 1]));
+          pm = fmaxf(pm, __uint_as_float(v[31]));
+          return on ? fmaxf((pm + __uint_as_float(bg)) * sc, kFloor) : kFloor;
+        };
+        if (g == 0 && i == 0) m = seen_max() + kMargin;
         uint32_t P[16], rest[16];
-        if (off == 0) {
+        float2 add;
+        for (;;) {
+          // p with the maximum as it stands, while the page's own comes in; kept unless that
+          // passes the slack
+          const float mx = seen_max();
+          const float shift = fmaf(__uint_as_float(bg), sc, -m);
+          const uint64_t sc2 = f2pack(sc, sc), shift2 = f2pack(shift, shift);
+          uint64_t acc = 0;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             uint64_t e2;
-            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(pair64(x[2 * k], x[2 * k + 1])), "l"(sc2), "l"(shift2));
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(pair64(v[2 * k], v[2 * k + 1])), "l"(sc2), "l"(shift2));
             float e0, e1;
             f2unpack(e2, e0, e1);
             e0 = ex2a(e0);
             e1 = ex2a(e1);
+            if (off != 0) {  // a mixed page (the whole warp): what a row does not see may hold anything
+              e0 = on ? e0 : 0.f;
+              e1 = on ? e1 : 0.f;
+            }
             if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
             P[k] = pack_probs<F>(e0, e1, rest[k]);
           }
-        } else {  // a mixed page: what a row does not see may hold anything
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float e0 = on ? ex2a(fmaf(__uint_as_float(x[2 * k]), sc, shift)) : 0.f;
-            const float e1 = on ? ex2a(fmaf(__uint_as_float(x[2 * k + 1]), sc, shift)) : 0.f;
-            if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
-            P[k] = pack_probs<F>(e0, e1, rest[k]);
-          }
+          f2unpack(acc, add.x, add.y);
+          if (__builtin_expect(!__any_sync(0xFFFFFFFFu, mx > m + kSlack), 1)) break;
+          // each row by its own maximum: what it gives does not depend on its neighbours'
+          const float nm = mx > m + kSlack ? mx + kMargin : m, f = nm > m ? ex2a(m - nm) : 1.f;
+          if (g + 1 < F::kPages) tmem_wait_ld(x[(g + 1) & 1]);
+          rescale_row<F>(O, S, g, i > 0, f);
+          sum = make_float2(sum.x * f, sum.y * f);
+          m = nm;
+          tmem_ld32(S + 32 * g, v);
+          tmem_wait_ld(v);
         }
-        f2unpack(acc, sum.x, sum.y);
+        sum = make_float2(sum.x + add.x, sum.y + add.y);
         // over the page's own scores, which this thread has taken
         tmem_st16(S + 32 * g, P);
         if (F::kPair) tmem_st16(S + 32 * g + 16, rest);
@@ -636,92 +652,94 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     if (real)
       *reinterpret_cast<float2*>(p.ws + (part_row * p.slots + slot0) * kPartialFloats) = make_float2(ok && any ? m : -INFINITY, total);
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
-  } else if (wid == kMmaWarp) {
+  } else if (wid < kLoadWarp) {
     // =========================================================== products
+    // One warp a lane, so that one lane's waits do not hold up the other's products; the whole
+    // warp runs this and one elected lane issues, so that descriptors stay in uniform
+    // registers.  The lanes take turns, a step's products in one piece: one lane's scores are
+    // then done half a period before the other's, and its softmax runs beside the other's
+    // products (without turns the two fell into phase, products and softmax by turns: 5000
+    // cycles a tile).
     constexpr uint32_t qk = mma_desc(F::kBf16, false, F::kS), pv = mma_desc(F::kBf16, !F::kPacked, F::kO);
-    if (n > 0) {
-      // The whole warp runs this, one elected lane issues: descriptors stay in uniform registers.
-      const uint64_t qdesc = smem_desc(base, 16, 1024, kSwizzle128), kdesc = smem_desc(kst, 16, 1024, kSwizzle128);
-      const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
-      const int both_shift = both ? 1 : 0;
-      bool started[2] = {false, false};
-      // S of step s; `first`: no step before it has waited for its tile's Keys
-      auto scores = [&](int s, int a, bool first, bool last) -> bool {
-        const int tile = s >> both_shift, st = tile % kStages;
-        if (first && !wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
-        tc_fence_after();
-        const uint64_t qa = qdesc + a * (128 * 128 / 16), kb = kdesc + st * (F::kKBytes / 16);
-        const uint32_t d = s_col(a);
+    const int a = wid - kMmaWarp, both_shift = both ? 1 : 0;
+    const uint64_t qdesc = smem_desc(base + a * (128 * 128), 16, 1024, kSwizzle128), kdesc = smem_desc(kst, 16, 1024, kSwizzle128);
+    const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
+    const uint32_t scol = s_col(a), ocol = o_col(a);
+    bool started = false, ok = true;
+    // S of step s; then the operands of its tile, and of the step before on this lane, are free
+    auto scores = [&](int s) -> bool {
+      const int tile = s >> both_shift, st = tile % kStages;
+      if (!wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
+      tc_fence_after();
+      const uint64_t kb = kdesc + st * (F::kKBytes / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k)
+          mma_ss(scol, qdesc + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
+        mma_commit(smem_u32(&sh.bars.sfull[a]));
+        mma_commit(smem_u32(&sh.bars.kempty[st]));
+        if (s >= 2) mma_commit(smem_u32(&sh.bars.vempty[((s - 2) >> both_shift) % kStages]));
+      }
+      __syncwarp();
+      return true;
+    };
+    if (a < steps) ok = wait_phase(&sh.bars.qready[a], 0, p.wait_polls, abort) && scores(a);
+    for (int s = a; ok && s < steps; s += 2) {
+      const int tile = s >> both_shift, st = tile % kStages, page0 = (t0 + tile) * F::kPages;
+      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
+           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort) &&
+           (s == 0 || wait_phase(&sh.bars.turn[a], ((s - 1) >> 1) & 1, p.wait_polls, abort));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vb = vdesc + st * (F::kVBytes / 16);
+      if (page0 + F::kPages <= full_pages && *static_cast<volatile int*>(&sh.bad) == 0) {
+        // every row of the block sees every page of the tile
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kD / 16; ++k)
-            mma_ss(d, qa + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
-          mma_commit(smem_u32(&sh.bars.sfull[a]));
-          if (last) mma_commit(smem_u32(&sh.bars.kempty[st]));
+          for (int k = 0; k < 2 * F::kPages; ++k) {
+            const uint64_t vk = vb + (F::kPacked ? ((k >> 1) * F::kSlab + 32 * (k & 1)) / 16 : 16 * k * 128 / 16);
+            mma_ts(ocol, scol + 16 * k - 8 * (k & 1), vk, pv, started || k > 0);
+            if (F::kPair) mma_ts(ocol, scol + 16 * k - 8 * (k & 1) + 16, vk, pv, true);
+          }
         }
-        __syncwarp();
-        return true;
-      };
-      // O += P V of step s, then the scores of the lane's next tile
-      auto step = [&](int s, int a) -> bool {
-        const bool first = !both || a == 0, last = !both || a == 1;  // of the tile's uses
-        const int tile = s >> both_shift, st = tile % kStages, page0 = (t0 + tile) * F::kPages;
-        if (first && !wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
-        if (!wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort)) return false;
-        tc_fence_after();
-        const uint64_t vb = vdesc + st * (F::kVBytes / 16);
-        const uint32_t d = o_col(a), pcol = s_col(a);
-        if (page0 + F::kPages <= full_pages && *static_cast<volatile int*>(&sh.bad) == 0) {
-          // every row of the block sees every page of the tile
+        started = true;
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < F::kPages; ++g) {
+          const uint4 o4 = *reinterpret_cast<const uint4*>(sh.off[a][g]);
+          if (__any_sync(0xFFFFFFFFu, (o4.x & o4.y & o4.z & o4.w) == 0xFFFFFFFFu)) continue;  // no row sees it, or no page
+          const uint32_t off[4] = {o4.x, o4.y, o4.z, o4.w};
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 2 * F::kPages; ++k) {
-              const uint64_t vk = vb + (F::kPacked ? ((k >> 1) * F::kSlab + 32 * (k & 1)) / 16 : 16 * k * 128 / 16);
-              mma_ts(d, pcol + 16 * k - 8 * (k & 1), vk, pv, started[a] || k > 0);
-              if (F::kPair) mma_ts(d, pcol + 16 * k - 8 * (k & 1) + 16, vk, pv, true);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t pa = scol + 32 * g + 8 * k;
+              const uint64_t vk = vb + (F::kPacked ? (g * F::kSlab + 32 * k) / 16 : (32 * g + 16 * k) * 128 / 16);
+              mma_ts_masked(ocol, pa, vk, pv, started || k > 0, off);
+              if (F::kPair) mma_ts_masked(ocol, pa + 16, vk, pv, true, off);
             }
           }
-          started[a] = true;
-        } else {
-#pragma unroll 1
-          for (int g = 0; g < F::kPages; ++g) {
-            const uint4 o4 = *reinterpret_cast<const uint4*>(sh.off[a][g]);
-            if (__any_sync(0xFFFFFFFFu, (o4.x & o4.y & o4.z & o4.w) == 0xFFFFFFFFu)) continue;  // no row sees it, or no page
-            const uint32_t off[4] = {o4.x, o4.y, o4.z, o4.w};
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t pa = pcol + 32 * g + 8 * k;
-                const uint64_t vk = vb + (F::kPacked ? (g * F::kSlab + 32 * k) / 16 : (32 * g + 16 * k) * 128 / 16);
-                mma_ts_masked(d, pa, vk, pv, started[a] || k > 0, off);
-                if (F::kPair) mma_ts_masked(d, pa + 16, vk, pv, true, off);
-              }
-            }
-            __syncwarp();
-            started[a] = true;
-          }
+          __syncwarp();
+          started = true;
         }
-        const bool more = s + 2 < steps;
-        if (elect_one()) {
-          if (last) mma_commit(smem_u32(&sh.bars.vempty[st]));
-          if (!more) mma_commit(smem_u32(&sh.bars.ofull[a]));
-        }
+      }
+      if (s + 2 < steps) {
+        ok = scores(s + 2);
+        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
+      } else {
+        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
+        if (elect_one()) mma_commit(smem_u32(&sh.bars.ofull[a]));
         __syncwarp();
-        return !more || scores(s + 2, a, first, last);
-      };
-      bool ok = wait_phase(&sh.bars.qready, 0, p.wait_polls, abort) && scores(0, 0, true, !both) &&
-                (steps < 2 || scores(1, 1, !both, true));
-      for (int s = 0; ok && s < steps; s += 2) ok = step(s, 0) && (s + 1 >= steps || step(s + 1, 1));
-      if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
+      }
     }
+    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
   } else if constexpr (F::kPacked) {
     // =========================================================== packed pages
-    const int d = wid - kLoadWarp, g = d % F::kPages;
-    const bool values = d >= F::kPages;
+    const int d = wid - kLoadWarp, g = d % F::kPages, part = d / F::kPages;  // 0, 1: halves of the Keys
+    const bool values = part == 2, idle = part == 3;
     const uint32_t part_bytes = values ? F::kRawV : 512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi;
     const size_t part_off = values ? (size_t)(512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi) : 0;
-    const uint32_t raw0 = raws + (values ? F::kPages * F::kRaw * F::kRawK + g * F::kRaw * F::kRawV : g * F::kRaw * F::kRawK);
+    const uint32_t raw0 = raws + (values ? 2 * F::kPages * F::kRaw * F::kRawK + g * F::kRaw * F::kRawV : d * F::kRaw * F::kRawK);
     const uint32_t raw_stride = values ? F::kRawV : F::kRawK;
     int ids = -1, ids_at = -1000;  // lane l: the id of this warp's page of tile ids_at + l
     auto id_of = [&](int tile) {
@@ -749,8 +767,9 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     };
     uint32_t phases = 0;  // bit: phase parity that the slot's barrier completes next
     bool ok = true;
-    for (int tile = 0; tile < min(n, F::kRaw); ++tile) fetch(tile);
-    for (int tile = 0; tile < n; ++tile) {
+    const int mine = idle ? 0 : n;
+    for (int tile = 0; tile < min(mine, F::kRaw); ++tile) fetch(tile);
+    for (int tile = 0; tile < mine; ++tile) {
       const int slot = tile % F::kRaw, st = tile % kStages;
       const bool in = (staged >> slot) & 1u;
       if (in) {
@@ -764,9 +783,9 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       if (in) {
         const uint32_t raw = raw0 + slot * raw_stride;
         if (values) put_values<F>(raw, vst + st * F::kVBytes + g * F::kSlab, p.d_status);
-        else put_keys<F>(raw, kst + st * F::kKBytes, g, p.n_hi, p.d_status);
+        else put_keys<F>(raw, kst + st * F::kKBytes, g, part, p.n_hi, p.d_status);
       }
-      if (!values && lane == 0) {
+      if (part == 0 && lane == 0) {
         sh.valid[tile % kFlags][g] = in;
         if (!in) sh.bad = 1;
       }
@@ -821,17 +840,18 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
   __syncthreads();
   // after a wait that ran out: nothing may be in flight when the block's memory is given back
   if (*abort != 0 && elect_one()) {
-    if (wid == kMmaWarp) {
-      mma_commit(smem_u32(&sh.bars.drain));
-      mbar_wait_bounded(&sh.bars.drain, 0, kPrefixWaitPolls);
+    if (wid >= kMmaWarp && wid < kLoadWarp) {
+      mma_commit(smem_u32(&sh.bars.drain[wid - kMmaWarp]));
+      mbar_wait_bounded(&sh.bars.drain[wid - kMmaWarp], 0, kPrefixWaitPolls);
     } else if (!F::kPacked && wid >= kLoadWarp) {
       for (int k = max(0, loads - kStages); k < loads; ++k)
         mbar_wait_bounded(wid == kLoadWarp ? &sh.bars.kfull[k % kStages] : &sh.bars.vfull[k % kStages],
                           (k / kStages) & 1, kPrefixWaitPolls);
     }
   }
-  __syncwarp();
+  if (*abort != 0) __syncthreads();  // both lanes' products have ended
   if (wid == kMmaWarp) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
