@@ -105,9 +105,8 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int maxpages, minpages;          // that a row of the block sees
-  int bad;                         // a page id out of range so far
   int row[kRows];                  // partials' row (sequence, query head); -1: padding
-  uint8_t valid[kFlags][4];        // page ids in range, by tile
+  alignas(4) uint8_t valid[kFlags][4];  // page ids in range, by tile
   alignas(16) uint32_t off[2][4][4];  // by lane and page: rows that do not see it, 32 a word
 };
 
@@ -369,51 +368,6 @@ __device__ __forceinline__ uint32_t pack_probs(float e0, float e1, uint32_t& res
   return hi;
 }
 
-// The maximum of some row of the warp has passed the slack at page g of a tile: O (when some
-// tile has gone into it) and the tile's probabilities so far are scaled by the rows' f (1:
-// unchanged, bit for bit; else the probabilities are rounded once more).
-template <class F>
-__device__ __forceinline__ void rescale_row(uint32_t O, uint32_t S, int g, bool has_o, float f) {
-#pragma unroll 1
-  for (int c = has_o ? 0 : F::kO; c < F::kO; c += 16) {
-    uint32_t x[16];
-    tmem_ld16(O + c, x);
-    tmem_wait_ld(x);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-    tmem_st16(O + c, x);
-  }
-  tmem_wait_st();  // this thread's probabilities are written before they are read
-#pragma unroll 1
-  for (int j = 0; j < g; ++j) {
-    uint32_t x[16], y[16];
-    tmem_ld16(S + 32 * j, x);
-    tmem_wait_ld(x);
-    if (F::kPair) {
-      tmem_ld16(S + 32 * j + 16, y);
-      tmem_wait_ld(y);
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (f == 1.f) break;  // rewritten as they are
-      float2 v;
-      if (F::kBf16) {
-        v.x = __uint_as_float(x[k] << 16) + (F::kPair ? __uint_as_float(y[k] << 16) : 0.f);
-        v.y = __uint_as_float(x[k] & 0xFFFF0000u) + (F::kPair ? __uint_as_float(y[k] & 0xFFFF0000u) : 0.f);
-      } else {
-        v = __half22float2(bits_h2(x[k]));
-        if (F::kPair) {
-          const float2 r = __half22float2(bits_h2(y[k]));
-          v = make_float2(v.x + r.x, v.y + r.y);
-        }
-      }
-      x[k] = pack_probs<F>(v.x * f, v.y * f, y[k]);
-    }
-    tmem_st16(S + 32 * j, x);
-    if (F::kPair) tmem_st16(S + 32 * j + 16, y);
-  }
-}
-
 template <class F>
 __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const PrefixArgs p,
                                                                     const __grid_constant__ CUtensorMap map) {
@@ -451,7 +405,6 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     sh.abort = 0;
     sh.maxpages = 0;
     sh.minpages = p.n_prefix;
-    sh.bad = 0;
   }
   // ---- the rows: what each sees of the prefix, its partials' place
   const int in_unit = unit * kRows + (both ? tid : (tid & 127));  // row of the kv head
@@ -495,11 +448,15 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
   int loads = 0;  // 16-bit pages: tiles that this warp has requested
   auto s_col = [&](int a) { return tmem + (uint32_t)(a * F::kS); };
+  auto all_valid = [&](int tile) {
+    constexpr uint32_t mask = F::kPages == 4 ? 0x01010101u : 0x00010101u;
+    return (*reinterpret_cast<const volatile uint32_t*>(sh.valid[tile % kFlags]) & mask) == mask;
+  };
   auto o_col = [&](int a) { return tmem + (uint32_t)(2 * F::kS + a * F::kO); };
 
-  // five warpgroups at 96 registers: the two of the softmax take 128, the others 64
+  // five warpgroups at 96 registers: the two of the softmax take 136, the others 64
   if (F::kPacked) {
-    if (wid < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if (wid < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
   if (wid < kSoftmaxWarps) {
@@ -536,72 +493,87 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       }
       tc_fence_after();
       const int tile = both ? s >> 1 : s, page0 = (t0 + tile) * F::kPages;
-      uint32_t x[2][32], bias[2] = {0, 0};
-      auto load = [&](int g) {
-        if (F::kPacked) tmem_ld1(S + F::kTok + g, bias[g & 1]);
-        tmem_ld32(S + 32 * g, x[g & 1]);
-      };
-      load(0);
+      // the tile's scores, all at once, in registers
+      uint32_t x[F::kPages][32], bias[F::kPages];
 #pragma unroll
       for (int g = 0; g < F::kPages; ++g) {
-        uint32_t (&v)[32] = x[g & 1];
-        uint32_t& bg = bias[g & 1];
-        // the rows that do not see this page, for the products' masks
-        const bool on = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
-        any = any || on;
-        const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on);
-        if (lane == 0) sh.off[a][g][wid & 3] = off;
-        tmem_wait_ld(v);
-        if (F::kPacked) pin(bg);
-        if (g + 1 < F::kPages) load(g + 1);
-        auto seen_max = [&]() {  // this row's maximum on the page, scaled
-          float pm = __uint_as_float(v[0]);
+        if (F::kPacked) tmem_ld1(S + F::kTok + g, bias[g]);
+        else bias[g] = 0;
+        tmem_ld32(S + 32 * g, x[g]);
+      }
+      // the pages that this row sees; the rows that do not, for the products' masks
+      const bool full = page0 + F::kPages <= full_pages && all_valid(tile);
+      bool on[F::kPages];
 #pragma unroll
-          for (int k = 1; k < 31; k += 2) pm = fmaxf(fmaxf(pm, __uint_as_float(v[k])), __uint_as_float(v[k + 1]));
-          pm = fmaxf(pm, __uint_as_float(v[31]));
-          return on ? fmaxf((pm + __uint_as_float(bg)) * sc, kFloor) : kFloor;
-        };
-        if (g == 0 && i == 0) m = seen_max() + kMargin;
-        uint32_t P[16], rest[16];
-        float2 add;
-        for (;;) {
-          // p with the maximum as it stands, while the page's own comes in; kept unless that
-          // passes the slack
-          const float mx = seen_max();
-          const float shift = fmaf(__uint_as_float(bg), sc, -m);
-          const uint64_t sc2 = f2pack(sc, sc), shift2 = f2pack(shift, shift);
-          uint64_t acc = 0;
+      for (int g = 0; g < F::kPages; ++g) on[g] = true;
+      if (!full) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            uint64_t e2;
-            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(pair64(v[2 * k], v[2 * k + 1])), "l"(sc2), "l"(shift2));
-            float e0, e1;
-            f2unpack(e2, e0, e1);
-            e0 = ex2a(e0);
-            e1 = ex2a(e1);
-            if (off != 0) {  // a mixed page (the whole warp): what a row does not see may hold anything
-              e0 = on ? e0 : 0.f;
-              e1 = on ? e1 : 0.f;
-            }
-            if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
-            P[k] = pack_probs<F>(e0, e1, rest[k]);
-          }
-          f2unpack(acc, add.x, add.y);
-          if (__builtin_expect(!__any_sync(0xFFFFFFFFu, mx > m + kSlack), 1)) break;
-          // each row by its own maximum: what it gives does not depend on its neighbours'
-          const float nm = mx > m + kSlack ? mx + kMargin : m, f = nm > m ? ex2a(m - nm) : 1.f;
-          if (g + 1 < F::kPages) tmem_wait_ld(x[(g + 1) & 1]);
-          rescale_row<F>(O, S, g, i > 0, f);
-          sum = make_float2(sum.x * f, sum.y * f);
-          m = nm;
-          tmem_ld32(S + 32 * g, v);
-          tmem_wait_ld(v);
+        for (int g = 0; g < F::kPages; ++g) {
+          on[g] = page0 + g < my_pages && sh.valid[tile % kFlags][g] != 0;
+          const uint32_t off = __ballot_sync(0xFFFFFFFFu, !on[g]);
+          if (lane == 0) sh.off[a][g][wid & 3] = off;
+          any = any || on[g];
         }
-        sum = make_float2(sum.x + add.x, sum.y + add.y);
+      } else {
+        any = true;
+      }
+#pragma unroll
+      for (int g = 0; g < F::kPages; ++g) {
+        tmem_wait_ld(x[g]);
+        if (F::kPacked) pin(bias[g]);
+      }
+      float mx = kFloor;  // this row's maximum, scaled
+#pragma unroll
+      for (int g = 0; g < F::kPages; ++g) {
+        float pm = fmaxf(__uint_as_float(x[g][0]), __uint_as_float(x[g][1]));
+#pragma unroll
+        for (int k = 2; k < 32; k += 2) pm = fmaxf(fmaxf(pm, __uint_as_float(x[g][k])), __uint_as_float(x[g][k + 1]));
+        pm = (pm + __uint_as_float(bias[g])) * sc;
+        mx = fmaxf(mx, full || on[g] ? pm : kFloor);
+      }
+      if (i == 0) {
+        m = mx + kMargin;
+      } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+        // each row by its own maximum: what it gives does not depend on its neighbours'
+        const float nm = mx > m + kSlack ? mx + kMargin : m, f = nm > m ? ex2a(m - nm) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < F::kO; c += 16) {
+          uint32_t y[16];
+          tmem_ld16(O + c, y);
+          tmem_wait_ld(y);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+          tmem_st16(O + c, y);
+        }
+        sum = make_float2(sum.x * f, sum.y * f);
+        m = nm;
+      }
+      uint64_t acc = f2pack(sum.x, sum.y);
+#pragma unroll
+      for (int g = 0; g < F::kPages; ++g) {
+        const float shift = fmaf(__uint_as_float(bias[g]), sc, -m);
+        const uint64_t sc2 = f2pack(sc, sc), shift2 = f2pack(shift, shift);
+        uint32_t P[16], rest[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          uint64_t e2;
+          asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(pair64(x[g][2 * k], x[g][2 * k + 1])), "l"(sc2), "l"(shift2));
+          float e0, e1;
+          f2unpack(e2, e0, e1);
+          e0 = ex2a(e0);
+          e1 = ex2a(e1);
+          if (!full) {  // what a row does not see may hold anything
+            e0 = on[g] ? e0 : 0.f;
+            e1 = on[g] ? e1 : 0.f;
+          }
+          if (!F::kPacked) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(f2pack(e0, e1)));
+          P[k] = pack_probs<F>(e0, e1, rest[k]);
+        }
         // over the page's own scores, which this thread has taken
         tmem_st16(S + 32 * g, P);
         if (F::kPair) tmem_st16(S + 32 * g + 16, rest);
       }
+      f2unpack(acc, sum.x, sum.y);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_s(smem_u32(&sh.bars.pready[a]));
@@ -666,33 +638,39 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
     const uint32_t scol = s_col(a), ocol = o_col(a);
     bool started = false, ok = true;
-    // S of step s; then the operands of its tile, and of the step before on this lane, are free
-    auto scores = [&](int s) -> bool {
-      const int tile = s >> both_shift, st = tile % kStages;
-      if (!wait_phase(&sh.bars.kfull[st], (tile / kStages) & 1, p.wait_polls, abort)) return false;
-      tc_fence_after();
-      const uint64_t kb = kdesc + st * (F::kKBytes / 16);
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kD / 16; ++k)
-          mma_ss(scol, qdesc + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
-        mma_commit(smem_u32(&sh.bars.sfull[a]));
-        mma_commit(smem_u32(&sh.bars.kempty[st]));
-        if (s >= 2) mma_commit(smem_u32(&sh.bars.vempty[((s - 2) >> both_shift) % kStages]));
-      }
-      __syncwarp();
-      return true;
+    auto keys_ready = [&](int s) {
+      const int tile = s >> both_shift;
+      return wait_phase(&sh.bars.kfull[tile % kStages], (tile / kStages) & 1, p.wait_polls, abort);
     };
-    if (a < steps) ok = wait_phase(&sh.bars.qready[a], 0, p.wait_polls, abort) && scores(a);
+    // S of step s, by the elected lane; then the operands of its tile's Keys, and of the
+    // Values of the step before on this lane, are free
+    auto scores = [&](int s) {
+      const int st = (s >> both_shift) % kStages;
+      const uint64_t kb = kdesc + st * (F::kKBytes / 16);
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k)
+        mma_ss(scol, qdesc + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
+      mma_commit(smem_u32(&sh.bars.sfull[a]));
+      mma_commit(smem_u32(&sh.bars.kempty[st]));
+      if (s >= 2) mma_commit(smem_u32(&sh.bars.vempty[((s - 2) >> both_shift) % kStages]));
+    };
+    if (a < steps) {
+      ok = wait_phase(&sh.bars.qready[a], 0, p.wait_polls, abort) && keys_ready(a);
+      tc_fence_after();
+      if (ok && elect_one()) scores(a);
+      __syncwarp();
+    }
     for (int s = a; ok && s < steps; s += 2) {
       const int tile = s >> both_shift, st = tile % kStages, page0 = (t0 + tile) * F::kPages;
-      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) &&
-           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort) &&
-           (s == 0 || wait_phase(&sh.bars.turn[a], ((s - 1) >> 1) & 1, p.wait_polls, abort));
+      const bool more = s + 2 < steps;
+      // the probabilities last: all the rest is there before them as a rule
+      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) && (!more || keys_ready(s + 2)) &&
+           (s == 0 || wait_phase(&sh.bars.turn[a], ((s - 1) >> 1) & 1, p.wait_polls, abort)) &&
+           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vb = vdesc + st * (F::kVBytes / 16);
-      if (page0 + F::kPages <= full_pages && *static_cast<volatile int*>(&sh.bad) == 0) {
+      if (page0 + F::kPages <= full_pages && all_valid(tile)) {
         // every row of the block sees every page of the tile
         if (elect_one()) {
 #pragma unroll
@@ -701,6 +679,9 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
             mma_ts(ocol, scol + 16 * k - 8 * (k & 1), vk, pv, started || k > 0);
             if (F::kPair) mma_ts(ocol, scol + 16 * k - 8 * (k & 1) + 16, vk, pv, true);
           }
+          if (more) scores(s + 2);
+          else mma_commit(smem_u32(&sh.bars.ofull[a]));
+          mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
         }
         started = true;
       } else {
@@ -721,15 +702,13 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
           __syncwarp();
           started = true;
         }
+        if (elect_one()) {
+          if (more) scores(s + 2);
+          else mma_commit(smem_u32(&sh.bars.ofull[a]));
+          mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
+        }
       }
-      if (s + 2 < steps) {
-        ok = scores(s + 2);
-        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
-      } else {
-        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
-        if (elect_one()) mma_commit(smem_u32(&sh.bars.ofull[a]));
-        __syncwarp();
-      }
+      __syncwarp();
     }
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
@@ -785,10 +764,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
         if (values) put_values<F>(raw, vst + st * F::kVBytes + g * F::kSlab, p.d_status);
         else put_keys<F>(raw, kst + st * F::kKBytes, g, part, p.n_hi, p.d_status);
       }
-      if (part == 0 && lane == 0) {
-        sh.valid[tile % kFlags][g] = in;
-        if (!in) sh.bad = 1;
-      }
+      if (part == 0 && lane == 0) sh.valid[tile % kFlags][g] = in;
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
@@ -817,10 +793,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       const int count = __popc(__ballot_sync(0xFFFFFFFFu, in));
       const uint32_t bar = smem_u32(&full[st]);
       if (lane < F::kPages) {
-        if (!values) {
-          sh.valid[tile % kFlags][lane] = in;
-          if (!in) sh.bad = 1;
-        }
+        if (!values) sh.valid[tile % kFlags][lane] = in;
         if (!in && page < page_end) set_status(p.d_status, KITTY_ST_BAD_PAGE);
       }
       __syncwarp();  // the flags, before the arrival that publishes them
