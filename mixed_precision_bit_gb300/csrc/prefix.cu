@@ -86,7 +86,7 @@ struct PlainFmt {
   static constexpr bool kPacked = false, kBf16 = BF, kPair = true;
   static constexpr int kPages = 4, kTok = 128, kS = 128, kO = 128;
   static constexpr int kKHalf = kTok * 128, kKBytes = 2 * kKHalf, kVBytes = kKBytes;
-  static constexpr int kSlab = 0, kLoadWarps = 2, kRawBytes = 0;
+  static constexpr int W = 0, kSlab = 0, kLoadWarps = 2, kRaw = 1, kRawK = 0, kRawV = 0, kRawBytes = 0;
 };
 
 template <class F>
@@ -97,7 +97,7 @@ __host__ __device__ constexpr int smem_of() { return 1024 + kQBytes + kStages * 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
   uint64_t sfull[2], pready[2], ofull[2], qready[2], drain[2], turn[2];
-  uint64_t raw[9][2];
+  uint64_t raw[9][2], based[3];
 };
 
 struct Shared {
@@ -183,8 +183,10 @@ __device__ __forceinline__ bool step_too_large(uint32_t pair) {
 // list) to rows 32 page .. of the stage, and their minima to row kTok + page.  Lane (r, qq)
 // holds tokens r, r + 8, r + 16, r + 24 of the channels 16j + 8h + 2qq + {0, 1}: pairs of
 // channels, and the eight rows of a warp's store lie in different swizzled 16-byte columns.
-template <class F>
-__device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page, int half, int n_hi, int32_t* d_status) {
+// `based`: called between the base plane and the boosted channels; returns when both halves
+// are at that point (false: given up).
+template <class F, class Based>
+__device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page, int half, int n_hi, int32_t* d_status, Based based) {
   constexpr int W = F::W;
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
   const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
@@ -226,18 +228,18 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
     sts32(dst + m * 128 + (((lane >> 2) ^ (m & 7)) << 4) + 4 * (lane & 3), v);
     if (step_too_large<W>(lds32(ks + 2 * c))) set_status(d_status, KITTY_ST_RANGE);
   }
-  // Boosted channels of this half again, from both planes: step * high + step / 2^W * low.
-  // This lane's columns of the extra plane are pairs too, of any two channels (c0 < c1): their
-  // words of the base plane lie in the lanes of the same tokens.
+  if (n_hi == 0) return true;
+  if (!based()) return false;
+  // Boosted channels again, from both planes: step * high + step / 2^W * low.  This lane's
+  // columns of the extra plane are pairs too, of any two channels: their words of the base
+  // plane lie in the lanes of the same tokens.  The halves take alternate groups of 16.
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
   const uint32_t lo_plane = raw + 512 * W + 2 * W * nx * lane, hi_plane = raw + 64 * W * r;
-  __syncwarp();
+  const uint32_t row0 = stage + (32 * page + r) * 128 + 16 * r;
 #pragma unroll 1
-  for (int js = 0; js < nx; ++js) {
+  for (int js = half; js < nx; js += 2) {
     const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
-    const uint32_t outside = (half ? ~ids : ids) & 0x40404040u;  // channels of the other half
-    if (__all_sync(0xFFFFFFFFu, outside == 0x40404040u)) continue;  // the list ascends: most groups lie in one half
     uint32_t lo[2];
     lo[0] = lds32(lo_plane + 2 * W * js);
     lo[1] = W == 4 ? lds32(lo_plane + 2 * W * js + 4) : 0;
@@ -252,16 +254,15 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
         const uint32_t x = lds32(from + 4 * mt);
         hi[i][mt] = __funnelshift_r(x, x, (c & 8) + 16 * (c & 1));  // the channel's codes in the low half
       }
-      at[i] = row ^ ((2 * c) & 0x7Eu);
+      at[i] = (row0 ^ ((2 * c) & 0x7Eu)) + (c >> 6) * F::kKHalf;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t s = __byte_perm(st[2 * h], st[2 * h + 1], 0x5410), sl = h2mul(s, part);
-      const bool in0 = !((outside >> (16 * h)) & 0x40u), in1 = !((outside >> (16 * h + 8)) & 0x40u);
       auto put = [&](int tau, uint32_t ch, uint32_t cl) {
         const uint32_t v = h2_bits(__hfma2(bits_h2(ch), bits_h2(s), bits_h2(h2mul(cl, sl))));
-        if (in0) sts16(at[2 * h] + 1024 * tau, v);
-        if (in1) sts16(at[2 * h + 1] + 1024 * tau, v >> 16);
+        sts16(at[2 * h] + 1024 * tau, v);
+        sts16(at[2 * h + 1] + 1024 * tau, v >> 16);
       };
 #pragma unroll
       for (int mt = 0; mt < W / 2; ++mt) {
@@ -279,6 +280,7 @@ __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t stage, int page,
       }
     }
   }
+  return true;
 }
 
 // A page's Value part (staged at raw: plane, steps, minima) to its slab, channels as rows of
@@ -399,12 +401,49 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       mbar_init(&sh.bars.drain[i], 1);
       mbar_init(&sh.bars.turn[i], 1);
     }
-    for (int i = 0; i < 9; ++i)
-      for (int k = 0; k < 2; ++k) mbar_init(&sh.bars.raw[i][k], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&sh.bars.based[i], 2);
     fence_mbar_init();
     sh.abort = 0;
     sh.maxpages = 0;
     sh.minpages = p.n_prefix;
+  }
+  // ---- packed pages: what a loading warp takes, and its first copies, before anything else.
+  // Keys (two warps a page) go to three schedulers, two each, the Values to the fourth.
+  const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
+  const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
+  const int item = wid >= kLoadWarp ? (int)((0x8952741360ull >> (4 * (wid - kLoadWarp))) & 15) : 9;
+  const int lg = item % 3, part = item / 3;  // page of the tile; 0, 1: halves of the Keys, 2: Values, 3: none
+  const bool values = part == 2;
+  constexpr int kRaw = F::kRaw;
+  const uint32_t key_bytes = F::kPacked ? 512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi : 0;
+  const uint32_t part_bytes = values ? F::kRawV : key_bytes;
+  const uint32_t raw0 = raws + (values ? 2 * F::kPages * kRaw * F::kRawK + lg * kRaw * F::kRawV : item * kRaw * F::kRawK);
+  const uint32_t raw_stride = values ? F::kRawV : F::kRawK;
+  uint32_t staged = 0;       // bit: the slot holds (or awaits) a page
+  int ids = -1, ids_at = 0;  // lane l: the id of this warp's page of tile ids_at + l
+  auto fetch = [&](int tile) {
+    if (tile == 0 || tile - ids_at >= 32) {
+      ids_at = tile;
+      const int page = (t0 + tile + lane) * F::kPages + lg;
+      ids = t0 + tile + lane < t1 && page < p.n_prefix ? p.table[page] : -1;
+    }
+    const int id = __shfl_sync(0xFFFFFFFFu, ids, tile - ids_at), slot = tile % kRaw;
+    const bool in = id >= 0 && id < p.pool_pages;
+    if (lane == 0 && in) {
+      const uint32_t bar = smem_u32(&sh.bars.raw[item][slot]);
+      mbar_arrive_expect_tx_s(bar, part_bytes);
+      bulk_g2s_s(raw0 + slot * raw_stride, p.pool + ((size_t)id * p.Hkv + kvh) * p.blob + (values ? key_bytes : 0),
+                 part_bytes, bar);
+    }
+    staged = in ? staged | (1u << slot) : staged & ~(1u << slot);
+  };
+  if (F::kPacked && part < 3) {
+    if (lane == 0) {
+      for (int k = 0; k < kRaw; ++k) mbar_init(&sh.bars.raw[item][k], 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    for (int tile = 0; tile < min(t1 - t0, kRaw); ++tile) fetch(tile);
   }
   // ---- the rows: what each sees of the prefix, its partials' place
   const int in_unit = unit * kRows + (both ? tid : (tid & 127));  // row of the kv head
@@ -440,8 +479,6 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     page_end = __shfl_sync(0xFFFFFFFFu, sh.maxpages, 0);
     full_pages = __shfl_sync(0xFFFFFFFFu, sh.minpages, 0);
   }
-  const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
-  const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
   const int n = max(0, min(t1, (page_end + F::kPages - 1) / F::kPages) - t0);  // tiles of this block
   const int steps = both ? 2 * n : n;  // step s: lane s & 1, tile s / 2 or s
   const int slot0 = both ? split : 2 * split + (tid >> 7);
@@ -714,66 +751,49 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     __syncwarp();
   } else if constexpr (F::kPacked) {
     // =========================================================== packed pages
-    const int d = wid - kLoadWarp, g = d % F::kPages, part = d / F::kPages;  // 0, 1: halves of the Keys
-    const bool values = part == 2, idle = part == 3;
-    const uint32_t part_bytes = values ? F::kRawV : 512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi;
-    const size_t part_off = values ? (size_t)(512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi) : 0;
-    const uint32_t raw0 = raws + (values ? 2 * F::kPages * F::kRaw * F::kRawK + g * F::kRaw * F::kRawV : d * F::kRaw * F::kRawK);
-    const uint32_t raw_stride = values ? F::kRawV : F::kRawK;
-    int ids = -1, ids_at = -1000;  // lane l: the id of this warp's page of tile ids_at + l
-    auto id_of = [&](int tile) {
-      if (tile - ids_at >= 32 || tile < ids_at) {
-        ids_at = tile;
-        const int page = (t0 + tile + lane) * F::kPages + g;
-        ids = page < page_end ? p.table[page] : -1;
-      }
-      return __shfl_sync(0xFFFFFFFFu, ids, tile - ids_at);
-    };
-    uint32_t staged = 0;  // bit: the slot holds (or awaits) a page
-    auto fetch = [&](int tile) {
-      const int id = id_of(tile), slot = tile % F::kRaw;
-      const bool in = id >= 0 && id < p.pool_pages;
-      if (lane == 0) {
-        if (in) {
-          const uint32_t bar = smem_u32(&sh.bars.raw[d][slot]);
-          mbar_arrive_expect_tx_s(bar, part_bytes);
-          bulk_g2s_s(raw0 + slot * raw_stride, p.pool + ((size_t)id * p.Hkv + kvh) * p.blob + part_off, part_bytes, bar);
-        } else if ((t0 + tile) * F::kPages + g < page_end) {
-          set_status(p.d_status, KITTY_ST_BAD_PAGE);
-        }
-      }
-      staged = in ? staged | (1u << slot) : staged & ~(1u << slot);
-    };
     uint32_t phases = 0;  // bit: phase parity that the slot's barrier completes next
+    uint32_t based_phase = 0;
     bool ok = true;
-    const int mine = idle ? 0 : n;
-    for (int tile = 0; tile < min(mine, F::kRaw); ++tile) fetch(tile);
-    for (int tile = 0; tile < mine; ++tile) {
-      const int slot = tile % F::kRaw, st = tile % kStages;
-      const bool in = (staged >> slot) & 1u;
+    for (int tile = 0; ok && tile < (part < 3 ? n : 0); ++tile) {
+      const int slot = tile % kRaw, st = tile % kStages;
+      const bool seen = (t0 + tile) * F::kPages + lg < page_end;
+      bool in = (staged >> slot) & 1u;
       if (in) {
-        ok = wait_phase(&sh.bars.raw[d][slot], (phases >> slot) & 1u, p.wait_polls, abort);
+        ok = wait_phase(&sh.bars.raw[item][slot], (phases >> slot) & 1u, p.wait_polls, abort);
         if (!ok) break;
         phases ^= 1u << slot;
         staged &= ~(1u << slot);
+      } else if (seen && part == 0 && lane == 0) {
+        set_status(p.d_status, KITTY_ST_BAD_PAGE);
       }
+      in = in && seen;
       ok = wait_phase(values ? &sh.bars.vempty[st] : &sh.bars.kempty[st], ((tile / kStages) & 1) ^ 1, p.wait_polls, abort);
       if (!ok) break;
+      auto based = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.based[lg]));
+        return wait_phase(&sh.bars.based[lg], based_phase, p.wait_polls, abort);
+      };
       if (in) {
         const uint32_t raw = raw0 + slot * raw_stride;
-        if (values) put_values<F>(raw, vst + st * F::kVBytes + g * F::kSlab, p.d_status);
-        else put_keys<F>(raw, kst + st * F::kKBytes, g, part, p.n_hi, p.d_status);
+        if (values) {
+          put_values<F>(raw, vst + st * F::kVBytes + lg * F::kSlab, p.d_status);
+        } else {
+          ok = put_keys<F>(raw, kst + st * F::kKBytes, lg, part, p.n_hi, p.d_status, based);
+          based_phase ^= 1u;
+        }
+        if (!ok) break;
       }
-      if (part == 0 && lane == 0) sh.valid[tile % kFlags][g] = in;
+      if (part == 0 && lane == 0) sh.valid[tile % kFlags][lg] = in;
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
-      if (tile + F::kRaw < n) fetch(tile + F::kRaw);
+      if (tile + kRaw < t1 - t0) fetch(tile + kRaw);
     }
-    if (!ok && lane == 0) {
-      set_status(p.d_status, KITTY_ST_TIMEOUT);
-      for (int k = 0; k < F::kRaw; ++k)  // this warp's copies in flight
-        if ((staged >> k) & 1u) mbar_wait_bounded(&sh.bars.raw[d][k], (phases >> k) & 1u, kPrefixWaitPolls);
+    if (lane == 0) {
+      if (!ok) set_status(p.d_status, KITTY_ST_TIMEOUT);
+      for (int k = 0; k < kRaw; ++k)  // this warp's copies still in flight
+        if ((staged >> k) & 1u) mbar_wait_bounded(&sh.bars.raw[item][k], (phases >> k) & 1u, kPrefixWaitPolls);
     }
     __syncwarp();
   } else {
