@@ -75,7 +75,10 @@ struct PackedFmt {
   // block is five warpgroups
   static constexpr int kLoadWarps = 3 * kPages + 1;
   static constexpr int kRaw = W == 2 ? 2 : 1;                // staged page parts a warp
-  static constexpr int kRawK = 512 * W + 128 * 4 * W + 512 + 128;  // at n_hi = 128
+  // The base plane is staged in eight rows 16 bytes apart (row r: what lanes 4r .. 4r + 3
+  // take), so that lanes that read one word of different rows do not share a bank.
+  static constexpr int kRawRow = 64 * W + 16, kRawBase = 8 * kRawRow;
+  static constexpr int kRawK = kRawBase + 128 * 4 * W + 512 + 128;  // at n_hi = 128
   static constexpr int kRawV = 512 * V + 512;
   static constexpr int kRawBytes = kPages * kRaw * (2 * kRawK + kRawV);
 };
@@ -86,7 +89,7 @@ struct PlainFmt {
   static constexpr bool kPacked = false, kBf16 = BF, kPair = true;
   static constexpr int kPages = 4, kTok = 128, kS = 128, kO = 128;
   static constexpr int kKHalf = kTok * 128, kKBytes = 2 * kKHalf, kVBytes = kKBytes;
-  static constexpr int W = 0, kSlab = 0, kLoadWarps = 2, kRaw = 1, kRawK = 0, kRawV = 0, kRawBytes = 0;
+  static constexpr int W = 0, kSlab = 0, kLoadWarps = 2, kRaw = 1, kRawK = 0, kRawV = 0, kRawBytes = 0, kRawRow = 0, kRawBase = 0;
 };
 
 template <class F>
@@ -189,12 +192,12 @@ template <class F, class Based>
 __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page, int half, int n_hi, int32_t* d_status, Based based) {
   constexpr int W = F::W;
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
-  const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
+  const uint32_t ks = raw + F::kRawBase + 4 * W * n_hi, km = ks + 256, kch = km + 256;
   const uint32_t dst = stage + half * F::kKHalf, row = dst + (32 * page + r) * 128 + 16 * r;  // + swizzle
   uint32_t w[2 * W];  // this lane's words of the half: one (W = 2) or two a j
 #pragma unroll
   for (int i = 0; i < W / 2; ++i) {
-    const uint4 v = lds128(raw + 16 * W * lane + 8 * W * half + 16 * i);
+    const uint4 v = lds128(raw + F::kRawRow * r + 16 * W * qq + 8 * W * half + 16 * i);
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
     w[4 * i + 2] = v.z;
@@ -235,7 +238,7 @@ __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page,
   // plane lie in the lanes of the same tokens.  The halves take alternate groups of 16.
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
-  const uint32_t lo_plane = raw + 512 * W + 2 * W * nx * lane, hi_plane = raw + 64 * W * r;
+  const uint32_t lo_plane = raw + F::kRawBase + 2 * W * nx * lane, hi_plane = raw + F::kRawRow * r;
   const uint32_t row0 = stage + (32 * page + r) * 128 + 16 * r;
 #pragma unroll 1
   for (int js = half; js < nx; js += 2) {
@@ -284,7 +287,7 @@ __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page,
 }
 
 // A page's Value part (staged at raw: plane, steps, minima) to its slab, channels as rows of
-// 32 tokens, the four groups' minima as rows 128 .. 131.  (Rolled over the groups: loading
+// 32 tokens, the four groups' minima as rows 128 .. 131.  (Rolled over pairs of groups: loading
 // warps, softmax and products share one instruction cache; with everything unrolled the
 // first page of a block took 4000 to 8700 cycles, each later one 2200 to 3300.)
 template <class F>
@@ -294,29 +297,38 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
   const uint32_t vs = raw + 512 * V, vm = vs + 256;
   const uint32_t sw = (r >> 1) & 3;
 #pragma unroll 1
-  for (int G = 0; G < 4; ++G) {
-    const uint4 s4 = lds128(vs + 64 * G + 16 * qq);
-    const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
-    uint32_t w[V];  // one (V = 2) or two a kt
+  for (int G0 = 0; G0 < 4; G0 += 2) {
+    uint32_t w[2 * V];  // of two groups: one (V = 2) or two a kt
 #pragma unroll
-    for (int i = 0; i < V; ++i) w[i] = lds32(raw + 16 * V * lane + 4 * V * G + 4 * i);
-    const uint32_t row = slab + (32 * G + r) * 64 + 16 * sw;
+    for (int i = 0; i < V / 2; ++i) {
+      const uint4 v = lds128(raw + 16 * V * lane + 4 * V * G0 + 16 * i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
+    for (int G = 0; G < 2; ++G) {
+      const uint4 s4 = lds128(vs + 64 * (G0 + G) + 16 * qq);
+      const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w};
+      const uint32_t row = slab + (32 * (G0 + G) + r) * 64 + 16 * sw;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t s = S[2 * kt + h], at = (row ^ (16 * (2 * kt + h))) + 4 * qq;
+      for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-        for (int mc = 0; mc < V / 2; ++mc) {
-          const uint32_t y = w[V / 2 * kt + mc], x = h ? __funnelshift_r(y, y, 8) : y;
-          if (V == 2) {
-            sts32(at, h2mul(codes<2, 0>(x), s));
-            sts32(at + 512, h2mul(codes<2, 1>(x), s));
-            sts32(at + 1024, h2mul(codes<2, 2>(x), s));
-            sts32(at + 1536, h2mul(codes<2, 3>(x), s));
-          } else {
-            sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
-            sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s = S[2 * kt + h], at = (row ^ (16 * (2 * kt + h))) + 4 * qq;
+#pragma unroll
+          for (int mc = 0; mc < V / 2; ++mc) {
+            const uint32_t y = w[V * G + V / 2 * kt + mc], x = h ? __funnelshift_r(y, y, 8) : y;
+            if (V == 2) {
+              sts32(at, h2mul(codes<2, 0>(x), s));
+              sts32(at + 512, h2mul(codes<2, 1>(x), s));
+              sts32(at + 1024, h2mul(codes<2, 2>(x), s));
+              sts32(at + 1536, h2mul(codes<2, 3>(x), s));
+            } else {
+              sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
+              sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
+            }
           }
         }
       }
@@ -429,11 +441,18 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     }
     const int id = __shfl_sync(0xFFFFFFFFu, ids, tile - ids_at), slot = tile % kRaw;
     const bool in = id >= 0 && id < p.pool_pages;
-    if (lane == 0 && in) {
-      const uint32_t bar = smem_u32(&sh.bars.raw[item][slot]);
-      mbar_arrive_expect_tx_s(bar, part_bytes);
-      bulk_g2s_s(raw0 + slot * raw_stride, p.pool + ((size_t)id * p.Hkv + kvh) * p.blob + (values ? key_bytes : 0),
-                 part_bytes, bar);
+    if (in) {
+      const uint32_t bar = smem_u32(&sh.bars.raw[item][slot]), to = raw0 + slot * raw_stride;
+      const uint8_t* from = p.pool + ((size_t)id * p.Hkv + kvh) * p.blob;
+      if (lane == 0) mbar_arrive_expect_tx_s(bar, part_bytes);
+      __syncwarp();
+      if (values) {
+        if (lane == 0) bulk_g2s_s(to, from + key_bytes, part_bytes, bar);
+      } else if (lane < 8) {  // the base plane's rows
+        bulk_g2s_s(to + lane * F::kRawRow, from + lane * 64 * F::W, 64 * F::W, bar);
+      } else if (lane == 8) {
+        bulk_g2s_s(to + F::kRawBase, from + 512 * F::W, part_bytes - 512 * F::W, bar);
+      }
     }
     staged = in ? staged | (1u << slot) : staged & ~(1u << slot);
   };
