@@ -71,16 +71,12 @@ struct PackedFmt {
   static constexpr int kKHalf = kS * 128, kKBytes = 2 * kKHalf;
   static constexpr int kSlab = kO * 64;   // a page's Values: [channel][64 bytes]
   static constexpr int kVBytes = kPages * kSlab;
-  // two warps for a page's Keys (64 channels each), one for its Values; one idle, so that the
-  // block is five warpgroups
+  // two warps for a page's Keys (64 channels each), one for its Values, and one that fetches
   static constexpr int kLoadWarps = 3 * kPages + 1;
-  static constexpr int kRaw = W == 2 ? 2 : 1;                // staged page parts a warp
-  // The base plane is staged in eight rows 16 bytes apart (row r: what lanes 4r .. 4r + 3
-  // take), so that lanes that read one word of different rows do not share a bank.
-  static constexpr int kRawRow = 64 * W + 16, kRawBase = 8 * kRawRow;
-  static constexpr int kRawK = kRawBase + 128 * 4 * W + 512 + 128;  // at n_hi = 128
+  static constexpr int kRaw = W == 2 ? 4 : 2;                // staged tiles
+  static constexpr int kRawK = 512 * W + 128 * 4 * W + 512 + 128;  // at n_hi = 128
   static constexpr int kRawV = 512 * V + 512;
-  static constexpr int kRawBytes = kPages * kRaw * (2 * kRawK + kRawV);
+  static constexpr int kRawBytes = kPages * kRaw * (kRawK + kRawV);
 };
 
 // 16-bit pages.
@@ -89,7 +85,7 @@ struct PlainFmt {
   static constexpr bool kPacked = false, kBf16 = BF, kPair = true;
   static constexpr int kPages = 4, kTok = 128, kS = 128, kO = 128;
   static constexpr int kKHalf = kTok * 128, kKBytes = 2 * kKHalf, kVBytes = kKBytes;
-  static constexpr int W = 0, kSlab = 0, kLoadWarps = 2, kRaw = 1, kRawK = 0, kRawV = 0, kRawBytes = 0, kRawRow = 0, kRawBase = 0;
+  static constexpr int W = 0, kSlab = 0, kLoadWarps = 2, kRaw = 1, kRawK = 0, kRawV = 0, kRawBytes = 0;
 };
 
 template <class F>
@@ -100,7 +96,7 @@ __host__ __device__ constexpr int smem_of() { return 1024 + kQBytes + kStages * 
 struct Bars {
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
   uint64_t sfull[2], pready[2], ofull[2], qready[2], drain[2], turn[2];
-  uint64_t raw[9][2], based[3];
+  uint64_t raw[6][4], freed[6][4], based[3];  // items: a tile's pages' Keys, then their Values
 };
 
 struct Shared {
@@ -109,15 +105,16 @@ struct Shared {
   int abort;
   int maxpages, minpages;          // that a row of the block sees
   int row[kRows];                  // partials' row (sequence, query head); -1: padding
+  uint8_t got[kFlags][4];               // packed pages that were fetched, by tile
   alignas(4) uint8_t valid[kFlags][4];  // page ids in range, by tile
   alignas(16) uint32_t off[2][4][4];  // by lane and page: rows that do not see it, 32 a word
 };
 
-// Whole warp: waits for a phase, at most `polls` polls; false when it, or another warp of
-// the block, has given up.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  bool done = false;
+// Whole warp: waits for each lane's phase (need: it has one), at most `polls` polls; false when
+// it, or another warp of the block, has given up.  Several barriers in one wait, a lane each,
+// cost no more than one: a wait that is over already takes 100 to 200 cycles.
+__device__ __forceinline__ bool wait_lanes(bool need, uint32_t a, uint32_t parity, uint32_t polls, volatile int* abort) {
+  bool done = !need;
   for (uint32_t i = 0;; ++i) {
     done = done || mbar_try(a, parity);
     if (__all_sync(0xFFFFFFFFu, done)) return true;
@@ -126,6 +123,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint3
   }
   *abort = 1;
   return false;
+}
+
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint32_t polls, volatile int* abort) {
+  return wait_lanes(true, smem_u32(bar), parity, polls, abort);
 }
 
 __device__ __forceinline__ float ex2a(float x) {
@@ -170,9 +171,9 @@ __device__ __forceinline__ uint32_t codes(uint32_t x) {
   constexpr int shift = BITS * K + 2;
   constexpr uint32_t mask = (((1u << BITS) - 1u) << shift) * 0x00010001u;
   const uint32_t y = (x & mask) | 0x64006400u;
-  const __half2 inv = __float2half2_rn(1.0f / (1 << shift));
-  const __half2 off = __float2half2_rn(-1024.0f / (1 << shift));
-  return h2_bits(__hfma2(bits_h2(y), inv, off));
+  constexpr uint32_t inv = ((15u - shift) << 10) * 0x00010001u;             // 2^-shift
+  constexpr uint32_t off = ((25u - shift) << 10 | 0x8000u) * 0x00010001u;  // -1024 * 2^-shift
+  return h2_bits(__hfma2(bits_h2(y), bits_h2(inv), bits_h2(off)));
 }
 
 // A stored step so large that a step times a code may leave fp16.
@@ -192,12 +193,12 @@ template <class F, class Based>
 __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page, int half, int n_hi, int32_t* d_status, Based based) {
   constexpr int W = F::W;
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
-  const uint32_t ks = raw + F::kRawBase + 4 * W * n_hi, km = ks + 256, kch = km + 256;
+  const uint32_t ks = raw + 512 * W + 4 * W * n_hi, km = ks + 256, kch = km + 256;
   const uint32_t dst = stage + half * F::kKHalf, row = dst + (32 * page + r) * 128 + 16 * r;  // + swizzle
   uint32_t w[2 * W];  // this lane's words of the half: one (W = 2) or two a j
 #pragma unroll
   for (int i = 0; i < W / 2; ++i) {
-    const uint4 v = lds128(raw + F::kRawRow * r + 16 * W * qq + 8 * W * half + 16 * i);
+    const uint4 v = lds128(raw + 16 * W * lane + 8 * W * half + 16 * i);
     w[4 * i] = v.x;
     w[4 * i + 1] = v.y;
     w[4 * i + 2] = v.z;
@@ -238,7 +239,7 @@ __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page,
   // plane lie in the lanes of the same tokens.  The halves take alternate groups of 16.
   const uint32_t part = W == 2 ? 0x34003400u : 0x2C002C00u;  // 1/4, 1/16
   const int nx = n_hi / 16;
-  const uint32_t lo_plane = raw + F::kRawBase + 2 * W * nx * lane, hi_plane = raw + F::kRawRow * r;
+  const uint32_t lo_plane = raw + 512 * W + 2 * W * nx * lane, hi_plane = raw + 64 * W * r;
   const uint32_t row0 = stage + (32 * page + r) * 128 + 16 * r;
 #pragma unroll 1
   for (int js = half; js < nx; js += 2) {
@@ -419,46 +420,54 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     sh.maxpages = 0;
     sh.minpages = p.n_prefix;
   }
-  // ---- packed pages: what a loading warp takes, and its first copies, before anything else.
-  // Keys (two warps a page) go to three schedulers, two each, the Values to the fourth.
+  // ---- packed pages: what a loading warp takes.  The two schedulers that issue products get
+  // a Key and a Value warp each, the others two Key warps and one more (measured against
+  // three other orders at 128 x 32768: 184.6 us a call, the others 187.6 to 197.3).
   const int tiles = (p.n_prefix + F::kPages - 1) / F::kPages;
   const int t0 = (int)((long)tiles * split / p.splits), t1 = (int)((long)tiles * (split + 1) / p.splits);
-  const int item = wid >= kLoadWarp ? (int)((0x8952741360ull >> (4 * (wid - kLoadWarp))) & 15) : 9;
-  const int lg = item % 3, part = item / 3;  // page of the tile; 0, 1: halves of the Keys, 2: Values, 3: none
+  const int role = wid >= kLoadWarp ? (int)((0x8930547621ull >> (4 * (wid - kLoadWarp))) & 15) : 12;
+  // page of the tile; 0, 1: halves of the Keys, 2: Values, 3: fetch, 4: not a loading warp
+  const int lg = role % 3, part = role / 3;
   const bool values = part == 2;
   constexpr int kRaw = F::kRaw;
   const uint32_t key_bytes = F::kPacked ? 512 * F::W + 4 * F::W * p.n_hi + 512 + p.n_hi : 0;
-  const uint32_t part_bytes = values ? F::kRawV : key_bytes;
-  const uint32_t raw0 = raws + (values ? 2 * F::kPages * kRaw * F::kRawK + lg * kRaw * F::kRawV : item * kRaw * F::kRawK);
-  const uint32_t raw_stride = values ? F::kRawV : F::kRawK;
-  uint32_t staged = 0;       // bit: the slot holds (or awaits) a page
-  int ids = -1, ids_at = 0;  // lane l: the id of this warp's page of tile ids_at + l
+  // item i of a slot: a page's Keys (i < 3) or Values
+  auto raw_at = [&](int i, int slot) {
+    return raws + (i < 3 ? (i * kRaw + slot) * F::kRawK : 3 * kRaw * F::kRawK + ((i - 3) * kRaw + slot) * F::kRawV);
+  };
+  uint32_t in_flight = 0;    // of this lane's item: bit: the slot awaits a copy
+  int ids = -1, ids_at = 0;  // lane l: the id of this lane's page of tile ids_at + l / 3
+  // The fetching warp: lane i < 6 requests item i of a tile, or arrives for it without one.
   auto fetch = [&](int tile) {
-    if (tile == 0 || tile - ids_at >= 32) {
+    if (tile == 0 || tile - ids_at >= 10) {
       ids_at = tile;
-      const int page = (t0 + tile + lane) * F::kPages + lg;
-      ids = t0 + tile + lane < t1 && page < p.n_prefix ? p.table[page] : -1;
+      const int t = t0 + tile + lane / 3, page = t * F::kPages + lane % 3;
+      ids = lane < 30 && t < t1 && page < p.n_prefix ? p.table[page] : -1;
     }
-    const int id = __shfl_sync(0xFFFFFFFFu, ids, tile - ids_at), slot = tile % kRaw;
+    const int id = __shfl_sync(0xFFFFFFFFu, ids, 3 * (tile - ids_at) + lane % 3), slot = tile % kRaw;
     const bool in = id >= 0 && id < p.pool_pages;
-    if (in) {
-      const uint32_t bar = smem_u32(&sh.bars.raw[item][slot]), to = raw0 + slot * raw_stride;
-      const uint8_t* from = p.pool + ((size_t)id * p.Hkv + kvh) * p.blob;
-      if (lane == 0) mbar_arrive_expect_tx_s(bar, part_bytes);
-      __syncwarp();
-      if (values) {
-        if (lane == 0) bulk_g2s_s(to, from + key_bytes, part_bytes, bar);
-      } else if (lane < 8) {  // the base plane's rows
-        bulk_g2s_s(to + lane * F::kRawRow, from + lane * 64 * F::W, 64 * F::W, bar);
-      } else if (lane == 8) {
-        bulk_g2s_s(to + F::kRawBase, from + 512 * F::W, part_bytes - 512 * F::W, bar);
+    if (lane < 3) sh.got[tile % kFlags][lane] = in;
+    __syncwarp();
+    if (lane < 6) {
+      const uint32_t bar = smem_u32(&sh.bars.raw[lane][slot]);
+      if (in) {
+        const uint32_t bytes = lane < 3 ? key_bytes : F::kRawV;
+        mbar_arrive_expect_tx_s(bar, bytes);
+        bulk_g2s_s(raw_at(lane, slot), p.pool + ((size_t)id * p.Hkv + kvh) * p.blob + (lane < 3 ? 0 : key_bytes), bytes, bar);
+        in_flight |= 1u << slot;
+      } else {
+        mbar_arrive_s(bar);
+        in_flight &= ~(1u << slot);
       }
     }
-    staged = in ? staged | (1u << slot) : staged & ~(1u << slot);
+    __syncwarp();
   };
-  if (F::kPacked && part < 3) {
-    if (lane == 0) {
-      for (int k = 0; k < kRaw; ++k) mbar_init(&sh.bars.raw[item][k], 1);
+  if (F::kPacked && part == 3) {  // the first copies, before anything else
+    if (lane < 6) {
+      for (int k = 0; k < kRaw; ++k) {
+        mbar_init(&sh.bars.raw[lane][k], 1);
+        mbar_init(&sh.bars.freed[lane][k], lane < 3 ? 2 : 1);
+      }
       fence_mbar_init();
     }
     __syncwarp();
@@ -694,24 +703,25 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     const uint64_t vdesc = F::kPacked ? smem_desc(vst, 16, 512, kSwizzle64) : smem_desc(vst, F::kKHalf, 1024, kSwizzle128);
     const uint32_t scol = s_col(a), ocol = o_col(a);
     bool started = false, ok = true;
-    auto keys_ready = [&](int s) {
-      const int tile = s >> both_shift;
-      return wait_phase(&sh.bars.kfull[tile % kStages], (tile / kStages) & 1, p.wait_polls, abort);
-    };
     // S of step s, by the elected lane; then the operands of its tile's Keys, and of the
     // Values of the step before on this lane, are free
     auto scores = [&](int s) {
       const int st = (s >> both_shift) % kStages;
       const uint64_t kb = kdesc + st * (F::kKBytes / 16);
 #pragma unroll
-      for (int k = 0; k < kD / 16; ++k)
+      for (int k = 0; k < kD / 16; ++k) {
+        // the other lane's turn, early enough that its products follow without a gap
+        if (k == kD / 32) mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
         mma_ss(scol, qdesc + (k >> 2) * (kQHalf / 16) + 2 * (k & 3), kb + (k >> 2) * (F::kKHalf / 16) + 2 * (k & 3), qk, k > 0);
+      }
       mma_commit(smem_u32(&sh.bars.sfull[a]));
       mma_commit(smem_u32(&sh.bars.kempty[st]));
       if (s >= 2) mma_commit(smem_u32(&sh.bars.vempty[((s - 2) >> both_shift) % kStages]));
     };
     if (a < steps) {
-      ok = wait_phase(&sh.bars.qready[a], 0, p.wait_polls, abort) && keys_ready(a);
+      const int tile = a >> both_shift;  // lane 1 after lane 0
+      ok = wait_lanes(lane < 2 + a, lane == 0 ? smem_u32(&sh.bars.qready[a]) : lane == 1 ? smem_u32(&sh.bars.kfull[tile]) : smem_u32(&sh.bars.turn[a]),
+                      0, p.wait_polls, abort);
       tc_fence_after();
       if (ok && elect_one()) scores(a);
       __syncwarp();
@@ -719,10 +729,11 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     for (int s = a; ok && s < steps; s += 2) {
       const int tile = s >> both_shift, st = tile % kStages, page0 = (t0 + tile) * F::kPages;
       const bool more = s + 2 < steps;
-      // the probabilities last: all the rest is there before them as a rule
-      ok = wait_phase(&sh.bars.vfull[st], (tile / kStages) & 1, p.wait_polls, abort) && (!more || keys_ready(s + 2)) &&
-           (s == 0 || wait_phase(&sh.bars.turn[a], ((s - 1) >> 1) & 1, p.wait_polls, abort)) &&
-           wait_phase(&sh.bars.pready[a], (s >> 1) & 1, p.wait_polls, abort);
+      // this step's probabilities and Values, and the turn (the other lane's arrivals: one with
+      // each of its scores, one with each end without)
+      const uint32_t bar = smem_u32(lane == 0 ? &sh.bars.pready[a] : lane == 1 ? &sh.bars.vfull[st] : &sh.bars.turn[a]);
+      const int phase = lane == 0 ? s >> 1 : lane == 1 ? tile / kStages : (s + a) >> 1;
+      ok = wait_lanes(lane < (steps > 1 ? 3 : 2), bar, phase & 1, p.wait_polls, abort);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vb = vdesc + st * (F::kVBytes / 16);
@@ -735,9 +746,6 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
             mma_ts(ocol, scol + 16 * k - 8 * (k & 1), vk, pv, started || k > 0);
             if (F::kPair) mma_ts(ocol, scol + 16 * k - 8 * (k & 1) + 16, vk, pv, true);
           }
-          if (more) scores(s + 2);
-          else mma_commit(smem_u32(&sh.bars.ofull[a]));
-          mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
         }
         started = true;
       } else {
@@ -758,9 +766,19 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
           __syncwarp();
           started = true;
         }
-        if (elect_one()) {
-          if (more) scores(s + 2);
-          else mma_commit(smem_u32(&sh.bars.ofull[a]));
+      }
+      __syncwarp();
+      if (more) {
+        const int next = (s + 2) >> both_shift;
+        ok = wait_phase(&sh.bars.kfull[next % kStages], (next / kStages) & 1, p.wait_polls, abort);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (elect_one()) {
+        if (more) {
+          scores(s + 2);
+        } else {
+          mma_commit(smem_u32(&sh.bars.ofull[a]));
           mbar_arrive_s(smem_u32(&sh.bars.turn[1 - a]));
         }
       }
@@ -770,50 +788,60 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     __syncwarp();
   } else if constexpr (F::kPacked) {
     // =========================================================== packed pages
-    uint32_t phases = 0;  // bit: phase parity that the slot's barrier completes next
-    uint32_t based_phase = 0;
     bool ok = true;
-    for (int tile = 0; ok && tile < (part < 3 ? n : 0); ++tile) {
-      const int slot = tile % kRaw, st = tile % kStages;
-      const bool seen = (t0 + tile) * F::kPages + lg < page_end;
-      bool in = (staged >> slot) & 1u;
-      if (in) {
-        ok = wait_phase(&sh.bars.raw[item][slot], (phases >> slot) & 1u, p.wait_polls, abort);
+    if (part == 3) {
+      int tile = min(t1 - t0, kRaw);
+      for (; tile < n; ++tile) {  // a slot is free when its item's readers are through
+        const int slot = tile % kRaw, turn = tile / kRaw - 1;
+        ok = wait_lanes(lane < 6, smem_u32(&sh.bars.freed[lane < 6 ? lane : 0][slot]), turn & 1, p.wait_polls, abort);
         if (!ok) break;
-        phases ^= 1u << slot;
-        staged &= ~(1u << slot);
-      } else if (seen && part == 0 && lane == 0) {
-        set_status(p.d_status, KITTY_ST_BAD_PAGE);
+        fetch(tile);
       }
-      in = in && seen;
-      ok = wait_phase(values ? &sh.bars.vempty[st] : &sh.bars.kempty[st], ((tile / kStages) & 1) ^ 1, p.wait_polls, abort);
-      if (!ok) break;
-      auto based = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.based[lg]));
-        return wait_phase(&sh.bars.based[lg], based_phase, p.wait_polls, abort);
-      };
-      if (in) {
-        const uint32_t raw = raw0 + slot * raw_stride;
-        if (values) {
-          put_values<F>(raw, vst + st * F::kVBytes + lg * F::kSlab, p.d_status);
-        } else {
-          ok = put_keys<F>(raw, kst + st * F::kKBytes, lg, part, p.n_hi, p.d_status, based);
-          based_phase ^= 1u;
-        }
-        if (!ok) break;
-      }
-      if (part == 0 && lane == 0) sh.valid[tile % kFlags][lg] = in;
-      fence_async_shared();
+      // copies that nobody waited for: after a wait that ran out, or past the last seen page
+      if (lane < 6)
+        for (int k = 0; k < kRaw; ++k)
+          if ((in_flight >> k) & 1u) {
+            const int last = (tile - 1 - k) / kRaw;  // the slot's latest use
+            mbar_wait_bounded(&sh.bars.raw[lane][k], last & 1, kPrefixWaitPolls);
+          }
       __syncwarp();
-      if (lane == 0) mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
-      if (tile + kRaw < t1 - t0) fetch(tile + kRaw);
+    } else {
+      uint32_t based_phase = 0;
+      for (int tile = 0; tile < n; ++tile) {
+        const int slot = tile % kRaw, st = tile % kStages, item = values ? 3 + lg : lg;
+        const bool seen = (t0 + tile) * F::kPages + lg < page_end;
+        // the staged page, and the stage's last readers
+        const uint32_t empty = smem_u32(values ? &sh.bars.vempty[st] : &sh.bars.kempty[st]);
+        ok = wait_lanes(lane < 2, lane == 0 ? smem_u32(&sh.bars.raw[item][slot]) : empty,
+                        lane == 0 ? (tile / kRaw) & 1 : ((tile / kStages) & 1) ^ 1, p.wait_polls, abort);
+        if (!ok) break;
+        const bool got = sh.got[tile % kFlags][lg] != 0, in = got && seen;
+        if (!got && seen && part == 0 && lane == 0) set_status(p.d_status, KITTY_ST_BAD_PAGE);
+        auto based = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_s(smem_u32(&sh.bars.based[lg]));
+          return wait_phase(&sh.bars.based[lg], based_phase, p.wait_polls, abort);
+        };
+        if (in) {
+          const uint32_t raw = raw_at(item, slot);
+          if (values) {
+            put_values<F>(raw, vst + st * F::kVBytes + lg * F::kSlab, p.d_status);
+          } else {
+            ok = put_keys<F>(raw, kst + st * F::kKBytes, lg, part, p.n_hi, p.d_status, based);
+            based_phase ^= 1u;
+          }
+          if (!ok) break;
+        }
+        if (part == 0 && lane == 0) sh.valid[tile % kFlags][lg] = in;
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_s(smem_u32(values ? &sh.bars.vfull[st] : &sh.bars.kfull[st]));
+          mbar_arrive_s(smem_u32(&sh.bars.freed[item][slot]));
+        }
+      }
     }
-    if (lane == 0) {
-      if (!ok) set_status(p.d_status, KITTY_ST_TIMEOUT);
-      for (int k = 0; k < kRaw; ++k)  // this warp's copies still in flight
-        if ((staged >> k) & 1u) mbar_wait_bounded(&sh.bars.raw[item][k], (phases >> k) & 1u, kPrefixWaitPolls);
-    }
+    if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
   } else {
     // =========================================================== 16-bit pages
