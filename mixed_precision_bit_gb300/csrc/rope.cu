@@ -6,8 +6,7 @@
 // arithmetic (about ten operations a channel) is far below the memory rate; the
 // sines of a token are computed once, by one thread a pair, and shared by its heads
 // through shared memory.  One block takes a token: 16 lanes a row, so a row's sum of
-// squares is four shuffles, and a pair's partner is in the same lane or one shuffle
-// away.
+// squares is four shuffles, and both channels of a pair are in one lane.
 #include "rope.cuh"
 #include "grid_dep.cuh"
 #include "host_common.h"
@@ -18,10 +17,24 @@
 namespace kitty {
 namespace {
 
+// A token's block: many tokens take 64 threads with five rows a 16-lane group in flight (40
+// query and key rows in two rounds, 16 blocks an SM), few tokens 256 threads with three (48
+// rows in one round: the shortest block).  Measured, us: 8192 tokens of 40 rows 32.9 against 48.6
+// (128 threads: 35.0 to 39.1), 64 tokens 4.9 against 3.2; 8180 appended tokens of 48 rows 43.8
+// against 58.8, 64 tokens 7.7 against 4.5.
+struct ManyTokens {
+  static constexpr int kThreads = 64, kAhead = 5, kBlocks = 16;
+};
+struct FewTokens {
+  static constexpr int kThreads = 256, kAhead = 3, kBlocks = 3;
+};
+// Many: more tokens than two large blocks an SM.
+inline bool many_tokens(int n) { return n > 2 * sm_count(); }
+
 // Queries and keys of token blockIdx.x, out of place or in place (a lane writes only
-// the channels that it read, after its row's shuffles).
-template <int DT>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(
+// the channels that it read).
+template <int DT, class B>
+__global__ void __launch_bounds__(B::kThreads, B::kBlocks) norm_rope_kernel(
     const RopeParams p, const uint16_t* q, size_t q_stride, const uint16_t* k, size_t k_stride,
     const int32_t* positions, uint16_t* qo, size_t qo_stride, uint16_t* ko, size_t ko_stride,
     int H1, int H2) {
@@ -29,11 +42,12 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(
   const size_t t = blockIdx.x;
   TokenRows rows = {q + t * q_stride, k + t * k_stride, nullptr, qo + t * qo_stride,
                     ko + t * ko_stride, nullptr, kD, H1, H2};
-  uint4 x[kRopeAhead];
-  rope_load(rows, 0, x);
+  RopeLane L = rope_lane(p);
+  uint4 x[B::kAhead];
+  rope_load<B::kThreads>(rows, L, 0, x);
   rope_angles(p, positions[t], cs);
   __syncthreads();
-  rope_token<DT>(p, cs, rows, x);
+  rope_token<DT, B::kThreads>(p, L, cs, rows, x);
 }
 
 // The 16-bit page blob of one (page, kv head): K [32][128] then V [32][128].
@@ -68,22 +82,22 @@ __device__ __forceinline__ int length_before(const Append16& p, int b, int n, bo
 
 // Token blockIdx.x.  The new tokens' own page ids come from new_page_ids (entry of the
 // token that begins the page), so no block depends on another's block-table write.
-template <int DT>
-__global__ void __launch_bounds__(kRopeThreads) f16kv_append_rope_kernel(const Append16 p) {
+template <int DT, class B>
+__global__ void __launch_bounds__(B::kThreads, B::kBlocks) f16kv_append_rope_kernel(const Append16 p) {
   __shared__ float2 cs[kD / 2];
   grid_trigger();
   const int t = blockIdx.x;
   TokenRows rows = {p.q + (size_t)t * p.q_stride, p.k + (size_t)t * p.k_stride,
                     p.v + (size_t)t * p.v_stride, p.qo + (size_t)t * p.qo_stride, nullptr, nullptr,
                     kBlob16, p.qo != nullptr ? p.Hq : 0, p.Hkv};
-  uint4 x[kRopeAhead];
-  rope_load(rows, 0, x);
+  RopeLane L = rope_lane(p.rope);
+  uint4 x[B::kAhead];
+  rope_load<B::kThreads>(rows, L, 0, x);
   int b = t, first = t, n = 1;
   if (p.seq_start != nullptr) {
-    // b = sequences that end at or before token t: one load a thread for up to 128
-    // sequences
+    // b = sequences that end at or before token t: one load a thread a round
     b = 0;
-    for (int s0 = 0; s0 < p.B; s0 += kRopeThreads) {
+    for (int s0 = 0; s0 < p.B; s0 += B::kThreads) {
       const int s = s0 + threadIdx.x;
       b += __syncthreads_count(s < p.B && p.seq_start[s + 1] <= t);
     }
@@ -109,7 +123,7 @@ __global__ void __launch_bounds__(kRopeThreads) f16kv_append_rope_kernel(const A
   __syncthreads();  // the angles; and every thread has read the length
   rows.ko = p.pool + (size_t)id * p.Hkv * kBlob16 + (size_t)slot * kD;
   rows.vo = rows.ko + (size_t)kPage * kD;
-  rope_token<DT>(p.rope, cs, rows, x);
+  rope_token<DT, B::kThreads>(p.rope, L, cs, rows, x);
   if (p.seq_start == nullptr && !p.counted && threadIdx.x == 0) {
     // this block is all of the sequence's append
     if (slot == 0) p.block_table[(size_t)b * p.max_pages + page] = id;
@@ -163,7 +177,6 @@ struct AppendTail {
 // rules are those of the append without rotation.
 template <int DT, int W, int V>
 __global__ void __launch_bounds__(kQThreads) append_rope_kernel(const AppendTail p) {
-  static_assert(kQThreads == kRopeThreads, "one block does both");
   __shared__ QuantSmem sm;
   __shared__ float2 cs[kD / 2];
   grid_trigger();
@@ -174,8 +187,9 @@ __global__ void __launch_bounds__(kQThreads) append_rope_kernel(const AppendTail
                     p.v + (size_t)b * p.v_stride + (size_t)h * kD,
                     p.qo + (size_t)b * p.qo_stride + (size_t)h * g * kD, nullptr, nullptr, 0,
                     p.qo != nullptr ? g : 0, 1};
-  uint4 x[kRopeAhead];
-  rope_load(rows, 0, x);
+  RopeLane L = rope_lane(p.rope);
+  uint4 x[2];  // 16 rows a round: a group of up to 14 query heads
+  rope_load<kQThreads>(rows, L, 0, x);
   const int fid = p.flush_page_ids[b];
   int len = p.tail_len[b], np = p.num_pages[b];
   if (p.counted) {  // the lengths count the new token: undo that
@@ -198,7 +212,7 @@ __global__ void __launch_bounds__(kQThreads) append_rope_kernel(const AppendTail
   const size_t sh = (size_t)b * p.Hkv + h;
   rows.ko = p.tail_k + (sh * kPage + len) * kD;
   rows.vo = p.tail_v + (sh * kPage + len) * kD;
-  rope_token<DT>(p.rope, cs, rows, x);
+  rope_token<DT, kQThreads>(p.rope, L, cs, rows, x);
   const int n = len + 1;
   if (fid >= 0 && n < kPage) {
     if (c == 0) set_status(p.d_status, KITTY_ST_BAD_FLUSH);
@@ -286,14 +300,15 @@ extern "C" int kitty_norm_rope(const kitty_cfg* cfg, const kitty_rope* rope, con
   if (!positions || (!q && !k) || (q && (!rows_ok(q, q_stride, Hq) || !rows_ok(q_out, q_out_stride, Hq))) ||
       (k && (!rows_ok(k, k_stride, Hkv) || !rows_ok(k_out, k_out_stride, Hkv))))
     return KITTY_ERR_INVALID_ARG;
+  const bool many = many_tokens(n_tokens), bf = cfg->in_dtype == KITTY_BF16;
   auto launch = [&](auto kernel) {
-    kernel<<<(unsigned)n_tokens, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+    kernel<<<(unsigned)n_tokens, many ? ManyTokens::kThreads : FewTokens::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
         p, static_cast<const uint16_t*>(q), (size_t)q_stride, static_cast<const uint16_t*>(k),
         (size_t)k_stride, positions, static_cast<uint16_t*>(q_out), (size_t)q_out_stride,
         static_cast<uint16_t*>(k_out), (size_t)k_out_stride, q ? Hq : 0, k ? Hkv : 0);
   };
-  if (cfg->in_dtype == KITTY_BF16) launch(norm_rope_kernel<KITTY_BF16>);
-  else launch(norm_rope_kernel<KITTY_F16>);
+  if (many) bf ? launch(norm_rope_kernel<KITTY_BF16, ManyTokens>) : launch(norm_rope_kernel<KITTY_F16, ManyTokens>);
+  else bf ? launch(norm_rope_kernel<KITTY_BF16, FewTokens>) : launch(norm_rope_kernel<KITTY_F16, FewTokens>);
   return cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
 }
 
@@ -340,8 +355,12 @@ extern "C" int kitty_f16kv_append_rope(const kitty_cfg* cfg, const kitty_rope* r
   p.Hkv = Hkv;
   p.counted = counted != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cfg->in_dtype == KITTY_BF16) f16kv_append_rope_kernel<KITTY_BF16><<<(unsigned)n_tokens, kRopeThreads, 0, s>>>(p);
-  else f16kv_append_rope_kernel<KITTY_F16><<<(unsigned)n_tokens, kRopeThreads, 0, s>>>(p);
+  const bool many = many_tokens(n_tokens), bf = cfg->in_dtype == KITTY_BF16;
+  auto launch = [&](auto kernel) {
+    kernel<<<(unsigned)n_tokens, many ? ManyTokens::kThreads : FewTokens::kThreads, 0, s>>>(p);
+  };
+  if (many) bf ? launch(f16kv_append_rope_kernel<KITTY_BF16, ManyTokens>) : launch(f16kv_append_rope_kernel<KITTY_F16, ManyTokens>);
+  else bf ? launch(f16kv_append_rope_kernel<KITTY_BF16, FewTokens>) : launch(f16kv_append_rope_kernel<KITTY_F16, FewTokens>);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && seq_start && !counted)
     e = launch_dependent(f16kv_append_rope_finish, dim3((unsigned)((B + 3) / 4)), 128, 0, s, p, (int)n_tokens);

@@ -22,7 +22,6 @@
 namespace kitty {
 
 constexpr int kRowLanes = 16;             // lanes of one head row, eight channels each
-constexpr int kRopeThreads = 128;         // eight rows at a time
 
 // A rotation as the kernels take it.
 struct RopeParams {
@@ -44,48 +43,38 @@ __device__ __forceinline__ void rope_angles(const RopeParams& p, int64_t positio
   }
 }
 
-// What a lane keeps for the rows it handles at one position: the coefficients of
-// its own channels and of each one's partner in its pair,
-//   y[i] = x[i] * c[i] + partner[i] * s[i],
-// and where the partners are.  Half layout: rot / 2 is a multiple of 8, so all eight
-// partners sit in one other lane of the row; interleaved: in the same lane.  Lanes
-// past the rotated channels pass theirs through.
+// What a lane of a row holds, so that both channels of a pair are its own and no rotation
+// needs a shuffle: four channels from c0 and four from c1.
+//   half layout   lanes below rot / 8: c0 = 4 lane, c1 = c0 + rot / 2 (pair i: c0 + i, c1 + i)
+//   interleaved   c0 = 8 lane, c1 = c0 + 4 (pairs c0, c0 + 1; c0 + 2, ..)
+// and the channels past rot, eight a lane, in the other lanes.  Rot is a multiple of 16,
+// so every four are 8-byte aligned.  c, s: the four pairs' coefficients.
 struct RopeLane {
-  float c[8], s[8];
-  int src;   // lane (of the warp) that holds the partners (half layout)
+  float c[4], s[4];
+  int c0, c1;
   bool on, interleaved;  // on: this lane's channels rotate
 };
 
-__device__ __forceinline__ RopeLane rope_lane(const RopeParams& p, const float2* cs) {
+// Where a lane's channels are (nothing of it depends on the position).
+__device__ __forceinline__ RopeLane rope_lane(const RopeParams& p) {
   RopeLane L;
-  const int lane = threadIdx.x & 31, ch = (lane & (kRowLanes - 1)) * 8;
+  const int lane = threadIdx.x & (kRowLanes - 1), h = p.rot / 2;
   L.interleaved = p.interleaved != 0;
-  L.src = lane;
-  L.on = ch < p.rot;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) L.c[i] = L.s[i] = 0.f;
-  if (L.on) {
-    const int h = p.rot / 2;
-    if (L.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 a = cs[(ch + i) / 2];
-        L.c[i] = L.c[i + 1] = a.x;
-        L.s[i] = -a.y;
-        L.s[i + 1] = a.y;
-      }
-    } else {
-      const bool first = ch < h;
-      L.src = first ? lane + h / 8 : lane - h / 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 a = cs[first ? ch + i : ch + i - h];
-        L.c[i] = a.x;
-        L.s[i] = first ? -a.y : a.y;
-      }
-    }
-  }
+  L.on = L.interleaved ? 8 * lane < p.rot : 4 * lane < h;
+  if (L.interleaved) L.c0 = 8 * lane;
+  else L.c0 = L.on ? 4 * lane : p.rot + 8 * (lane - h / 4);
+  L.c1 = !L.interleaved && L.on ? L.c0 + h : L.c0 + 4;
   return L;
+}
+
+// Its pairs' coefficients, from the block's table.
+__device__ __forceinline__ void rope_coefficients(RopeLane& L, const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = L.on ? cs[(L.interleaved ? L.c0 / 2 : L.c0) + i] : make_float2(1.f, 0.f);
+    L.c[i] = a.x;
+    L.s[i] = a.y;
+  }
 }
 
 template <int DT>
@@ -102,21 +91,29 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
   return h2_bits(__floats2half2_rn(a, b));
 }
 
-// Eight weights of this lane's channels (all 1 without a weight).
-template <int DT>
-__device__ __forceinline__ void rope_weights(const uint16_t* w, float (&f)[8]) {
-  const int ch = (threadIdx.x & (kRowLanes - 1)) * 8;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = w != nullptr ? load16<DT>(w + ch + i) : 1.f;
+// Eight 16-bit values of a lane: the four from c0 in x, y, the four from c1 in z, w.
+__device__ __forceinline__ uint4 rope_get(const uint16_t* row, const RopeLane& L) {
+  const uint2 a = *reinterpret_cast<const uint2*>(row + L.c0), b = *reinterpret_cast<const uint2*>(row + L.c1);
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void rope_put(uint16_t* row, const RopeLane& L, uint4 v) {
+  *reinterpret_cast<uint2*>(row + L.c0) = make_uint2(v.x, v.y);
+  *reinterpret_cast<uint2*>(row + L.c1) = make_uint2(v.z, v.w);
+}
+// Weights of the lane's channels (any alignment; zeros without a weight).
+__device__ __forceinline__ uint4 rope_weights(const uint16_t* w, const RopeLane& L) {
+  if (w == nullptr) return make_uint4(0, 0, 0, 0);
+  if ((reinterpret_cast<uintptr_t>(w) & 7u) == 0) return rope_get(w, L);
+  auto two = [&](int c) { return (uint32_t)w[c] | ((uint32_t)w[c + 1] << 16); };
+  return make_uint4(two(L.c0), two(L.c0 + 2), two(L.c1), two(L.c1 + 2));
 }
 
-// One row: x = this lane's eight channels in, normed (weight != null) and rotated
-// out.  Called by whole warps; rows are 16 lanes, so a warp takes two.
+// One row: x = this lane's eight channels in, normed and rotated out.  Called by whole warps;
+// rows are 16 lanes, so a warp takes two.
 template <int DT>
-__device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, const float (&w)[8], bool norm,
-                                          float eps) {
+__device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, uint4 weight, bool norm, float eps) {
   float f[8];
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w}, w[4] = {weight.x, weight.y, weight.z, weight.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = unpack16<DT>(in[i]);
@@ -130,22 +127,31 @@ __device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, const floa
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
     const float r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
+    if (norm) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = norm ? f[i] * r * w[i] : f[i];
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack16<DT>(w[i]);
+        f[2 * i] = f[2 * i] * r * v.x;
+        f[2 * i + 1] = f[2 * i + 1] * r * v.y;
+      }
+    }
   }
-  float y[8];
-  if (L.interleaved) {
+  if (L.on) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(f[i], L.c[i], f[i ^ 1] * L.s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = fmaf(f[i], L.c[i], __shfl_sync(0xFFFFFFFFu, f[i], L.src) * L.s[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float a = L.interleaved ? f[2 * i] : f[i], b = L.interleaved ? f[2 * i + 1] : f[4 + i];
+      const float ya = fmaf(a, L.c[i], -b * L.s[i]), yb = fmaf(b, L.c[i], a * L.s[i]);
+      if (L.interleaved) {
+        f[2 * i] = ya;
+        f[2 * i + 1] = yb;
+      } else {
+        f[i] = ya;
+        f[4 + i] = yb;
+      }
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = L.on ? y[i] : f[i];
-  return make_uint4(pack16<DT>(y[0], y[1]), pack16<DT>(y[2], y[3]), pack16<DT>(y[4], y[5]),
-                    pack16<DT>(y[6], y[7]));
+  return make_uint4(pack16<DT>(f[0], f[1]), pack16<DT>(f[2], f[3]), pack16<DT>(f[4], f[5]),
+                    pack16<DT>(f[6], f[7]));
 }
 
 // The rows of one token: H1 query rows and H2 key rows through rope_row, H2 value
@@ -167,49 +173,43 @@ struct TokenRows {
   }
 };
 
-// Rows a 16-lane group loads before it uses the first of them: with eight groups a
-// block, 48 rows in one round of independent loads.
-constexpr int kRopeAhead = 6;
-
-// First round of a token's rows (nothing depends on its position yet).
-__device__ __forceinline__ void rope_load(const TokenRows& t, int r0, uint4 (&x)[kRopeAhead]) {
-  const int grp = threadIdx.x / kRowLanes, ch = (threadIdx.x & (kRowLanes - 1)) * 8, n = t.rows();
+// A block of THREADS takes THREADS / 16 rows at a time and loads AHEAD rows a 16-lane group
+// before it uses the first of them.  First round of a token's rows (nothing depends on its
+// position yet).
+template <int THREADS, int AHEAD>
+__device__ __forceinline__ void rope_load(const TokenRows& t, const RopeLane& L, int r0, uint4 (&x)[AHEAD]) {
+  const int n = t.rows();
 #pragma unroll
-  for (int u = 0; u < kRopeAhead; ++u) {
-    const int i = r0 + grp + u * (kRopeThreads / kRowLanes);
-    x[u] = i < n ? *reinterpret_cast<const uint4*>(t.in(i) + ch) : make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < AHEAD; ++u) {
+    const int i = r0 + threadIdx.x / kRowLanes + u * (THREADS / kRowLanes);
+    x[u] = i < n ? rope_get(t.in(i), L) : make_uint4(0, 0, 0, 0);
   }
 }
 
 // Every row of a token, the first round's already in x.  All threads of the block,
 // after the angles (cs) are visible to them.
-template <int DT>
-__device__ __forceinline__ void rope_token(const RopeParams& p, const float2* cs, const TokenRows& t,
-                                           uint4 (&x)[kRopeAhead]) {
-  const int grp = threadIdx.x / kRowLanes, ch = (threadIdx.x & (kRowLanes - 1)) * 8, n = t.rows();
-  const RopeLane L = rope_lane(p, cs);
-  float wq[8], wk[8];
-  rope_weights<DT>(p.q_weight, wq);
-  rope_weights<DT>(p.k_weight, wk);
-  constexpr int kStep = kRopeThreads / kRowLanes;
-  for (int r0 = 0; r0 < n; r0 += kRopeAhead * kStep) {
-    if (r0 > 0) rope_load(t, r0, x);
+template <int DT, int THREADS, int AHEAD>
+__device__ __forceinline__ void rope_token(const RopeParams& p, RopeLane& L, const float2* cs, const TokenRows& t,
+                                           uint4 (&x)[AHEAD]) {
+  const int grp = threadIdx.x / kRowLanes, n = t.rows();
+  rope_coefficients(L, cs);
+  const uint4 wq = rope_weights(p.q_weight, L), wk = rope_weights(p.k_weight, L);
+  constexpr int kStep = THREADS / kRowLanes;
+  for (int r0 = 0; r0 < n; r0 += AHEAD * kStep) {
+    if (r0 > 0) rope_load<THREADS>(t, L, r0, x);
 #pragma unroll
-    for (int u = 0; u < kRopeAhead; ++u) {
-      const int first = r0 + u * kStep;  // the block's rows of this step: first .. first + 7
+    for (int u = 0; u < AHEAD; ++u) {
+      const int first = r0 + u * kStep;  // the block's rows of this step from here
       if (first >= n) break;
       const int i = first + grp;
       uint4 y = x[u];
       if (first < t.H1 + t.H2) {  // some row of the step rotates: whole warps take part
         const bool key = i >= t.H1;
         const bool norm = (key ? p.k_weight : p.q_weight) != nullptr;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = key ? wk[e] : wq[e];
-        const uint4 z = rope_row<DT>(x[u], L, w, norm, p.eps);
+        const uint4 z = rope_row<DT>(x[u], L, key ? wk : wq, norm, p.eps);
         if (i < t.H1 + t.H2) y = z;
       }
-      if (i < n) *reinterpret_cast<uint4*>(t.out(i) + ch) = y;
+      if (i < n) rope_put(t.out(i), L, y);
     }
   }
 }

@@ -57,6 +57,20 @@ class Config:
     v_group: int = 32
     v_bit: int = 2                  # Value code width: 2, or 4 with lo_bit 4
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_ref", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+    def ref(self):
+        """A reference to the C structure, kept until a field changes."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
     def c(self):
         return _Cfg(self.head_dim, self.num_kv_heads, self.num_q_heads, self.page_tokens,
                     self.n_hi, self.hi_bit, self.lo_bit, self.v_group, self.rank_mode,
@@ -352,74 +366,94 @@ class Rope:
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self._c = _Rope(self.rot_dim, layout, amplitude, eps, _ptr(self.turns), _ptr(q_weight),
                         _ptr(k_weight))
+        self._ref = ctypes.byref(self._c)
 
-    def c(self):
-        return self._c
+    def ref(self, dev: int):
+        for t in (self.turns, self.q_weight, self.k_weight):
+            if t is not None:
+                _here(t, dev)
+        return self._ref
 
 
-def _rows(t, heads: int):
+def _device():
+    """The current CUDA device, which the calls below launch on: every tensor must be there."""
+    import torch
+    return torch.cuda.current_device()
+
+
+def _here(t, dev: int):
+    if t.get_device() != dev:  # -1: host memory
+        if not t.is_cuda:
+            raise ValueError("kitty: tensor arguments must be in device memory (got %s)" % t.device)
+        raise ValueError("kitty: a tensor is on %s, the current device is cuda:%d" % (t.device, dev))
+
+
+def _dense(t, dev: int):
+    """Device address of a dense array on the current device (None: null)."""
+    if t is None:
+        return None
+    _here(t, dev)
+    if not t.is_contiguous():
+        raise ValueError("kitty: tensor arguments must be contiguous (shape %s, strides %s)"
+                         % (tuple(t.shape), t.stride()))
+    return t.data_ptr()
+
+
+def _rows(t, n: int, heads: int, dev: int):
     """(device address, elements from token to token) of rows [n, heads, 128]: 16-bit, each
     token's heads dense, any stride between tokens."""
     if t is None:
         return None, 0
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.element_size() != 2:
-        raise ValueError("kitty: expected 16-bit rows [n, %d, %d] (got %s, %s)"
-                         % (heads, D, tuple(t.shape), t.dtype))
+    if t.shape != (n, heads, D) or t.element_size() != 2:
+        raise ValueError("kitty: expected 16-bit rows [%d, %d, %d] (got %s, %s)"
+                         % (n, heads, D, tuple(t.shape), t.dtype))
+    _here(t, dev)
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError("kitty: the heads of a token must be contiguous (strides %s)" % (t.stride(),))
-    if t.shape[0] <= 1:  # the stride between tokens of one token says nothing
-        s0 = heads * D
-    return t.data_ptr(), s0
+    # the stride between tokens of one token says nothing
+    return t.data_ptr(), s0 if n > 1 else heads * D
 
 
-def _on_current_device(*tensors):
-    """Every tensor in the current CUDA device's memory: the launch goes to its stream."""
-    import torch
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("kitty: tensor arguments must be in device memory (got %s)" % t.device)
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError("kitty: a tensor is on cuda:%d, the current device is cuda:%d"
-                             % (t.get_device(), dev))
-
-
-def _ints(name: str, t, n: int):
-    """Address of a dense int32 array of at least n entries."""
+def _ints(name: str, t, n: int, dev: int):
+    """Address of a dense int32 array of at least n entries (None: null)."""
     if t is None:
         return None
     if t.element_size() != 4 or t.is_floating_point() or t.numel() < n:
         raise ValueError("kitty: %s must be int32 with %d entries (got %s, %s)"
                          % (name, n, tuple(t.shape), t.dtype))
-    return _ptr(t)
+    return _dense(t, dev)
 
 
-def _table(t, B: int):
+def _table(t, B: int, dev: int):
     """(address, entries of a row) of a block table [>= B, max_pages]."""
     if t.dim() != 2 or t.shape[0] < B:
         raise ValueError("kitty: the block table must be [%d, max_pages] (got %s)" % (B, tuple(t.shape)))
-    return _ints("block_table", t, 0), t.shape[1]
+    return _ints("block_table", t, 0, dev), t.shape[1]
+
+
+def _raw_stream(stream, dev: int):
+    """As _stream, for the current device's current stream without making a stream object."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def norm_rope(cfg: Config, rope: Rope, q, k, positions, q_out, k_out, stream=None):
     """Per-head norms and the position rotation of queries q [n, Hq, 128] and keys k
     [n, Hkv, 128] at positions [n] into q_out and k_out (which may be q and k); q or k may
     be None.  Rows may be slices of a joint projection (any token stride)."""
-    _on_current_device(q, k, positions, q_out, k_out, rope.turns)
-    n = positions.numel()
-    a = []
-    for x, y, heads in ((q, q_out, cfg.num_q_heads), (k, k_out, cfg.num_kv_heads)):
-        if (x is None) != (y is None) or (x is not None and (x.shape[0] != n or y.shape[0] != n)):
-            raise ValueError("kitty: %d positions need as many rows in and out" % n)
-        a.append(_rows(x, heads) + _rows(y, heads))
+    dev, n = _device(), positions.numel()
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("kitty: rows in need rows out")
+    qp, qs = _rows(q, n, cfg.num_q_heads, dev)
+    kp, ks = _rows(k, n, cfg.num_kv_heads, dev)
+    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev)
+    ko, kos = _rows(k_out, n, cfg.num_kv_heads, dev)
     _chk("kitty_norm_rope", load().kitty_norm_rope(
-        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), a[0][0], a[0][1], a[1][0], a[1][1],
-        _ints("positions", positions, n), n, a[0][2], a[0][3], a[1][2], a[1][3], _stream(stream)))
+        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, _ints("positions", positions, n, dev), n, qo, qos,
+        ko, kos, _raw_stream(stream, dev)))
 
 
 def append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, tail_k, tail_v, tail_len, run_sum,
@@ -427,21 +461,20 @@ def append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, tail_k, tail_v,
                 pool_pages: int, pos_base=None, counted: bool = False, status=None, stream=None):
     """append_token with norm and rotation on the way (kitty_append_rope): the rotated query
     rows go to q_out (q and q_out may be None), the rotated key into the tail."""
-    B = tail_len.numel()
-    _on_current_device(q, k_new, v_new, q_out, tail_k, tail_v, tail_len, run_sum, run_sumsq,
-                       run_count, flush_page_ids, block_table, num_pages, pool, pos_base, status,
-                       rope.turns)
-    (qp, qs), (op, os_) = _rows(q, cfg.num_q_heads), _rows(q_out, cfg.num_q_heads)
-    (kp, ks), (vp, vs) = _rows(k_new, cfg.num_kv_heads), _rows(v_new, cfg.num_kv_heads)
-    for x in (q, k_new, v_new, q_out):
-        if x is not None and x.shape[0] != B:
-            raise ValueError("kitty: %d sequences need as many rows (got %s)" % (B, tuple(x.shape)))
+    dev, B = _device(), tail_len.numel()
+    qp, qs = _rows(q, B, cfg.num_q_heads, dev)
+    qo, qos = _rows(q_out, B, cfg.num_q_heads, dev)
+    kp, ks = _rows(k_new, B, cfg.num_kv_heads, dev)
+    vp, vs = _rows(v_new, B, cfg.num_kv_heads, dev)
+    table, max_pages = _table(block_table, B, dev)
     _chk("kitty_append_rope", load().kitty_append_rope(
-        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), qp, qs, kp, ks, vp, vs, op, os_, _ptr(tail_k),
-        _ptr(tail_v), _ptr(tail_len), _ptr(run_sum), _ptr(run_sumsq), _ptr(run_count),
-        _ints("flush_page_ids", flush_page_ids, B), *_table(block_table, B),
-        _ints("num_pages", num_pages, B), _ptr(pool), pool_pages, _ints("pos_base", pos_base, B),
-        int(counted), B, _ptr(status), _stream(stream)))
+        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, vp, vs, qo, qos, _dense(tail_k, dev),
+        _dense(tail_v, dev), _ints("tail_len", tail_len, B, dev), _dense(run_sum, dev),
+        _dense(run_sumsq, dev), _dense(run_count, dev),
+        _ints("flush_page_ids", flush_page_ids, B, dev), table, max_pages,
+        _ints("num_pages", num_pages, B, dev), _dense(pool, dev), pool_pages,
+        _ints("pos_base", pos_base, B, dev), int(counted), B, _dense(status, dev),
+        _raw_stream(stream, dev)))
 
 
 def f16kv_append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, pool, pool_pages: int,
@@ -450,19 +483,18 @@ def f16kv_append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, pool, poo
     """Norm, rotation and append into the 16-bit paged cache (kitty_f16kv_append_rope): one
     token a sequence, or the runs that seq_start [B + 1] marks; rows behind the last run
     are left alone."""
-    B, n = ctx_len.numel(), k_new.shape[0]
-    _on_current_device(q, k_new, v_new, q_out, pool, block_table, ctx_len, new_page_ids, seq_start,
-                       pos_base, status, rope.turns)
-    (qp, qs), (op, os_) = _rows(q, cfg.num_q_heads), _rows(q_out, cfg.num_q_heads)
-    (kp, ks), (vp, vs) = _rows(k_new, cfg.num_kv_heads), _rows(v_new, cfg.num_kv_heads)
-    for x in (q, v_new, q_out):
-        if x is not None and x.shape[0] != n:
-            raise ValueError("kitty: %d tokens need as many rows (got %s)" % (n, tuple(x.shape)))
+    dev, B, n = _device(), ctx_len.numel(), k_new.shape[0]
+    qp, qs = _rows(q, n, cfg.num_q_heads, dev)
+    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev)
+    kp, ks = _rows(k_new, n, cfg.num_kv_heads, dev)
+    vp, vs = _rows(v_new, n, cfg.num_kv_heads, dev)
+    table, max_pages = _table(block_table, B, dev)
     _chk("kitty_f16kv_append_rope", load().kitty_f16kv_append_rope(
-        ctypes.byref(cfg.c()), ctypes.byref(rope.c()), qp, qs, kp, ks, vp, vs, n, op, os_, _ptr(pool),
-        pool_pages, *_table(block_table, B), _ptr(ctx_len),
-        _ints("new_page_ids", new_page_ids, n), _ints("seq_start", seq_start, B + 1),
-        _ints("pos_base", pos_base, B), int(counted), B, _ptr(status), _stream(stream)))
+        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, vp, vs, n, qo, qos, _dense(pool, dev), pool_pages,
+        table, max_pages, _ints("ctx_len", ctx_len, B, dev),
+        _ints("new_page_ids", new_page_ids, n, dev), _ints("seq_start", seq_start, B + 1, dev),
+        _ints("pos_base", pos_base, B, dev), int(counted), B, _dense(status, dev),
+        _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------------------------ 16-bit paged baseline
@@ -528,10 +560,13 @@ def f16kv_shared_workspace_bytes(cfg: Config, B: int, n_prefix: int, max_pages: 
     return _shared_bytes("kitty_f16kv_shared_workspace_bytes", cfg, B, n_prefix, max_pages)
 
 
-def _attended(cfg, q, out, B):
-    if q.shape != (B, cfg.num_q_heads, D) or q.element_size() != 2 or out.shape != q.shape:
+def _attended(cfg, q, out, B, dev):
+    """Addresses of q (16-bit) and out, both [B, Hq, 128]."""
+    shape = (B, cfg.num_q_heads, D)
+    if q.shape != shape or q.element_size() != 2 or out.shape != shape:
         raise ValueError("kitty: q (16-bit) and out must be [%d, %d, %d] (got %s, %s)"
-                         % (B, cfg.num_q_heads, D, tuple(q.shape), tuple(out.shape)))
+                         % (*shape, tuple(q.shape), tuple(out.shape)))
+    return _dense(q, dev), _dense(out, dev)
 
 
 def decode_attention_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, prefix_pages,
@@ -540,16 +575,16 @@ def decode_attention_shared(cfg: Config, q, pool, pool_pages: int, prefix_table,
     """decode_attention of a batch that shares a prefix (kitty_decode_attention_shared):
     sequence b attends the first prefix_pages[b] pages of prefix_table (prefix_pages None: all
     of them), then its own pages and tail."""
-    B = num_pages.numel()
-    _on_current_device(q, pool, prefix_table, prefix_pages, block_table, num_pages, tail_k, tail_v,
-                       tail_len, out, workspace, status)
-    _attended(cfg, q, out, B)
+    dev, B = _device(), num_pages.numel()
+    qp, op = _attended(cfg, q, out, B, dev)
+    table, max_pages = _table(block_table, B, dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _chk("kitty_decode_attention_shared", load().kitty_decode_attention_shared(
-        ctypes.byref(cfg.c()), _ptr(q), _ptr(pool), pool_pages, _ints("prefix_table", prefix_table, 0),
-        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B), *_table(block_table, B),
-        _ptr(num_pages), _ptr(tail_k), _ptr(tail_v), _ints("tail_len", tail_len, B), float(sm_scale),
-        _ptr(out), _out_dtype(out), _ptr(workspace), ws_bytes, B, _ptr(status), _stream(stream)))
+        cfg.ref(), qp, _dense(pool, dev), pool_pages, _ints("prefix_table", prefix_table, 0, dev),
+        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev), table, max_pages,
+        _ints("num_pages", num_pages, B, dev), _dense(tail_k, dev), _dense(tail_v, dev),
+        _ints("tail_len", tail_len, B, dev), float(sm_scale), op, _out_dtype(out),
+        _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))
 
 
 def f16kv_decode_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, prefix_pages,
@@ -557,13 +592,12 @@ def f16kv_decode_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, pre
                         stream=None):
     """f16kv_decode of a batch that shares a prefix (kitty_f16kv_decode_shared); ctx_len counts
     a sequence's own tokens."""
-    B = ctx_len.numel()
-    _on_current_device(q, pool, prefix_table, prefix_pages, block_table, ctx_len, out, workspace,
-                       status)
-    _attended(cfg, q, out, B)
+    dev, B = _device(), ctx_len.numel()
+    qp, op = _attended(cfg, q, out, B, dev)
+    table, max_pages = _table(block_table, B, dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _chk("kitty_f16kv_decode_shared", load().kitty_f16kv_decode_shared(
-        ctypes.byref(cfg.c()), _ptr(q), _ptr(pool), pool_pages, _ints("prefix_table", prefix_table, 0),
-        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B), *_table(block_table, B),
-        _ptr(ctx_len), float(sm_scale), _ptr(out), _out_dtype(out), _ptr(workspace), ws_bytes, B,
-        _ptr(status), _stream(stream)))
+        cfg.ref(), qp, _dense(pool, dev), pool_pages, _ints("prefix_table", prefix_table, 0, dev),
+        prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev), table, max_pages,
+        _ints("ctx_len", ctx_len, B, dev), float(sm_scale), op, _out_dtype(out),
+        _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))

@@ -170,19 +170,50 @@ def test_f16kv_append_rope_refusals(lib):
     assert _append16(lib, rope=_rope(rot_dim=40)) == -2
 
 
+class _OnDevice:
+    """A host tensor that claims to be on a device: the checks read shapes and strides only."""
+
+    def __init__(self, t, dev=0):
+        self._t, self._dev = t, dev
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    is_cuda = True
+
+    def get_device(self):
+        return self._dev
+
+    @property
+    def device(self):
+        return "cuda:%d" % self._dev
+
+
 def test_rows_of_the_binding_are_checked():
     import torch
     x = torch.zeros(3, 20, 128, dtype=torch.int16)
-    assert K._rows(x, 20)[1] == 20 * 128
-    assert K._rows(x[:, 4:6], 2)[1] == 20 * 128           # a slice of a joint projection
-    assert K._rows(x[:1, 4:6], 2)[1] == 2 * 128
-    assert K._rows(None, 2) == (None, 0)
-    for bad in (x[:, ::2], x.float(), x[0], x.transpose(1, 2), x[:, :3]):
+    rows = lambda t, n, h, dev=0: K._rows(_OnDevice(t), n, h, dev)  # noqa: E731
+    assert rows(x, 3, 20)[1] == 20 * 128
+    assert rows(x[:, 4:6], 3, 2)[1] == 20 * 128           # a slice of a joint projection
+    assert rows(x[:1, 4:6], 1, 2)[1] == 2 * 128
+    assert K._rows(None, 3, 2, 0) == (None, 0)
+    for bad in (x[:, ::2], x.float()[:, :10], x[0], x.transpose(1, 2), x[:, :3], x[:2, :10]):
         with pytest.raises(ValueError):
-            K._rows(bad, 10)
+            rows(bad, 3, 10)
     with pytest.raises(ValueError):
-        K._on_current_device(x)                           # host memory
+        rows(x, 3, 20, 1)                                 # another device than the current one
     with pytest.raises(ValueError):
-        K._ints("positions", torch.zeros(3, dtype=torch.int64), 3)
+        K._rows(x, 3, 20, 0)                              # host memory
+    for bad, n in ((torch.zeros(3, dtype=torch.int64), 3), (torch.zeros(3), 3), (torch.zeros(2, dtype=torch.int32), 3)):
+        with pytest.raises(ValueError):
+            K._ints("positions", _OnDevice(bad), n, 0)
     with pytest.raises(ValueError):
-        K._ints("positions", torch.zeros(2, dtype=torch.int32), 3)
+        K._dense(_OnDevice(x[:, 4:6]), 0)
+
+
+def test_config_reference_follows_its_fields():
+    cfg = K.Config(num_kv_heads=2, num_q_heads=8)
+    first = cfg.ref()
+    assert cfg.ref() is first
+    cfg.n_hi = 16
+    assert cfg.ref() is not first and cfg.ref()._obj.n_hi == 16

@@ -68,10 +68,11 @@ def test_binding_checks_shapes():
     import torch
     cfg = _cfg()
     out = torch.zeros(2, 8, 128)
-    with pytest.raises(ValueError):
-        K._attended(cfg, torch.zeros(2, 7, 128, dtype=torch.int16), out, 2)
-    with pytest.raises(ValueError):
-        K._attended(cfg, torch.zeros(2, 8, 128), out, 2)
-    with pytest.raises(ValueError):
-        K._table(torch.zeros(1, 4, dtype=torch.int32), 2)
-    K._attended(cfg, torch.zeros(2, 8, 128, dtype=torch.int16), out, 2)
+    with pytest.raises(ValueError, match="must be"):
+        K._attended(cfg, torch.zeros(2, 7, 128, dtype=torch.int16), out, 2, 0)
+    with pytest.raises(ValueError, match="must be"):
+        K._attended(cfg, torch.zeros(2, 8, 128), out, 2, 0)
+    with pytest.raises(ValueError, match="block table"):
+        K._table(torch.zeros(1, 4, dtype=torch.int32), 2, 0)
+    with pytest.raises(ValueError, match="device memory"):
+        K._attended(cfg, torch.zeros(2, 8, 128, dtype=torch.int16), out, 2, 0)
