@@ -7,6 +7,11 @@ sequences complete a 32-token page this step, and which physical page each one
 gets) without reading device memory; the device state is only ever changed by
 the library's kernels.  Paper: Abstract (page-centric layout, lightweight
 runtime pipeline); VeloxQuant-MLX docs, Decode phase.
+
+Beside the calls on rotated keys there are those from the projections (prefill_rope,
+extend_rope, append_rope, step_rope: norms and rotation on the way), and a prefix that the
+sequences share (share_prefix: its pages are stored once and attended once a call for the
+whole batch).
 """
 
 from __future__ import annotations
@@ -23,7 +28,71 @@ PAGE = 32
 D = 128
 
 
-class LayerCache:
+class _SharedPrefix:
+    """Pages that the sequences of a layer's cache share: attended once for all of them, in
+    front of each sequence's own.  What both caches keep of it."""
+
+    prefix = None        # device int32 [n]: page ids of the shared prefix; None: there is none
+    prefix_pages = None  # device int32 [B]: pages of it that each sequence sees; None: all
+    pos_base = None      # device int32 [B]: positions ahead of a sequence's own tokens
+    h_prefix = 0         # host mirror: pages that each sequence sees
+
+    def _prefix_plan(self, k_pages, v_pages, pages_of):
+        """(pages of the prefix, pages of it that each sequence sees), checked."""
+        if self.prefix is not None:
+            raise ValueError("the cache has a shared prefix (drop_prefix)")
+        if self.kv_tokens():
+            raise ValueError("the sequences hold tokens already: their positions begin at the prefix's end")
+        n = k_pages.shape[0] // PAGE
+        rows = (n * PAGE, self.cfg.num_kv_heads, D)
+        for t in (k_pages, v_pages):
+            if t.shape != rows or t.element_size() != 2:
+                raise ValueError("a prefix is 16-bit [pages * %d, %d, %d] (got %s, %s)"
+                                 % (PAGE, *rows[1:], tuple(t.shape), t.dtype))
+        pages = np.full(self.B, n, np.int32) if pages_of is None else np.asarray(pages_of, np.int32)
+        if pages.shape != (self.B,) or (pages < 0).any() or (pages > n).any():
+            raise ValueError("pages_of: one count in [0, %d] for each of %d sequences" % (n, self.B))
+        return n, pages
+
+    def _set_prefix(self, ids, pages, pages_of):
+        dev = self.pool.device
+        self.prefix = torch.from_numpy(ids.astype(np.int32)).to(dev)
+        self.prefix_pages = None if pages_of is None else torch.from_numpy(pages.copy()).to(dev)
+        self.pos_base = torch.from_numpy(pages * PAGE).to(dev)
+        self.h_prefix = pages.astype(np.int64)
+        self._size_shared()
+
+    def _size_shared(self):
+        """A workspace for the shared call, grown when its plan needs more."""
+        if self.prefix is None:
+            return
+        need = max(self._shared_bytes(self.cfg, self.B, self.prefix.numel(), self.max_pages), 16)
+        ws = getattr(self, "shared_workspace", None)
+        if ws is None or ws.numel() < need:
+            self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.pool.device)
+
+    def drop_prefix(self):
+        """Forget the shared prefix and give its pages back: between batches, as the tokens of
+        the sequences stand behind it.  Graphs captured with the prefix are not to be replayed
+        any more."""
+        if self.prefix is not None:
+            self.alloc.free(self.prefix.cpu().numpy())
+            self.prefix = self.prefix_pages = self.pos_base = None
+            self.h_prefix = 0
+
+    def _prefix_tokens(self) -> int:
+        return int(np.sum(self.h_prefix)) * PAGE
+
+    def _prefix_bytes(self) -> int:
+        """The prefix's pages and table, read once for the whole batch."""
+        if self.prefix is None:
+            return 0
+        return self.prefix.numel() * (self.cfg.num_kv_heads * self.blob + 4)
+
+
+class LayerCache(_SharedPrefix):
+    _shared_bytes = staticmethod(kitty.shared_workspace_bytes)
+
     def __init__(self, cfg: kitty.Config, B: int, max_pages: int, pool_pages: int,
                  device="cuda"):
         self.cfg, self.B, self.max_pages, self.pool_pages = cfg, B, max_pages, pool_pages
@@ -97,6 +166,66 @@ class LayerCache:
         need = kitty.decode_workspace_bytes(self.cfg, self.B, self.max_pages)
         if need > self.workspace.numel() * 4:
             self.workspace = torch.empty(need // 4, dtype=torch.float32, device=self.pool.device)
+        self._size_shared()
+
+    def share_prefix(self, k_pages, v_pages, pages_of=None):
+        """Quantize a prefix that the sequences share, once: k_pages, v_pages 16-bit
+        [n * 32, Hkv, D], rotated as the sequences' own keys are (n full pages; a prompt's
+        remainder is each sequence's own).  pages_of: how many of its pages each sequence sees
+        (default: all); with running or sequence-wide ranking all or none of them, and those
+        sequences' channel statistics go on from the prefix's.  Before the prefill or the first
+        append of the sequences, on the current stream; returns the page ids."""
+        n, pages = self._prefix_plan(k_pages, v_pages, pages_of)
+        dev, run = self.pool.device, {}
+        if self.run_sum is not None:
+            if not ((pages == 0) | (pages == n)).all():
+                raise ValueError("running statistics: a sequence sees all of the prefix or none")
+            one = (torch.zeros_like(self.run_sum[:1]), torch.zeros_like(self.run_sum[:1]),
+                   torch.zeros_like(self.run_count[:1]))
+            run = dict(seq_of_page=torch.zeros(n, dtype=torch.int32, device=dev), n_seqs=1,
+                       run_sum=one[0], run_sumsq=one[1], run_count=one[2])
+        ids = self.alloc.alloc(n)
+        self._set_prefix(ids, pages, pages_of)
+        if n:
+            kitty.quantize_pages(self.cfg, k_pages, v_pages, self.prefix, self.pool, self.pool_pages,
+                                 status=self.status, **run)
+        if run:
+            sees = torch.from_numpy(pages > 0).to(dev)
+            for mine, theirs in ((self.run_sum, one[0]), (self.run_sumsq, one[1]), (self.run_count, one[2])):
+                shape = (-1,) + (1,) * (mine.dim() - 1)
+                mine.copy_(torch.where(sees.view(shape), theirs.expand_as(mine), mine))
+        return ids
+
+    def prefill_rope(self, rope: kitty.Rope, q, k, v, lens, q_out):
+        """Prompts straight from the projections: q [T, Hq, D], k, v [T, Hkv, D] 16-bit (any
+        token stride), lens[b] tokens of each sequence one after the other, behind the shared
+        prefix if there is one.  Queries and keys are normed and rotated (kitty.norm_rope; the
+        queries into q_out; q and q_out may be None), full pages quantized, the rest goes to the
+        tails.  On the current stream."""
+        lens = np.asarray(lens, np.int64)
+        dev, T = self.pool.device, int(lens.sum())
+        if lens.shape != (self.B,) or (lens < 0).any() or (lens // PAGE > self.max_pages).any():
+            raise ValueError("lens: one length up to %d pages for each of %d sequences"
+                             % (self.max_pages, self.B))
+        if k.shape != (T, self.cfg.num_kv_heads, D) or v.shape != k.shape:
+            raise ValueError("k, v: [%d, %d, %d] (got %s, %s)"
+                             % (T, self.cfg.num_kv_heads, D, tuple(k.shape), tuple(v.shape)))
+        start = np.concatenate([[0], np.cumsum(lens)])
+        n_pages, tails = lens // PAGE, lens % PAGE
+        pos = np.concatenate([np.arange(n) for n in lens]) if T else np.zeros(0)
+        pos = pos + np.repeat(np.broadcast_to(np.asarray(self.h_prefix), self.B) * PAGE, lens)
+        k_rot = torch.empty((T, self.cfg.num_kv_heads, D), dtype=k.dtype, device=dev)
+        kitty.norm_rope(self.cfg, rope, q, k, torch.from_numpy(pos.astype(np.int32)).to(dev), q_out,
+                        k_rot)
+        full = [np.arange(start[b], start[b] + n_pages[b] * PAGE) for b in range(self.B)]
+        sel = torch.from_numpy(np.concatenate(full).astype(np.int64)).to(dev)
+        tail_k, tail_v = torch.zeros_like(self.tail_k), torch.zeros_like(self.tail_v)
+        for b in np.nonzero(tails)[0]:
+            rows = slice(int(start[b + 1] - tails[b]), int(start[b + 1]))
+            for t, x in ((tail_k, k_rot), (tail_v, v)):
+                t[b, :, :tails[b]] = x[rows].view(torch.int16).transpose(0, 1)
+        return self.prefill(k_rot.index_select(0, sel), v.index_select(0, sel), n_pages, tail_k, tail_v,
+                            tails)
 
     def plan_flush(self) -> np.ndarray:
         """Host decision for the next append: a fresh page id for each sequence whose
@@ -114,8 +243,8 @@ class LayerCache:
     def step(self, k_new, v_new, flush_ids, q, out, sm_scale=None, stream=None):
         """append(k_new, v_new, flush_ids) then attend(q, out) as one fused launch
         (plus the split combine).  The fused call takes query groups of at most 4
-        heads per kv head; larger groups make the two calls."""
-        if self.cfg.num_q_heads // self.cfg.num_kv_heads > 4:
+        heads per kv head and no shared prefix; otherwise the two calls are made."""
+        if self.prefix is not None or self.cfg.num_q_heads // self.cfg.num_kv_heads > 4:
             self.append(k_new, v_new, flush_ids, stream=stream)
             self.attend(q, out, sm_scale, stream=stream)
             return
@@ -141,8 +270,29 @@ class LayerCache:
                            self.block_table, self.num_pages, self.pool, self.pool_pages,
                            status=self.status, stream=stream)
 
+    def append_rope(self, rope: kitty.Rope, q, k_new, v_new, flush_ids, q_out, stream=None):
+        """append from the projections: norms and rotation of q, k_new at each sequence's
+        position (behind the shared prefix) on the way; the queries go to q_out."""
+        kitty.append_rope(self.cfg, rope, q, k_new, v_new, q_out, self.tail_k, self.tail_v,
+                          self.tail_len, self.run_sum, self.run_sumsq, self.run_count, flush_ids,
+                          self.block_table, self.num_pages, self.pool, self.pool_pages,
+                          pos_base=self.pos_base, status=self.status, stream=stream)
+
+    def step_rope(self, rope: kitty.Rope, q, k_new, v_new, flush_ids, q_out, out, sm_scale=None,
+                  stream=None):
+        """append_rope, then attend with the rotated queries."""
+        self.append_rope(rope, q, k_new, v_new, flush_ids, q_out, stream=stream)
+        self.attend(q_out, out, sm_scale, stream=stream)
+
     def attend(self, q, out, sm_scale=None, stream=None):
         sm = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
+        if self.prefix is not None:
+            kitty.decode_attention_shared(self.cfg, q, self.pool, self.pool_pages, self.prefix,
+                                          self.prefix_pages, self.block_table, self.num_pages,
+                                          self.tail_k, self.tail_v, self.tail_len, sm, out,
+                                          workspace=self.shared_workspace, status=self.status,
+                                          stream=stream)
+            return
         kitty.decode_attention(self.cfg, q, self.pool, self.pool_pages, self.block_table,
                                self.num_pages, self.tail_k, self.tail_v, self.tail_len, sm, out,
                                workspace=self.workspace, status=self.status, stream=stream)
@@ -162,7 +312,7 @@ class LayerCache:
     def kv_tokens(self) -> int:
         """Cached tokens one decode call attends to, over the batch (host mirror):
         full pages and unquantized tail tokens."""
-        return int(self.h_pages.sum()) * PAGE + int(self.h_tail.sum())
+        return int(self.h_pages.sum()) * PAGE + int(self.h_tail.sum()) + self._prefix_tokens()
 
     def algorithmic_bytes(self) -> int:
         """Bytes one decode call must move: packed pages + tails + Q + O + block
@@ -170,15 +320,17 @@ class LayerCache:
         Hkv, Hq = self.cfg.num_kv_heads, self.cfg.num_q_heads
         pages = int(self.h_pages.sum())
         return (pages * Hkv * self.blob + int(self.h_tail.sum()) * Hkv * D * 2 * 2
-                + self.B * Hq * D * 2 * 2 + pages * 4)
+                + self.B * Hq * D * 2 * 2 + pages * 4 + self._prefix_bytes())
 
 
-class F16LayerCache:
+class F16LayerCache(_SharedPrefix):
     """The unquantized 16-bit paged KV cache of one layer (the paper's comparison
     layout for its same-budget claims, Abstract), with the same decode-loop
     interface as LayerCache: every token lives in a 32-token page (no tail), a
     token that starts a page gets a fresh page id from the host allocator, and
     the host mirrors every length."""
+
+    _shared_bytes = staticmethod(kitty.f16kv_shared_workspace_bytes)
 
     def __init__(self, cfg: kitty.Config, B: int, max_pages: int, pool_pages: int,
                  device="cuda"):
@@ -243,12 +395,71 @@ class F16LayerCache:
         self.h_len += 1
         return fl
 
+    def share_prefix(self, k_pages, v_pages, pages_of=None):
+        """As LayerCache.share_prefix (any pages_of)."""
+        n, pages = self._prefix_plan(k_pages, v_pages, pages_of)
+        ids = self.alloc.alloc(n)
+        self._set_prefix(ids, pages, pages_of)
+        if ids.size:
+            kitty.f16kv_write_pages(self.cfg, k_pages, v_pages, self.prefix, self.pool,
+                                    self.pool_pages, status=self.status)
+        return ids
+
+    def plan_extend(self, lens):
+        """Host decision for appending lens[b] tokens to each sequence: (new_page_ids [T],
+        seq_start [B + 1]), a fresh page id at every token that begins a page; advances the
+        host mirror."""
+        lens = np.asarray(lens, np.int64)
+        if lens.shape != (self.B,) or (lens < 0).any():
+            raise ValueError("lens: one length for each of %d sequences" % self.B)
+        if ((self.h_len + lens) > self.max_pages * PAGE).any():
+            raise ValueError("a sequence has no room for its new tokens")
+        start = np.concatenate([[0], np.cumsum(lens)])
+        ids = np.full(int(start[-1]), -1, np.int32)
+        at = np.concatenate([np.arange(start[b] + (-self.h_len[b]) % PAGE, start[b + 1], PAGE)
+                             for b in range(self.B)]).astype(np.int64)
+        ids[at] = self.alloc.alloc(at.size)
+        self.h_len += lens
+        return ids, start.astype(np.int32)
+
+    def extend_rope(self, rope: kitty.Rope, q, k, v, lens, q_out):
+        """Append lens[b] tokens to each sequence (prompts, or parts of them) from the projections
+        q [T, Hq, D], k, v [T, Hkv, D], normed and rotated at their positions (behind the shared
+        prefix) on the way into the pages; the queries go to q_out (q and q_out may be None).
+        On the current stream."""
+        T, Hq, Hkv = int(np.sum(lens)), self.cfg.num_q_heads, self.cfg.num_kv_heads
+        for x, heads in ((q, Hq), (q_out, Hq), (k, Hkv), (v, Hkv)):  # before pages are taken
+            if x is not None and x.shape != (T, heads, D):
+                raise ValueError("expected rows [%d, %d, %d] (got %s)" % (T, heads, D, tuple(x.shape)))
+        ids, start = (torch.from_numpy(x).to(self.pool.device) for x in self.plan_extend(lens))
+        kitty.f16kv_append_rope(self.cfg, rope, q, k, v, q_out, self.pool, self.pool_pages,
+                                self.block_table, self.ctx_len, ids, seq_start=start,
+                                pos_base=self.pos_base, status=self.status)
+
+    def append_rope(self, rope: kitty.Rope, q, k_new, v_new, new_page_ids, q_out, stream=None):
+        """append from the projections, as LayerCache.append_rope."""
+        kitty.f16kv_append_rope(self.cfg, rope, q, k_new, v_new, q_out, self.pool, self.pool_pages,
+                                self.block_table, self.ctx_len, new_page_ids, pos_base=self.pos_base,
+                                status=self.status, stream=stream)
+
+    def step_rope(self, rope: kitty.Rope, q, k_new, v_new, new_page_ids, q_out, out, sm_scale=None,
+                  stream=None):
+        """append_rope, then attend with the rotated queries."""
+        self.append_rope(rope, q, k_new, v_new, new_page_ids, q_out, stream=stream)
+        self.attend(q_out, out, sm_scale, stream=stream)
+
     def append(self, k_new, v_new, new_page_ids, stream=None):
         kitty.f16kv_append(self.cfg, k_new, v_new, self.pool, self.pool_pages, self.block_table,
                            self.ctx_len, new_page_ids, status=self.status, stream=stream)
 
     def attend(self, q, out, sm_scale=None, stream=None):
         sm = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
+        if self.prefix is not None:
+            kitty.f16kv_decode_shared(self.cfg, q, self.pool, self.pool_pages, self.prefix,
+                                      self.prefix_pages, self.block_table, self.ctx_len, sm, out,
+                                      workspace=self.shared_workspace, status=self.status,
+                                      stream=stream)
+            return
         kitty.f16kv_decode(self.cfg, q, self.pool, self.pool_pages, self.block_table,
                            self.ctx_len, sm, out, workspace=self.workspace, status=self.status,
                            stream=stream)
@@ -263,14 +474,15 @@ class F16LayerCache:
         return self.B * self.cfg.num_kv_heads * D * 2 * 2 * 2
 
     def kv_tokens(self) -> int:
-        return int(self.h_len.sum())
+        return int(self.h_len.sum()) + self._prefix_tokens()
 
     def algorithmic_bytes(self) -> int:
         """Bytes one decode call must move: the K and V rows of every cached token,
         Q, O and the block-table entries (host mirror of the lengths)."""
         Hkv, Hq = self.cfg.num_kv_heads, self.cfg.num_q_heads
         pages = int(((self.h_len + PAGE - 1) // PAGE).sum())
-        return (int(self.h_len.sum()) * Hkv * D * 2 * 2 + self.B * Hq * D * 2 * 2 + pages * 4)
+        return (int(self.h_len.sum()) * Hkv * D * 2 * 2 + self.B * Hq * D * 2 * 2 + pages * 4
+                + self._prefix_bytes())
 
 
 def capture_layers_step(layers, k_new, v_new, flush_ids, q, out, sm_scale=None,

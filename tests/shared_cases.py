@@ -23,6 +23,8 @@ def torch_type(dt):
 class Packed:
     """B sequences behind n_prefix packed pages; own[b] pages and tails[b] tokens of their own."""
 
+    sm = SM
+
     def __init__(self, Hkv, Hq, dt, n_prefix, shared, own, tails, seed=0, n_hi=32, lo_bit=2, v_bit=2,
                  spare=0, q_scale=1.0):
         import torch
@@ -71,7 +73,7 @@ class Packed:
         from mixed_precision_bit_gb300 import kitty
         d = self.dev
         kitty.decode_attention_shared(self.cfg, d["q"], self.pool, self.pool_pages, d["prefix"], d["shared"],
-                                      d["bt"], d["own"], d["tail_k"], d["tail_v"], d["tails"], SM, out,
+                                      d["bt"], d["own"], d["tail_k"], d["tail_v"], d["tails"], self.sm, out,
                                       workspace=self.workspace() if ws is None else ws, status=status,
                                       stream=stream)
 
@@ -92,11 +94,13 @@ class Packed:
         oracle.set_threads(8)
         return oracle.decode_attention(self.Hkv, self.Hq, self.n_hi, self.dt, self.q, pool, self.pool_pages, bt,
                                        n.astype(np.int32), self.tail_k, self.tail_v,
-                                       self.tails.astype(np.int32), SM, lo_bit=self.lo_bit, v_bit=self.v_bit)
+                                       self.tails.astype(np.int32), self.sm, lo_bit=self.lo_bit, v_bit=self.v_bit)
 
 
 class Plain16:
     """The same on 16-bit pages; lens[b] own tokens."""
+
+    sm = SM
 
     def __init__(self, Hkv, Hq, dt, n_prefix, shared, lens, seed=0, q_scale=1.0):
         import torch
@@ -137,7 +141,7 @@ class Plain16:
         from mixed_precision_bit_gb300 import kitty
         d = self.dev
         kitty.f16kv_decode_shared(self.cfg, d["q"], self.pool, self.pool_pages, d["prefix"], d["shared"], d["bt"],
-                                  d["lens"], SM, out, workspace=self.workspace() if ws is None else ws,
+                                  d["lens"], self.sm, out, workspace=self.workspace() if ws is None else ws,
                                   status=status, stream=stream)
 
     run = Packed.run
@@ -149,4 +153,4 @@ class Plain16:
             m = (self.lens[b] + P - 1) // P
             bt[b, :self.shared[b] + m] = np.concatenate([self.prefix[:self.shared[b]], self.bt[b, :m]])
         return oracle.decode_f16kv(self.Hkv, self.Hq, self.dt, self.q, self.host, self.pool_pages, bt,
-                                   n.astype(np.int32), SM)
+                                   n.astype(np.int32), self.sm)

@@ -1,9 +1,11 @@
 """Decode attention behind a shared prefix, on the GPU, against the fp64 oracle's decode over
 each sequence's prefix pages followed by its own: within the decode's 2e-3 of the output RMS
-(+ half an output ulp).  Where that comes from here: a probability is rounded to the type of
-the tensor cores' operand once (fp16: 2^-12 of it at most, taken with random signs over the
-tokens, so under 2^-12 of the RMS in the mean, 8 deviations below the bound); Key steps times
-codes, Value steps times codes and both minima are exact in fp16 for 2- and 4-bit codes."""
+(+ half an output ulp).  Where that comes from here: a probability is rounded to fp16 once, by
+at most 2^-11 of it, and the sum of the softmax is that of the rounded ones: an output is off
+by sum p d (v - out) with |d| <= 2^-11 and random signs, 2^-11 / sqrt(3) = 2.8e-4 of the output
+RMS (which is that of sum p v with random v): 7 deviations.  16-bit pages keep p in two parts
+(2^-17 or less).  Key steps times codes, Value steps times codes and both minima are exact in
+fp16 for 2- and 4-bit codes."""
 
 import numpy as np
 import pytest

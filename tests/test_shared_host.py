@@ -3,6 +3,7 @@ workspace sizes."""
 
 import ctypes
 
+import numpy as np
 import pytest
 
 from mixed_precision_bit_gb300 import kitty as K
@@ -76,3 +77,58 @@ def test_binding_checks_shapes():
         K._table(torch.zeros(1, 4, dtype=torch.int32), 2, 0)
     with pytest.raises(ValueError, match="device memory"):
         K._attended(cfg, torch.zeros(2, 8, 128, dtype=torch.int16), out, 2, 0)
+
+
+def _caches():
+    from mixed_precision_bit_gb300.cache import F16LayerCache, LayerCache
+    return [c(_cfg(), 3, 4, 16, device="cpu") for c in (LayerCache, F16LayerCache)]
+
+
+def test_cache_refuses_a_bad_prefix_and_keeps_its_pages():
+    import torch
+    rows = lambda n, h=2, t=torch.int16: torch.zeros(n, h, 128, dtype=t)  # noqa: E731
+    for lc in _caches():
+        for k, v, of in ((rows(33), rows(33), None), (rows(32), rows(64), None), (rows(32, 3), rows(32, 3), None),
+                         (rows(32, 2, torch.float32), rows(32), None), (rows(32), rows(32), [1, 1]),
+                         (rows(32), rows(32), [0, 1, 2]), (rows(32), rows(32), [-1, 1, 1])):
+            with pytest.raises(ValueError):
+                lc.share_prefix(k, v, pages_of=of)
+            assert lc.alloc.free_count == 16 and lc.prefix is None
+        lc.plan_flush()                                   # the sequences hold a token now
+        with pytest.raises(ValueError, match="hold tokens"):
+            lc.share_prefix(rows(32), rows(32))
+    from mixed_precision_bit_gb300.cache import LayerCache
+    lc = LayerCache(_cfg(rank_mode=K.RANK_RUNNING), 3, 4, 16, device="cpu")
+    with pytest.raises(ValueError, match="all of the prefix or none"):
+        lc.share_prefix(rows(64), rows(64), pages_of=[2, 1, 0])
+    assert lc.alloc.free_count == 16
+
+
+def test_cache_plans_of_several_tokens():
+    lc = _caches()[1]
+    ids, start = lc.plan_extend([40, 0, 32])
+    assert list(start) == [0, 40, 40, 72] and list(np.nonzero(ids >= 0)[0]) == [0, 32, 40]
+    ids, start = lc.plan_extend([24, 1, 1])               # up to a page's end; a first token; a new page
+    assert list(np.nonzero(ids >= 0)[0]) == [24, 25] and list(lc.h_len) == [64, 1, 33]
+    free = lc.alloc.free_count
+    for lens in ([65, 0, 0], [1, 1], [1, -1, 1]):
+        with pytest.raises(ValueError):
+            lc.plan_extend(lens)
+    with pytest.raises(ValueError):
+        lc.extend_rope(None, None, torch_rows(4), torch_rows(5), [1, 1, 2], None)
+    assert lc.alloc.free_count == free and list(lc.h_len) == [64, 1, 33]
+
+
+def torch_rows(n):
+    import torch
+    return torch.zeros(n, 2, 128, dtype=torch.int16)
+
+
+def test_prefill_refuses_lengths_that_do_not_fit():
+    lc = _caches()[0]
+    for k, v, lens in ((torch_rows(3), torch_rows(3), [1, 1]), (torch_rows(3), torch_rows(3), [1, 1, 2]),
+                       (torch_rows(3), torch_rows(2), [1, 1, 1]), (torch_rows(160), torch_rows(160), [160, 0, 0]),
+                       (torch_rows(1), torch_rows(1), [2, -1, 0])):
+        with pytest.raises(ValueError):
+            lc.prefill_rope(None, None, k, v, lens, None)
+    assert lc.alloc.free_count == 16
