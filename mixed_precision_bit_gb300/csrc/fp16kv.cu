@@ -19,6 +19,7 @@
 //   PV      O^T[c][n] = sum_t V[t][c] P[t][n], V^T from transposing ldmatrix,
 //           P as a (high, rest) pair in the 16-bit type per head.
 // Splits are merged by a second kernel in split order.
+#include "grid_dep.cuh"
 #include "kitty_common.cuh"
 #include "host_common.h"
 #include "partials.h"
@@ -69,6 +70,7 @@ __device__ __forceinline__ void store_o(void* out, int dt, size_t i, float v) {
 template <int DT>
 __global__ void __launch_bounds__(kFWarps * 32, kFBlocks) f16kv_decode_kernel(const F16Params p) {
   extern __shared__ __align__(128) uint8_t fsm[];
+  grid_trigger();  // a dependent grid (a shared prefix's) may fill the SMs that this one leaves
   const int u = blockIdx.x, s = blockIdx.y;
   const int b = u / p.Hkv, kvh = u - b * p.Hkv;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
