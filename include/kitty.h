@@ -316,8 +316,8 @@ int kitty_decode_attention_noalloc(const kitty_cfg* cfg, const void* q, const vo
  * step so large that a step times a code may leave fp16's range (a step above 65504 / 2^bits;
  * channels or groups that span more than half the range of the input rule) sets
  * KITTY_ST_RANGE, and the outputs of the sequences that share it are then undefined.
- * Launches, in stream order: the decode kernel, the prefix kernel, the merge; all three can
- * be captured. */
+ * Launches, in stream order: the prefix kernel, the decode kernel beside its end, the merge;
+ * all three can be captured. */
 int kitty_shared_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_prefix,
                                  int32_t max_pages, size_t* bytes);
 int kitty_decode_attention_shared(const kitty_cfg* cfg, const void* q, const void* pool,

@@ -41,6 +41,7 @@
 // measured on the GB300, the PV products of codes in mantissa bits 0-1 kept an
 // error near 2^-13 of the output's scale over an 8192-token sequence, 4 to 8
 // times that of the next two bits up.
+#include "grid_dep.cuh"
 #include "kitty_common.cuh"
 #include "quant_tile.cuh"
 #include "host_common.h"
@@ -139,17 +140,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Programmatic dependent launch: a dependent grid may start once every CTA of
-// this grid has called trigger_dependents (or exited); wait blocks until this
-// grid has completed and its memory is visible.  Both are no-ops for a grid
-// launched without the attribute.
-__device__ __forceinline__ void trigger_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Shared-memory loads from a 32-bit shared address plus a compile-time offset.
@@ -716,7 +706,7 @@ __device__ __forceinline__ void merge_get(const uint8_t* stages, const int warp_
 template <int DT, int NX, int W, int V>
 __global__ void __launch_bounds__(kDThreads, kDMinBlocks) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t dsm[];
-  trigger_dependents();  // the combine step may be scheduled once every CTA is running
+  grid_trigger();  // the combine step may be scheduled once every CTA is running
   const int u = blockIdx.x, s = blockIdx.y;
   const int bk = u / p.HG, hgi = u - bk * p.HG;  // (sequence, kv head), head group
   const int b = bk / p.Hkv, kvh = bk - b * p.Hkv;
@@ -1016,6 +1006,7 @@ __global__ void __launch_bounds__(kDThreads, kDMinBlocks) decode_kernel(const De
   merge_put(w, wst, L);
   __syncthreads();
   merge_get<V>(stages, kDStages * kBlob, 0, p, b, s, h0, gh, L);
+  if (blockIdx.x + blockIdx.y == 0) grid_wait();  // launched behind another grid: this one ends after it
 }
 
 // Merge the split partials of a (sequence, query head) row: the maximum of the
@@ -1055,7 +1046,7 @@ constexpr int kCombineSplits = 8;  // splits one 32-thread row merges in one rou
 // (16-byte loads), four rows per 128-thread CTA; every split's (m, l, o) in one
 // round of independent loads.
 __global__ void __launch_bounds__(128) combine_kernel(const DecodeParams p, int rows) {
-  grid_dependency_wait();
+  grid_wait();
   const int bh = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (bh >= rows) return;
   const float* base = p.ws + (size_t)bh * p.splits * kPartial;
@@ -1087,7 +1078,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const DecodeParams p, int 
 // the four warps' results through shared memory.  Two dependent rounds of
 // loads instead of one per 16 splits (maxima) plus one per 8 (sums).
 __global__ void __launch_bounds__(128) combine_wide_kernel(const DecodeParams p, int rows) {
-  grid_dependency_wait();
+  grid_wait();
   __shared__ float4 wo[4][32];
   __shared__ float wm[4], wl[4];
   const int bh = blockIdx.x, wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1144,7 +1135,7 @@ __global__ void __launch_bounds__(128) combine_wide_kernel(const DecodeParams p,
 
 // Fused append bookkeeping when there is no combine step (one split).
 __global__ void finalize_kernel(const DecodeParams p, int B) {
-  grid_dependency_wait();
+  grid_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b < B)
     append_finalize_one(b, p.ap.tail_len, p.ap.flush_page_ids, p.ap.block_table, p.max_pages,
@@ -1319,7 +1310,7 @@ template <int DT, int NX>
 __global__ void __launch_bounds__(kDThreads, kDMinBlocks8) decode8_kernel(const DecodeParams p) {
   constexpr int W = 2, V = 2;
   extern __shared__ __align__(128) uint8_t dsm[];
-  trigger_dependents();
+  grid_trigger();
   const int u = blockIdx.x, s = blockIdx.y;
   const int bk = u / p.HG, hgi = u - bk * p.HG;
   const int b = bk / p.Hkv, kvh = bk - b * p.Hkv;
@@ -1521,10 +1512,11 @@ __global__ void __launch_bounds__(kDThreads, kDMinBlocks8) decode8_kernel(const 
   merge_get<V>(stages, kDStages * kBlob, 0, p, b, s, h0, min(kHeadsPerCta, gh), L);
   if (gh > kHeadsPerCta)
     merge_get<V>(stages, kDStages * kBlob, kMergeBytes, p, b, s, h0 + kHeadsPerCta, gh - kHeadsPerCta, L);
+  if (blockIdx.x + blockIdx.y == 0) grid_wait();  // launched behind another grid: this one ends after it
 }
 
 template <int DT, int NX, int W, int V>
-cudaError_t launch_decode(dim3 grid, size_t smem, cudaStream_t s, const DecodeParams& p) {
+cudaError_t launch_decode(dim3 grid, size_t smem, cudaStream_t s, bool behind, const DecodeParams& p) {
   // the shared-memory opt-in is a per-device function attribute (smem is fixed
   // per instantiation): set it on the first launch on each device only
   static std::atomic<uint64_t> opted_in{0};
@@ -1537,12 +1529,11 @@ cudaError_t launch_decode(dim3 grid, size_t smem, cudaStream_t s, const DecodePa
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit);
   }
-  decode_kernel<DT, NX, W, V><<<grid, kDThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(decode_kernel<DT, NX, W, V>, grid, kDThreads, smem, s, behind, p);
 }
 
 template <int DT, int NX>
-cudaError_t launch_decode8(dim3 grid, size_t smem, cudaStream_t s, const DecodeParams& p) {
+cudaError_t launch_decode8(dim3 grid, size_t smem, cudaStream_t s, bool behind, const DecodeParams& p) {
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -1553,37 +1544,36 @@ cudaError_t launch_decode8(dim3 grid, size_t smem, cudaStream_t s, const DecodeP
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit);
   }
-  decode8_kernel<DT, NX><<<grid, kDThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(decode8_kernel<DT, NX>, grid, kDThreads, smem, s, behind, p);
 }
 
 template <int DT>
-cudaError_t launch_decode8_nx(int nx, dim3 grid, size_t smem, cudaStream_t s, const DecodeParams& p) {
+cudaError_t launch_decode8_nx(int nx, dim3 grid, size_t smem, cudaStream_t s, bool behind, const DecodeParams& p) {
   switch (nx) {
-    case 0: return launch_decode8<DT, 0>(grid, smem, s, p);
-    case 1: return launch_decode8<DT, 1>(grid, smem, s, p);
-    case 2: return launch_decode8<DT, 2>(grid, smem, s, p);
-    case 3: return launch_decode8<DT, 3>(grid, smem, s, p);
-    case 4: return launch_decode8<DT, 4>(grid, smem, s, p);
-    case 5: return launch_decode8<DT, 5>(grid, smem, s, p);
-    case 6: return launch_decode8<DT, 6>(grid, smem, s, p);
-    case 7: return launch_decode8<DT, 7>(grid, smem, s, p);
-    default: return launch_decode8<DT, 8>(grid, smem, s, p);
+    case 0: return launch_decode8<DT, 0>(grid, smem, s, behind, p);
+    case 1: return launch_decode8<DT, 1>(grid, smem, s, behind, p);
+    case 2: return launch_decode8<DT, 2>(grid, smem, s, behind, p);
+    case 3: return launch_decode8<DT, 3>(grid, smem, s, behind, p);
+    case 4: return launch_decode8<DT, 4>(grid, smem, s, behind, p);
+    case 5: return launch_decode8<DT, 5>(grid, smem, s, behind, p);
+    case 6: return launch_decode8<DT, 6>(grid, smem, s, behind, p);
+    case 7: return launch_decode8<DT, 7>(grid, smem, s, behind, p);
+    default: return launch_decode8<DT, 8>(grid, smem, s, behind, p);
   }
 }
 
 template <int DT, int W, int V>
-cudaError_t launch_decode_nx(int nx, dim3 grid, size_t smem, cudaStream_t s, const DecodeParams& p) {
+cudaError_t launch_decode_nx(int nx, dim3 grid, size_t smem, cudaStream_t s, bool behind, const DecodeParams& p) {
   switch (nx) {
-    case 0: return launch_decode<DT, 0, W, V>(grid, smem, s, p);
-    case 1: return launch_decode<DT, 1, W, V>(grid, smem, s, p);
-    case 2: return launch_decode<DT, 2, W, V>(grid, smem, s, p);
-    case 3: return launch_decode<DT, 3, W, V>(grid, smem, s, p);
-    case 4: return launch_decode<DT, 4, W, V>(grid, smem, s, p);
-    case 5: return launch_decode<DT, 5, W, V>(grid, smem, s, p);
-    case 6: return launch_decode<DT, 6, W, V>(grid, smem, s, p);
-    case 7: return launch_decode<DT, 7, W, V>(grid, smem, s, p);
-    default: return launch_decode<DT, 8, W, V>(grid, smem, s, p);
+    case 0: return launch_decode<DT, 0, W, V>(grid, smem, s, behind, p);
+    case 1: return launch_decode<DT, 1, W, V>(grid, smem, s, behind, p);
+    case 2: return launch_decode<DT, 2, W, V>(grid, smem, s, behind, p);
+    case 3: return launch_decode<DT, 3, W, V>(grid, smem, s, behind, p);
+    case 4: return launch_decode<DT, 4, W, V>(grid, smem, s, behind, p);
+    case 5: return launch_decode<DT, 5, W, V>(grid, smem, s, behind, p);
+    case 6: return launch_decode<DT, 6, W, V>(grid, smem, s, behind, p);
+    case 7: return launch_decode<DT, 7, W, V>(grid, smem, s, behind, p);
+    default: return launch_decode<DT, 8, W, V>(grid, smem, s, behind, p);
   }
 }
 
@@ -1772,7 +1762,8 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
               const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
               const void* tail_k, const void* tail_v, const int32_t* tail_len, float sm_scale,
               void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes_in, int32_t B,
-              int32_t* d_status, void* stream, const AppendParams& ap, int* partial_splits = nullptr) {
+              int32_t* d_status, void* stream, const AppendParams& ap, int* partial_splits = nullptr,
+              Partials mode = Partials::kLaunch) {
   int rc = check_cfg(cfg, kMaxGroup);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
@@ -1793,6 +1784,9 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
   const size_t need = workspace_bytes(cfg, B, sc);
   if (workspace_bytes_in < need || (need > 0 && (!workspace || !aligned16(workspace))))
     return KITTY_ERR_WORKSPACE;
+  if (partial_splits != nullptr) *partial_splits = sc.splits;
+  if (mode == Partials::kCheck) return KITTY_OK;
+  const bool behind = mode == Partials::kBehind;
   for (int i = 0; i <= sc.splits; ++i) p.starts[i] = sc.starts[i];
   p.ap = ap;
   p.q = static_cast<const uint16_t*>(q);
@@ -1823,20 +1817,17 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   dim3 grid((unsigned)B * cfg->num_kv_heads * p.HG, sc.splits);
   const int nx = cfg->n_hi / 16, v = v_bits(cfg);
-  const cudaError_t e = h8 ? (cfg->in_dtype == KITTY_BF16 ? launch_decode8_nx<KITTY_BF16>(nx, grid, smem, s, p)
-                                                          : launch_decode8_nx<KITTY_F16>(nx, grid, smem, s, p))
+  const cudaError_t e = h8 ? (cfg->in_dtype == KITTY_BF16 ? launch_decode8_nx<KITTY_BF16>(nx, grid, smem, s, behind, p)
+                                                          : launch_decode8_nx<KITTY_F16>(nx, grid, smem, s, behind, p))
       : cfg->in_dtype == KITTY_BF16
-      ? (cfg->lo_bit == 4 ? (v == 4 ? launch_decode_nx<KITTY_BF16, 4, 4>(nx, grid, smem, s, p)
-                                    : launch_decode_nx<KITTY_BF16, 4, 2>(nx, grid, smem, s, p))
-                          : launch_decode_nx<KITTY_BF16, 2, 2>(nx, grid, smem, s, p))
-      : (cfg->lo_bit == 4 ? (v == 4 ? launch_decode_nx<KITTY_F16, 4, 4>(nx, grid, smem, s, p)
-                                    : launch_decode_nx<KITTY_F16, 4, 2>(nx, grid, smem, s, p))
-                          : launch_decode_nx<KITTY_F16, 2, 2>(nx, grid, smem, s, p));
+      ? (cfg->lo_bit == 4 ? (v == 4 ? launch_decode_nx<KITTY_BF16, 4, 4>(nx, grid, smem, s, behind, p)
+                                    : launch_decode_nx<KITTY_BF16, 4, 2>(nx, grid, smem, s, behind, p))
+                          : launch_decode_nx<KITTY_BF16, 2, 2>(nx, grid, smem, s, behind, p))
+      : (cfg->lo_bit == 4 ? (v == 4 ? launch_decode_nx<KITTY_F16, 4, 4>(nx, grid, smem, s, behind, p)
+                                    : launch_decode_nx<KITTY_F16, 4, 2>(nx, grid, smem, s, behind, p))
+                          : launch_decode_nx<KITTY_F16, 2, 2>(nx, grid, smem, s, behind, p));
   if (e != cudaSuccess) return KITTY_ERR_CUDA;
-  if (partial_splits != nullptr) {
-    *partial_splits = sc.splits;
-    return KITTY_OK;
-  }
+  if (partial_splits != nullptr) return KITTY_OK;
   // the merge step follows the decode grid as a programmatic dependent
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1927,10 +1918,11 @@ int kitty::decode_partials(const kitty_cfg* cfg, const void* q, const void* pool
                            const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
                            const void* tail_k, const void* tail_v, const int32_t* tail_len,
                            float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
-                           int32_t B, int32_t* d_status, void* stream, int* splits) {
+                           int32_t B, int32_t* d_status, void* stream, int* splits, Partials mode) {
   const AppendParams none = {};
   return attention(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k, tail_v,
-                   tail_len, sm_scale, out, out_dtype, ws, ws_bytes, B, d_status, stream, none, splits);
+                   tail_len, sm_scale, out, out_dtype, ws, ws_bytes, B, d_status, stream, none, splits,
+                   mode);
 }
 
 // ------------------------------------------------------------------ no-allocation variant

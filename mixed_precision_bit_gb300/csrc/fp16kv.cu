@@ -70,7 +70,7 @@ __device__ __forceinline__ void store_o(void* out, int dt, size_t i, float v) {
 template <int DT>
 __global__ void __launch_bounds__(kFWarps * 32, kFBlocks) f16kv_decode_kernel(const F16Params p) {
   extern __shared__ __align__(128) uint8_t fsm[];
-  grid_trigger();  // a dependent grid (a shared prefix's) may fill the SMs that this one leaves
+  grid_trigger();
   const int u = blockIdx.x, s = blockIdx.y;
   const int b = u / p.Hkv, kvh = u - b * p.Hkv;
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(kFWarps * 32, kFBlocks) f16kv_decode_kernel(co
       if (c == 0) { part[0] = L > 0.f ? ms : -INFINITY; part[1] = L; }
     }
   }
+  if (blockIdx.x + blockIdx.y == 0) grid_wait();  // launched behind another grid: this one ends after it
 }
 
 // Split merge: one 128-thread CTA per (sequence, query head), splits in order.
@@ -377,7 +378,7 @@ void f16kv_plan(int units, int max_pages, int* splits, int* pps) {
 }
 
 template <int DT>
-cudaError_t launch_f16kv(dim3 grid, cudaStream_t s, const F16Params& p) {
+cudaError_t launch_f16kv(dim3 grid, cudaStream_t s, bool behind, const F16Params& p) {
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -389,8 +390,7 @@ cudaError_t launch_f16kv(dim3 grid, cudaStream_t s, const F16Params& p) {
     if (e != cudaSuccess) return e;
     opted_in.fetch_or(bit);
   }
-  f16kv_decode_kernel<DT><<<grid, kFWarps * 32, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(f16kv_decode_kernel<DT>, grid, kFWarps * 32, smem, s, behind, p);
 }
 
 }  // namespace
@@ -465,7 +465,7 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
                     const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
                     float sm_scale, void* out, int32_t out_dtype, void* workspace,
                     size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream,
-                    int* partial_splits) {
+                    int* partial_splits, Partials mode) {
   const int rc = check_cfg(cfg, 4);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
@@ -483,6 +483,8 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
       p.splits > 1 ? (size_t)B * cfg->num_q_heads * p.splits * kFPartial * sizeof(float) : 0;
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
     return KITTY_ERR_WORKSPACE;
+  if (mode == Partials::kCheck) return KITTY_OK;
+  const bool behind = mode == Partials::kBehind;
   p.q = static_cast<const uint16_t*>(q);
   p.pool = static_cast<const uint8_t*>(pool);
   p.block_table = block_table;
@@ -499,8 +501,8 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
   p.g = cfg->num_q_heads / cfg->num_kv_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)B * cfg->num_kv_heads, p.splits);
-  const cudaError_t e = cfg->in_dtype == KITTY_BF16 ? launch_f16kv<KITTY_BF16>(grid, s, p)
-                                                    : launch_f16kv<KITTY_F16>(grid, s, p);
+  const cudaError_t e = cfg->in_dtype == KITTY_BF16 ? launch_f16kv<KITTY_BF16>(grid, s, behind, p)
+                                                    : launch_f16kv<KITTY_F16>(grid, s, behind, p);
   if (e != cudaSuccess) return KITTY_ERR_CUDA;
   if (p.splits > 1 && partial_splits == nullptr) f16kv_combine_kernel<<<(unsigned)B * cfg->num_q_heads, 128, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
@@ -515,7 +517,8 @@ extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const voi
                                   size_t workspace_bytes, int32_t B, int32_t* d_status,
                                   void* stream) {
   return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
-                         out_dtype, workspace, workspace_bytes, B, d_status, stream, nullptr);
+                         out_dtype, workspace, workspace_bytes, B, d_status, stream, nullptr,
+                         Partials::kLaunch);
 }
 
 size_t kitty::f16kv_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
@@ -527,7 +530,7 @@ size_t kitty::f16kv_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
 int kitty::f16kv_partials(const kitty_cfg* cfg, const void* q, const void* pool, int32_t pool_pages,
                           const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
                           float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
-                          int32_t B, int32_t* d_status, void* stream, int* splits) {
+                          int32_t B, int32_t* d_status, void* stream, int* splits, Partials mode) {
   return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
-                         out_dtype, ws, ws_bytes, B, d_status, stream, splits);
+                         out_dtype, ws, ws_bytes, B, d_status, stream, splits, mode);
 }

@@ -14,9 +14,10 @@ __device__ __forceinline__ void grid_trigger() {
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// behind: as a dependent of the grid before it in the stream; else an ordinary launch.
 template <class... P, class... A>
-inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
-                                    cudaStream_t s, A... args) {
+inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                 cudaStream_t s, bool behind, const A&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -26,8 +27,14 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
   lc.dynamicSmemBytes = smem;
   lc.stream = s;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = behind ? 1 : 0;
   return cudaLaunchKernelEx(&lc, kernel, P(args)...);
+}
+
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                    cudaStream_t s, const A&... args) {
+  return launch_behind(kernel, grid, threads, smem, s, true, args...);
 }
 
 }  // namespace kitty

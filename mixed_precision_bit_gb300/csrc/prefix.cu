@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
                                                                     const __grid_constant__ CUtensorMap map) {
   extern __shared__ uint8_t dyn[];
   __shared__ Shared sh;
-  grid_trigger();
+  grid_trigger();  // the own pages' blocks may fill the SMs that are free, or get free
   const int tid = threadIdx.x, lane = tid & 31;
   const int wid = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // the compiler sees a warp-uniform role
   const int R = p.B * p.g, units = (R + kRows - 1) / kRows;
@@ -895,19 +895,29 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (tid == 0) grid_wait();  // whoever waits for this grid has waited for the one before, too
 }
 
-// Splits of the prefix: one block an SM; a block costs its tiles and a start and end worth
-// about kBlockTiles tiles; each split adds a partial a row, written and read.
-PrefixPlan plan_for(int Hkv, int rows, int tiles, int sms) {
+// Splits of the prefix.  A block has an SM to itself; the SMs that no block takes, or that get
+// free, attend the sequences' own pages meanwhile.  So more splits shorten the longest block,
+// but each costs SM time for its start and end and a partial a row, written and read.  In us,
+// measured on GB300 by forcing the splits of five shapes (the model's choice was the fastest
+// or within 2% of it at all five; one block on every SM, the choice without the own pages'
+// share: 64 x 8192 tokens 34.3 against 30.1 us, on 16-bit pages 41.3 against 31.9 us,
+// 128 x 32768 177 against 165 us):
+constexpr double kTileUs = 1.8;    // a tile of both lanes
+constexpr double kPathTiles = 7;   // start and end of a block, in tiles, on the critical path ..
+constexpr double kBlockTiles = 8.5;  // .. and of its SM's time
+PrefixPlan plan_for(int Hkv, int rows, int tiles, int sms, double own_us) {
   PrefixPlan pl = {Hkv * ((rows + kRows - 1) / kRows), 1, 1};
-  const double tile = rows > 128 ? 1.0 : 0.5, kBlockTiles = 4.0;
-  const double per_split = (double)Hkv * rows * 1056.0 / 6.0e6;  // us, against 1.3 us a tile
+  const double tile = rows > 128 ? 1.0 : 0.5;  // lanes that share their rows halve a block's tiles
+  const double per_split = (double)Hkv * rows * 1056.0 / 6.0e6;
   double best = 1e30;
   for (int s = 1; s <= std::min(tiles, 64); ++s) {
-    const int waves = (pl.units * s + sms - 1) / sms, per = (tiles + s - 1) / s;
-    const double cost = waves * (per * tile + kBlockTiles) * 1.3 + s * per_split;
+    const int blocks = pl.units * s, waves = (blocks + sms - 1) / sms;
+    const double per = tile * ((tiles + s - 1) / s);
+    const double path = waves * (per + kPathTiles) * kTileUs;
+    const double all = (blocks * (per + kBlockTiles) * kTileUs + own_us) / sms;
+    const double cost = std::max(path, all) + s * per_split;
     if (cost < best - 1e-9) {
       best = cost;
       pl.splits = s;
@@ -915,6 +925,16 @@ PrefixPlan plan_for(int Hkv, int rows, int tiles, int sms) {
   }
   pl.slots = rows > 128 ? pl.splits : 2 * pl.splits;
   return pl;
+}
+
+// SM time of the own pages' kernel, us: per (sequence, kv head) a start and its pages (from
+// the same measurements).  Pages by the plan's hint; without one, up to 4: a block table's
+// width says little of how much of it is filled, and a guess too high leaves the prefix on too
+// few SMs (all of it), one too low costs about 1 us a needless split.
+double own_us_of(const kitty_cfg* cfg, bool packed, int B, int max_pages) {
+  const double pages = cfg->decode_total_pages > 0 ? (double)cfg->decode_total_pages / B : std::min(4.0, 0.5 * max_pages);
+  const int g = cfg->num_q_heads / cfg->num_kv_heads;
+  return (double)B * cfg->num_kv_heads * ((g + 7) / 8) * (packed ? 1.0 + 0.16 * pages : 2.5 + 0.5 * pages);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -954,17 +974,18 @@ int launch(const PrefixArgs& a, const PrefixPlan& pl, const CUtensorMap& map, cu
       return KITTY_ERR_CUDA;
     opted_in.fetch_or(bit);
   }
-  const cudaError_t e = launch_dependent(prefix_kernel<F>, dim3((unsigned)pl.units, (unsigned)pl.splits),
-                                         threads_of<F>(), (size_t)smem_of<F>(), s, a, map);
+  const cudaError_t e = launch_behind(prefix_kernel<F>, dim3((unsigned)pl.units, (unsigned)pl.splits),
+                                      threads_of<F>(), (size_t)smem_of<F>(), s, false, a, map);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
 }
 
 }  // namespace
 
-PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix) {
+PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pages) {
   if (n_prefix <= 0 || B <= 0) return {0, 0, 0};
   const int pages = packed ? PackedFmt<2, 2>::kPages : PlainFmt<true>::kPages;
-  return plan_for(cfg->num_kv_heads, B * (cfg->num_q_heads / cfg->num_kv_heads), (n_prefix + pages - 1) / pages, sm_count());
+  return plan_for(cfg->num_kv_heads, B * (cfg->num_q_heads / cfg->num_kv_heads), (n_prefix + pages - 1) / pages, sm_count(),
+                  own_us_of(cfg, packed, B, max_pages));
 }
 
 int prefix_launch(const kitty_cfg* cfg, bool packed, const PrefixArgs& args, const PrefixPlan& pl, cudaStream_t s) {

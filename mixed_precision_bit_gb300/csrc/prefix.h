@@ -27,10 +27,10 @@ struct PrefixPlan {
   int slots;   // partials a row
 };
 
-PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix);
+PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pages);
 
-// KITTY_OK or an error code.  A dependent launch: it may start before the grid ahead of it
-// in the stream has finished, and finishes after it.
+// KITTY_OK or an error code.  A dependent launch behind it may start once all of its blocks
+// have started.
 int prefix_launch(const kitty_cfg* cfg, bool packed, const PrefixArgs& args, const PrefixPlan& plan,
                   cudaStream_t stream);
 

@@ -3,8 +3,10 @@
 //   out[b][hq] = softmax(sm_scale * q . [K_prefix; K_b]) . [V_prefix; V_b]
 //
 // with the prefix's pages attended once for the whole batch and each sequence's own
-// cache by the split-K decode.  Three launches: the decode kernel's partials over the
-// own pages and tails, the prefix kernel's partials, and one merge of both.
+// cache by the split-K decode.  Three launches: the prefix kernel's partials; behind it, as a
+// dependent that fills the SMs that the prefix leaves, the decode kernel's partials over the
+// own pages and tails; and one merge of both.  (The prefix kernel behind the decode kernel
+// waited for whole SMs: 16 x 4096 tokens 20.7 against 17.2 us.)
 #include "grid_dep.cuh"
 #include "host_common.h"
 #include "kitty_common.cuh"
@@ -31,13 +33,15 @@ struct MergeParams {
 };
 
 // WARPS warps a row (4 / WARPS rows a block).  Every warp reads the row's maxima, one slot a
-// lane, and weighs them; then warp w sums slots w, w + WARPS, ... of the unscaled outputs,
-// four channels a lane, kAhead loads in flight, and the warps' sums meet in shared memory.
+// lane, and weighs them; warp w sums slots w, w + WARPS, ... of the unscaled outputs, four
+// channels a lane, requested together with the maxima; the warps' sums meet in shared memory.
 // A slot that attended nothing (m = -inf) has weight 0 and its outputs are not used.
 constexpr int kAhead = 8;
 
 template <int WARPS>
 __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
+  constexpr int kRound = WARPS * kAhead;  // slots of a row taken at once
+  static_assert(kRound <= 32, "a lane a slot");
   __shared__ float4 part[4][32];
   grid_wait();
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31, w = wid % WARPS;
@@ -49,10 +53,15 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
   auto slot = [&](int s) { return s < p.na ? a + (size_t)s * kPartialFloats : b + (size_t)(s - p.na) * kPartialFloats; };
   float ms = -INFINITY, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 32) {
-    // this round's maxima and sums, one slot a lane, and the first outputs, all in flight
-    const int mine = s0 + lane;
-    const float2 ml = mine < n ? *reinterpret_cast<const float2*>(slot(mine)) : make_float2(-INFINITY, 0.f);
+  for (int s0 = 0; s0 < n; s0 += kRound) {
+    const int end = min(n, s0 + kRound);
+    const float2 ml = s0 + lane < end ? *reinterpret_cast<const float2*>(slot(s0 + lane)) : make_float2(-INFINITY, 0.f);
+    float4 o[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int s = s0 + w + k * WARPS;
+      o[k] = s < end ? reinterpret_cast<const float4*>(slot(s) + 4)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float mr = fmaxf(ml.x, ms);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xFFFFFFFFu, mr, d));
@@ -65,24 +74,14 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
     L = L * f + l;
     O = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
     ms = mr;
-    const int m = min(32, n - s0);
-    for (int k0 = w; k0 < m; k0 += WARPS * kAhead) {
-      float4 o[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int s = k0 + k * WARPS;
-        o[k] = s < m ? reinterpret_cast<const float4*>(slot(s0 + s) + 4)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int s = k0 + k * WARPS;
-        const float es = __shfl_sync(0xFFFFFFFFu, e, s & 31);
-        if (s < m && es != 0.f) {
-          O.x = fmaf(o[k].x, es, O.x);
-          O.y = fmaf(o[k].y, es, O.y);
-          O.z = fmaf(o[k].z, es, O.z);
-          O.w = fmaf(o[k].w, es, O.w);
-        }
+    for (int k = 0; k < kAhead; ++k) {
+      const float es = __shfl_sync(0xFFFFFFFFu, e, w + k * WARPS);
+      if (es != 0.f) {
+        O.x = fmaf(o[k].x, es, O.x);
+        O.y = fmaf(o[k].y, es, O.y);
+        O.z = fmaf(o[k].z, es, O.z);
+        O.w = fmaf(o[k].w, es, O.w);
       }
     }
   }
@@ -124,8 +123,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const MergeParams p) {
   }
 }
 
-size_t prefix_bytes(const kitty_cfg* cfg, bool packed, int B, int n_prefix) {
-  return (size_t)B * cfg->num_q_heads * prefix_plan(cfg, packed, B, n_prefix).slots * kPartialFloats * sizeof(float);
+size_t prefix_bytes(const kitty_cfg* cfg, const PrefixPlan& plan, int B) {
+  return (size_t)B * cfg->num_q_heads * plan.slots * kPartialFloats * sizeof(float);
 }
 
 int check_shared(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pages) {
@@ -140,7 +139,7 @@ int workspace(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pa
   if (rc != KITTY_OK) return rc;
   if (!bytes) return KITTY_ERR_INVALID_ARG;
   *bytes = B == 0 ? 0
-                  : prefix_bytes(cfg, packed, B, n_prefix) + (packed ? decode_partial_bytes(cfg, B, max_pages)
+                  : prefix_bytes(cfg, prefix_plan(cfg, packed, B, n_prefix, max_pages), B) + (packed ? decode_partial_bytes(cfg, B, max_pages)
                                                              : f16kv_partial_bytes(cfg, B, max_pages));
   return KITTY_OK;
 }
@@ -160,11 +159,11 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
   if (B == 0) return KITTY_OK;
   if (q && !aligned16(q)) return KITTY_ERR_INVALID_ARG;
   if (ws_bytes < need || !ws || !aligned16(ws)) return KITTY_ERR_WORKSPACE;
-  const PrefixPlan plan = prefix_plan(cfg, packed, B, n_prefix);
-  const size_t mine = prefix_bytes(cfg, packed, B, n_prefix);
+  const PrefixPlan plan = prefix_plan(cfg, packed, B, n_prefix, max_pages);
+  const size_t mine = prefix_bytes(cfg, plan, B);
   float* own_ws = static_cast<float*>(ws) + mine / sizeof(float);
   MergeParams m = {static_cast<float*>(ws), own_ws, out, d_status, plan.slots, 0, B * cfg->num_q_heads, out_dtype, aligned16(out)};
-  rc = own(own_ws, ws_bytes - mine, &m.nb);
+  rc = own(own_ws, ws_bytes - mine, &m.nb, Partials::kCheck);
   if (rc != KITTY_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (plan.splits > 0) {
@@ -191,9 +190,15 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
     rc = prefix_launch(cfg, packed, p, plan, s);
     if (rc != KITTY_OK) return rc;
   }
-  // few partials a row: a warp a row; more (measured at 10 to 32): four warps
-  const cudaError_t e = m.na + m.nb <= kAhead
+  rc = own(own_ws, ws_bytes - mine, &m.nb, plan.splits > 0 ? Partials::kBehind : Partials::kLaunch);
+  if (rc != KITTY_OK) return rc;
+  // warps a row by its partials, eight requests in flight a warp (8192 rows of 11: 11.6 us
+  // cold with two, 18.8 with four that waited for the maxima first)
+  const int n = m.na + m.nb;
+  const cudaError_t e = n <= kAhead
       ? launch_dependent(merge_kernel<1>, dim3((unsigned)((m.rows + 3) / 4)), 128, 0, s, m)
+      : n <= 2 * kAhead
+      ? launch_dependent(merge_kernel<2>, dim3((unsigned)((m.rows + 1) / 2)), 128, 0, s, m)
       : launch_dependent(merge_kernel<4>, dim3((unsigned)m.rows), 128, 0, s, m);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
 }
@@ -222,10 +227,10 @@ extern "C" int kitty_decode_attention_shared(
   return shared_attention(
       cfg, true, q, pool, pool_pages, prefix_table, n_prefix, prefix_pages, max_pages, sm_scale, out,
       out_dtype, workspace, workspace_bytes, B, d_status, stream,
-      [&](float* ws, size_t bytes, int* splits) {
+      [&](float* ws, size_t bytes, int* splits, Partials mode) {
         return decode_partials(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k,
                                tail_v, tail_len, sm_scale, out, out_dtype, ws, bytes, B, d_status,
-                               stream, splits);
+                               stream, splits, mode);
       });
 }
 
@@ -239,8 +244,8 @@ extern "C" int kitty_f16kv_decode_shared(const kitty_cfg* cfg, const void* q, co
   return shared_attention(
       cfg, false, q, pool, pool_pages, prefix_table, n_prefix, prefix_pages, max_pages, sm_scale, out,
       out_dtype, workspace, workspace_bytes, B, d_status, stream,
-      [&](float* ws, size_t bytes, int* splits) {
+      [&](float* ws, size_t bytes, int* splits, Partials mode) {
         return f16kv_partials(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
-                              out_dtype, ws, bytes, B, d_status, stream, splits);
+                              out_dtype, ws, bytes, B, d_status, stream, splits, mode);
       });
 }
