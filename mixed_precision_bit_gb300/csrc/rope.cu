@@ -2,11 +2,14 @@
 // pass of its own (before quantize_pages, a prefill or a fused step), and on the way
 // into the packed cache's tails or the 16-bit cache's pages.
 //
-// What bounds them: bytes.  Every row is read once and written once, and a row's
-// arithmetic (about ten operations a channel) is far below the memory rate; the
-// sines of a token are computed once, by one thread a pair, and shared by its heads
-// through shared memory.  One block takes a token: 16 lanes a row, so a row's sum of
-// squares is four shuffles, and both channels of a pair are in one lane.
+// What bounds them.  Every row is read once and written once: bytes, with many heads a token
+// (4095 tokens of 80 half-rotated rows 25.0 us, 89% of the copy rate).  With fewer heads the
+// issue of instructions comes near it (8192 tokens of 40 rows 32.6 us, 76%; 73 to 76% of issue
+// slots): a token's sines, computed once, by one thread a pair, and shared by its heads
+// through shared memory, and per row the norm's sum (four shuffles over 16 lanes), the
+// rotation (both channels of a pair in one lane, two pairs an instruction) and the
+// conversions.  A few tokens take one launch's latency, 2.5 to 5 us.  One block takes a token,
+// so that nothing but its own position stands between its loads and its sines.
 #include "rope.cuh"
 #include "grid_dep.cuh"
 #include "host_common.h"
@@ -21,7 +24,8 @@ namespace {
 // query and key rows in two rounds, 16 blocks an SM), few tokens 256 threads with three (48
 // rows in one round: the shortest block).  Measured, us: 8192 tokens of 40 rows 32.9 against 48.6
 // (128 threads: 35.0 to 39.1), 64 tokens 4.9 against 3.2; 8180 appended tokens of 48 rows 43.8
-// against 58.8, 64 tokens 7.7 against 4.5.
+// against 58.8, 64 tokens 7.7 against 4.5 (before the arithmetic took two pairs at a time:
+// now 32.6, 2.6, 42.0 and 4.0 as chosen).
 struct ManyTokens {
   static constexpr int kThreads = 64, kAhead = 5, kBlocks = 16;
 };

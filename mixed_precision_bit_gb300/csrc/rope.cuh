@@ -48,10 +48,14 @@ __device__ __forceinline__ void rope_angles(const RopeParams& p, int64_t positio
 //   half layout   lanes below rot / 8: c0 = 4 lane, c1 = c0 + rot / 2 (pair i: c0 + i, c1 + i)
 //   interleaved   c0 = 8 lane, c1 = c0 + 4 (pairs c0, c0 + 1; c0 + 2, ..)
 // and the channels past rot, eight a lane, in the other lanes.  Rot is a multiple of 16,
-// so every four are 8-byte aligned.  c, s: the four pairs' coefficients.
+// so every four are 8-byte aligned.  In registers the first and second channels of the pairs
+// are two words each (by byte permutations that the layout picks: a, b = first words of both
+// fours, then their second words), so the arithmetic takes two pairs at a time.  c, s: the
+// coefficients of pairs (0, 1), (2, 3); interleaved: of pairs (0, 2), (1, 3).
 struct RopeLane {
-  float c[4], s[4];
+  uint64_t c[2], s[2], ns[2];  // ns = -s
   int c0, c1;
+  uint32_t first, second;  // the permutations
   bool on, interleaved;  // on: this lane's channels rotate
 };
 
@@ -64,17 +68,39 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeParams& p) {
   if (L.interleaved) L.c0 = 8 * lane;
   else L.c0 = L.on ? 4 * lane : p.rot + 8 * (lane - h / 4);
   L.c1 = !L.interleaved && L.on ? L.c0 + h : L.c0 + 4;
+  L.first = L.interleaved ? 0x5410u : 0x3210u;
+  L.second = L.interleaved ? 0x7632u : 0x7654u;
   return L;
 }
 
 // Its pairs' coefficients, from the block's table.
 __device__ __forceinline__ void rope_coefficients(RopeLane& L, const float2* cs) {
+  const float2* at = cs + (L.interleaved ? L.c0 / 2 : L.c0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = L.on ? cs[(L.interleaved ? L.c0 / 2 : L.c0) + i] : make_float2(1.f, 0.f);
-    L.c[i] = a.x;
-    L.s[i] = a.y;
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = L.on ? at[L.interleaved ? i : 2 * i] : make_float2(1.f, 0.f);
+    const float2 b = L.on ? at[L.interleaved ? i + 2 : 2 * i + 1] : make_float2(1.f, 0.f);
+    L.c[i] = f2pack(a.x, b.x);
+    L.s[i] = f2pack(a.y, b.y);
+    L.ns[i] = f2pack(-a.y, -b.y);
   }
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Both fours' words to (first, second) channels of the pairs, and back.
+__device__ __forceinline__ uint4 rope_permute(uint4 x, const RopeLane& L) {
+  return make_uint4(__byte_perm(x.x, x.z, L.first), __byte_perm(x.y, x.w, L.first),
+                    __byte_perm(x.x, x.z, L.second), __byte_perm(x.y, x.w, L.second));
 }
 
 template <int DT>
@@ -108,22 +134,25 @@ __device__ __forceinline__ uint4 rope_weights(const uint16_t* w, const RopeLane&
   return make_uint4(two(L.c0), two(L.c0 + 2), two(L.c1), two(L.c1 + 2));
 }
 
-// One row: x = this lane's eight channels in, normed and rotated out.  Called by whole warps;
-// rows are 16 lanes, so a warp takes two.
+// One row: x = this lane's eight channels in, normed and rotated out (weight: permuted).  Called
+// by whole warps; rows are 16 lanes, so a warp takes two.  any: a row of the warp may be normed.
 template <int DT>
-__device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, uint4 weight, bool norm, float eps) {
-  float f[8];
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w}, w[4] = {weight.x, weight.y, weight.z, weight.w};
+__device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, uint4 weight, bool any, bool norm, float eps) {
+  const uint4 y = rope_permute(x, L);
+  const uint32_t in[4] = {y.x, y.y, y.z, y.w}, w[4] = {weight.x, weight.y, weight.z, weight.w};
+  uint64_t f[4];  // first channels of two pairs, of two more; second channels
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = unpack16<DT>(in[i]);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
+    f[i] = f2pack(v.x, v.y);
   }
-  if (__any_sync(0xFFFFFFFFu, norm)) {  // the warp's two rows may be a query's and a key's
-    float ss = 0.f;
+  if (any) {
+    uint64_t s2 = mul2(f[0], f[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+    for (int i = 1; i < 4; ++i) s2 = fma2(f[i], f[i], s2);
+    float ss, s1;
+    f2unpack(s2, ss, s1);
+    ss += s1;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
     const float r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
@@ -131,27 +160,26 @@ __device__ __forceinline__ uint4 rope_row(uint4 x, const RopeLane& L, uint4 weig
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 v = unpack16<DT>(w[i]);
-        f[2 * i] = f[2 * i] * r * v.x;
-        f[2 * i + 1] = f[2 * i + 1] * r * v.y;
+        f[i] = mul2(mul2(f[i], f2pack(r, r)), f2pack(v.x, v.y));
       }
     }
   }
   if (L.on) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = L.interleaved ? f[2 * i] : f[i], b = L.interleaved ? f[2 * i + 1] : f[4 + i];
-      const float ya = fmaf(a, L.c[i], -b * L.s[i]), yb = fmaf(b, L.c[i], a * L.s[i]);
-      if (L.interleaved) {
-        f[2 * i] = ya;
-        f[2 * i + 1] = yb;
-      } else {
-        f[i] = ya;
-        f[4 + i] = yb;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t a = f[i], b = f[2 + i];
+      f[i] = fma2(a, L.c[i], mul2(b, L.ns[i]));
+      f[2 + i] = fma2(b, L.c[i], mul2(a, L.s[i]));
     }
   }
-  return make_uint4(pack16<DT>(f[0], f[1]), pack16<DT>(f[2], f[3]), pack16<DT>(f[4], f[5]),
-                    pack16<DT>(f[6], f[7]));
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2unpack(f[i], lo, hi);
+    o[i] = pack16<DT>(lo, hi);
+  }
+  return rope_permute(make_uint4(o[0], o[1], o[2], o[3]), L);  // its own inverse
 }
 
 // The rows of one token: H1 query rows and H2 key rows through rope_row, H2 value
@@ -164,8 +192,8 @@ struct TokenRows {
   int H1, H2;
   __device__ int rows() const { return H1 + (v != nullptr ? 2 : 1) * H2; }
   __device__ const uint16_t* in(int i) const {
-    if (i < H1) return q + (size_t)i * kD;
-    return i < H1 + H2 ? k + (size_t)(i - H1) * kD : v + (size_t)(i - H1 - H2) * kD;
+    const uint16_t* base = i < H1 ? q : i < H1 + H2 ? k - (ptrdiff_t)H1 * kD : v - (ptrdiff_t)(H1 + H2) * kD;
+    return base + (ptrdiff_t)i * kD;
   }
   __device__ uint16_t* out(int i) const {
     if (i < H1) return qo + (size_t)i * kD;
@@ -193,7 +221,8 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, RopeLane& L, con
                                            uint4 (&x)[AHEAD]) {
   const int grp = threadIdx.x / kRowLanes, n = t.rows();
   rope_coefficients(L, cs);
-  const uint4 wq = rope_weights(p.q_weight, L), wk = rope_weights(p.k_weight, L);
+  const uint4 wq = rope_permute(rope_weights(p.q_weight, L), L), wk = rope_permute(rope_weights(p.k_weight, L), L);
+  const bool any = p.q_weight != nullptr || p.k_weight != nullptr;
   constexpr int kStep = THREADS / kRowLanes;
   for (int r0 = 0; r0 < n; r0 += AHEAD * kStep) {
     if (r0 > 0) rope_load<THREADS>(t, L, r0, x);
@@ -206,7 +235,7 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, RopeLane& L, con
       if (first < t.H1 + t.H2) {  // some row of the step rotates: whole warps take part
         const bool key = i >= t.H1;
         const bool norm = (key ? p.k_weight : p.q_weight) != nullptr;
-        const uint4 z = rope_row<DT>(x[u], L, key ? wk : wq, norm, p.eps);
+        const uint4 z = rope_row<DT>(x[u], L, key ? wk : wq, any, norm, p.eps);
         if (i < t.H1 + t.H2) y = z;
       }
       if (i < n) rope_put(t.out(i), L, y);
