@@ -3,7 +3,7 @@
 // into the packed cache's tails or the 16-bit cache's pages.
 //
 // What bounds them.  Every row is read once and written once: bytes, with many heads a token
-// (4095 tokens of 80 half-rotated rows 25.0 us, 89% of the copy rate).  With fewer heads the
+// (4095 tokens of 72 half-rotated rows without a norm 25.0 us, 89% of the copy rate).  With fewer heads the
 // issue of instructions comes near it (8192 tokens of 40 rows 32.6 us, 76%; 73 to 76% of issue
 // slots): a token's sines, computed once, by one thread a pair, and shared by its heads
 // through shared memory, and per row the norm's sum (four shuffles over 16 lanes), the
