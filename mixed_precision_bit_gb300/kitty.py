@@ -381,6 +381,8 @@ def _device():
     return torch.cuda.current_device()
 
 
+# Each check below is one expression over a tensor's attributes, and says what was wrong only
+# when it fails: a call of a few microseconds on the device takes a dozen tensors.
 def _here(t, dev: int):
     if t.get_device() != dev:  # -1: host memory
         if not t.is_cuda:
@@ -392,8 +394,8 @@ def _dense(t, dev: int):
     """Device address of a dense array on the current device (None: null)."""
     if t is None:
         return None
-    _here(t, dev)
-    if not t.is_contiguous():
+    if t.get_device() != dev or not t.is_contiguous():
+        _here(t, dev)
         raise ValueError("kitty: tensor arguments must be contiguous (shape %s, strides %s)"
                          % (tuple(t.shape), t.stride()))
     return t.data_ptr()
@@ -407,9 +409,9 @@ def _rows(t, n: int, heads: int, dev: int):
     if t.shape != (n, heads, D) or t.element_size() != 2:
         raise ValueError("kitty: expected 16-bit rows [%d, %d, %d] (got %s, %s)"
                          % (n, heads, D, tuple(t.shape), t.dtype))
-    _here(t, dev)
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != D):
+    if s2 != 1 or (s1 != D and heads > 1) or t.get_device() != dev:
+        _here(t, dev)
         raise ValueError("kitty: the heads of a token must be contiguous (strides %s)" % (t.stride(),))
     # the stride between tokens of one token says nothing
     return t.data_ptr(), s0 if n > 1 else heads * D
@@ -422,14 +424,17 @@ def _ints(name: str, t, n: int, dev: int):
     if t.element_size() != 4 or t.is_floating_point() or t.numel() < n:
         raise ValueError("kitty: %s must be int32 with %d entries (got %s, %s)"
                          % (name, n, tuple(t.shape), t.dtype))
-    return _dense(t, dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        _dense(t, dev)
+    return t.data_ptr()
 
 
 def _table(t, B: int, dev: int):
     """(address, entries of a row) of a block table [>= B, max_pages]."""
-    if t.dim() != 2 or t.shape[0] < B:
-        raise ValueError("kitty: the block table must be [%d, max_pages] (got %s)" % (B, tuple(t.shape)))
-    return _ints("block_table", t, 0, dev), t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < B:
+        raise ValueError("kitty: the block table must be [%d, max_pages] (got %s)" % (B, tuple(shape)))
+    return _ints("block_table", t, 0, dev), shape[1]
 
 
 def _raw_stream(stream, dev: int):
