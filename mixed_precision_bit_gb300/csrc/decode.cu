@@ -1763,7 +1763,7 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
               const void* tail_k, const void* tail_v, const int32_t* tail_len, float sm_scale,
               void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes_in, int32_t B,
               int32_t* d_status, void* stream, const AppendParams& ap, int* partial_splits = nullptr,
-              Partials mode = Partials::kLaunch) {
+              const GridAhead* ahead = nullptr) {
   int rc = check_cfg(cfg, kMaxGroup);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
@@ -1785,8 +1785,6 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
   if (workspace_bytes_in < need || (need > 0 && (!workspace || !aligned16(workspace))))
     return KITTY_ERR_WORKSPACE;
   if (partial_splits != nullptr) *partial_splits = sc.splits;
-  if (mode == Partials::kCheck) return KITTY_OK;
-  const bool behind = mode == Partials::kBehind;
   for (int i = 0; i <= sc.splits; ++i) p.starts[i] = sc.starts[i];
   p.ap = ap;
   p.q = static_cast<const uint16_t*>(q);
@@ -1817,6 +1815,8 @@ int attention(const kitty_cfg* cfg, const void* q, const void* pool, int32_t poo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   dim3 grid((unsigned)B * cfg->num_kv_heads * p.HG, sc.splits);
   const int nx = cfg->n_hi / 16, v = v_bits(cfg);
+  const bool behind = ahead != nullptr;
+  if (behind && (rc = ahead->launch(ahead->arg)) != KITTY_OK) return rc;
   const cudaError_t e = h8 ? (cfg->in_dtype == KITTY_BF16 ? launch_decode8_nx<KITTY_BF16>(nx, grid, smem, s, behind, p)
                                                           : launch_decode8_nx<KITTY_F16>(nx, grid, smem, s, behind, p))
       : cfg->in_dtype == KITTY_BF16
@@ -1918,11 +1918,12 @@ int kitty::decode_partials(const kitty_cfg* cfg, const void* q, const void* pool
                            const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
                            const void* tail_k, const void* tail_v, const int32_t* tail_len,
                            float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
-                           int32_t B, int32_t* d_status, void* stream, int* splits, Partials mode) {
+                           int32_t B, int32_t* d_status, void* stream, int* splits,
+                           const GridAhead* ahead) {
   const AppendParams none = {};
   return attention(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k, tail_v,
                    tail_len, sm_scale, out, out_dtype, ws, ws_bytes, B, d_status, stream, none, splits,
-                   mode);
+                   ahead);
 }
 
 // ------------------------------------------------------------------ no-allocation variant

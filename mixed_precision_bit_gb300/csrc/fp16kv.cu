@@ -465,8 +465,8 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
                     const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
                     float sm_scale, void* out, int32_t out_dtype, void* workspace,
                     size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream,
-                    int* partial_splits, Partials mode) {
-  const int rc = check_cfg(cfg, 4);
+                    int* partial_splits, const GridAhead* ahead) {
+  int rc = check_cfg(cfg, 4);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || max_pages < 0 || pool_pages < 0) return KITTY_ERR_INVALID_ARG;
   if (out_dtype != KITTY_F32 && out_dtype != KITTY_BF16 && out_dtype != KITTY_F16)
@@ -483,8 +483,6 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
       p.splits > 1 ? (size_t)B * cfg->num_q_heads * p.splits * kFPartial * sizeof(float) : 0;
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned16(workspace))))
     return KITTY_ERR_WORKSPACE;
-  if (mode == Partials::kCheck) return KITTY_OK;
-  const bool behind = mode == Partials::kBehind;
   p.q = static_cast<const uint16_t*>(q);
   p.pool = static_cast<const uint8_t*>(pool);
   p.block_table = block_table;
@@ -501,6 +499,8 @@ int f16kv_attention(const kitty_cfg* cfg, const void* q, const void* pool, int32
   p.g = cfg->num_q_heads / cfg->num_kv_heads;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)B * cfg->num_kv_heads, p.splits);
+  const bool behind = ahead != nullptr;
+  if (behind && (rc = ahead->launch(ahead->arg)) != KITTY_OK) return rc;
   const cudaError_t e = cfg->in_dtype == KITTY_BF16 ? launch_f16kv<KITTY_BF16>(grid, s, behind, p)
                                                     : launch_f16kv<KITTY_F16>(grid, s, behind, p);
   if (e != cudaSuccess) return KITTY_ERR_CUDA;
@@ -518,7 +518,7 @@ extern "C" int kitty_f16kv_decode(const kitty_cfg* cfg, const void* q, const voi
                                   void* stream) {
   return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
                          out_dtype, workspace, workspace_bytes, B, d_status, stream, nullptr,
-                         Partials::kLaunch);
+                         nullptr);
 }
 
 size_t kitty::f16kv_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
@@ -530,7 +530,8 @@ size_t kitty::f16kv_partial_bytes(const kitty_cfg* cfg, int B, int max_pages) {
 int kitty::f16kv_partials(const kitty_cfg* cfg, const void* q, const void* pool, int32_t pool_pages,
                           const int32_t* block_table, int32_t max_pages, const int32_t* ctx_len,
                           float sm_scale, void* out, int32_t out_dtype, float* ws, size_t ws_bytes,
-                          int32_t B, int32_t* d_status, void* stream, int* splits, Partials mode) {
+                          int32_t B, int32_t* d_status, void* stream, int* splits,
+                          const GridAhead* ahead) {
   return f16kv_attention(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
-                         out_dtype, ws, ws_bytes, B, d_status, stream, splits, mode);
+                         out_dtype, ws, ws_bytes, B, d_status, stream, splits, ahead);
 }

@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kitty.h"
 
 namespace kitty {
@@ -40,9 +42,12 @@ inline int check_cfg(const kitty_cfg* c, int max_group = 0) {
 // Streaming multiprocessors of the current device (148 if it cannot be read);
 // for the CUDA translation units (host.cpp is built without the CUDA headers).
 inline int sm_count() {
+  static std::atomic<int> known[64];  // by device; 0: not asked yet
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 #endif

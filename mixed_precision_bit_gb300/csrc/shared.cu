@@ -144,56 +144,61 @@ int workspace(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pa
   return KITTY_OK;
 }
 
-// Checks, the own pages' partials (`own` launches them behind the prefix's in the
-// workspace), the prefix kernel and the merge.
+// Launches the prefix kernel, for GridAhead.
+struct PrefixCall {
+  const kitty_cfg* cfg;
+  bool packed;
+  PrefixArgs args;
+  PrefixPlan plan;
+  cudaStream_t stream;
+  static int launch(void* arg) {
+    const PrefixCall* c = static_cast<const PrefixCall*>(arg);
+    return prefix_launch(c->cfg, c->packed, c->args, c->plan, c->stream);
+  }
+};
+
+// Checks; then the prefix kernel, the own pages' partials (`own` checks the rest and launches
+// both) behind the prefix's in the workspace, and the merge.
 template <class Own>
 int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const void* pool,
                      int32_t pool_pages, const int32_t* prefix_table, int32_t n_prefix,
                      const int32_t* prefix_pages, int32_t max_pages, float sm_scale, void* out,
                      int32_t out_dtype, void* ws, size_t ws_bytes, int32_t B, int32_t* d_status,
                      void* stream, Own own) {
-  size_t need = 0;
-  int rc = workspace(cfg, packed, B, n_prefix, max_pages, &need);
+  int rc = check_shared(cfg, packed, B, n_prefix, max_pages);
   if (rc != KITTY_OK) return rc;
   if (n_prefix > 0 && (!prefix_table || !pool || !aligned16(pool))) return KITTY_ERR_INVALID_ARG;
   if (B == 0) return KITTY_OK;
   if (q && !aligned16(q)) return KITTY_ERR_INVALID_ARG;
-  if (ws_bytes < need || !ws || !aligned16(ws)) return KITTY_ERR_WORKSPACE;
-  const PrefixPlan plan = prefix_plan(cfg, packed, B, n_prefix, max_pages);
-  const size_t mine = prefix_bytes(cfg, plan, B);
-  float* own_ws = static_cast<float*>(ws) + mine / sizeof(float);
-  MergeParams m = {static_cast<float*>(ws), own_ws, out, d_status, plan.slots, 0, B * cfg->num_q_heads, out_dtype, aligned16(out)};
-  rc = own(own_ws, ws_bytes - mine, &m.nb, Partials::kCheck);
-  if (rc != KITTY_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (plan.splits > 0) {
-    PrefixArgs p = {};
-    p.q = static_cast<const uint16_t*>(q);
-    p.pool = static_cast<const uint8_t*>(pool);
-    p.table = prefix_table;
-    p.prefix_pages = prefix_pages;
-    p.ws = static_cast<float*>(ws);
-    p.d_status = d_status;
-    p.sm_log2 = sm_scale * 1.4426950408889634f;
-    p.wait_polls = cfg->decode_wait_polls > 0 ? (uint32_t)cfg->decode_wait_polls : 1u << 22;
-    p.pool_pages = pool_pages;
-    p.n_prefix = n_prefix;
-    p.B = B;
-    p.Hq = cfg->num_q_heads;
-    p.Hkv = cfg->num_kv_heads;
-    p.g = p.Hq / p.Hkv;
-    p.n_hi = cfg->n_hi;
-    p.blob = (int)blob_bytes(cfg->n_hi, cfg->lo_bit, v_bits(cfg));
-    p.in_dtype = cfg->in_dtype;
-    p.splits = plan.splits;
-    p.slots = plan.slots;
-    rc = prefix_launch(cfg, packed, p, plan, s);
-    if (rc != KITTY_OK) return rc;
-  }
-  rc = own(own_ws, ws_bytes - mine, &m.nb, plan.splits > 0 ? Partials::kBehind : Partials::kLaunch);
+  PrefixCall call = {cfg, packed, {}, prefix_plan(cfg, packed, B, n_prefix, max_pages), s};
+  const size_t mine = prefix_bytes(cfg, call.plan, B);
+  if (ws_bytes < mine || !ws || !aligned16(ws)) return KITTY_ERR_WORKSPACE;
+  float* own_ws = static_cast<float*>(ws) + mine / sizeof(float);
+  PrefixArgs& p = call.args;
+  p.q = static_cast<const uint16_t*>(q);
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.table = prefix_table;
+  p.prefix_pages = prefix_pages;
+  p.ws = static_cast<float*>(ws);
+  p.d_status = d_status;
+  p.sm_log2 = sm_scale * 1.4426950408889634f;
+  p.wait_polls = cfg->decode_wait_polls > 0 ? (uint32_t)cfg->decode_wait_polls : 1u << 22;
+  p.pool_pages = pool_pages;
+  p.n_prefix = n_prefix;
+  p.B = B;
+  p.Hq = cfg->num_q_heads;
+  p.Hkv = cfg->num_kv_heads;
+  p.g = p.Hq / p.Hkv;
+  p.n_hi = cfg->n_hi;
+  p.blob = (int)blob_bytes(cfg->n_hi, cfg->lo_bit, v_bits(cfg));
+  p.in_dtype = cfg->in_dtype;
+  p.splits = call.plan.splits;
+  p.slots = call.plan.slots;
+  MergeParams m = {static_cast<float*>(ws), own_ws, out, d_status, call.plan.slots, 0, B * cfg->num_q_heads, out_dtype, aligned16(out)};
+  const GridAhead ahead = {PrefixCall::launch, &call};
+  rc = own(own_ws, ws_bytes - mine, &m.nb, call.plan.splits > 0 ? &ahead : nullptr);
   if (rc != KITTY_OK) return rc;
-  // warps a row by its partials, eight requests in flight a warp (8192 rows of 11: 11.6 us
-  // cold with two, 18.8 with four that waited for the maxima first)
   const int n = m.na + m.nb;
   const cudaError_t e = n <= kAhead
       ? launch_dependent(merge_kernel<1>, dim3((unsigned)((m.rows + 3) / 4)), 128, 0, s, m)
@@ -227,10 +232,10 @@ extern "C" int kitty_decode_attention_shared(
   return shared_attention(
       cfg, true, q, pool, pool_pages, prefix_table, n_prefix, prefix_pages, max_pages, sm_scale, out,
       out_dtype, workspace, workspace_bytes, B, d_status, stream,
-      [&](float* ws, size_t bytes, int* splits, Partials mode) {
+      [&](float* ws, size_t bytes, int* splits, const GridAhead* ahead) {
         return decode_partials(cfg, q, pool, pool_pages, block_table, max_pages, num_pages, tail_k,
                                tail_v, tail_len, sm_scale, out, out_dtype, ws, bytes, B, d_status,
-                               stream, splits, mode);
+                               stream, splits, ahead);
       });
 }
 
@@ -244,8 +249,8 @@ extern "C" int kitty_f16kv_decode_shared(const kitty_cfg* cfg, const void* q, co
   return shared_attention(
       cfg, false, q, pool, pool_pages, prefix_table, n_prefix, prefix_pages, max_pages, sm_scale, out,
       out_dtype, workspace, workspace_bytes, B, d_status, stream,
-      [&](float* ws, size_t bytes, int* splits, Partials mode) {
+      [&](float* ws, size_t bytes, int* splits, const GridAhead* ahead) {
         return f16kv_partials(cfg, q, pool, pool_pages, block_table, max_pages, ctx_len, sm_scale, out,
-                              out_dtype, ws, bytes, B, d_status, stream, splits, mode);
+                              out_dtype, ws, bytes, B, d_status, stream, splits, ahead);
       });
 }
