@@ -308,8 +308,9 @@ int kitty_decode_attention_noalloc(const kitty_cfg* cfg, const void* q, const vo
  *                 shares fewer pages; 0: none), or NULL: all share all n_prefix pages.  A
  *                 value outside sets KITTY_ST_BAD_LEN and counts as 0
  *   q             16-byte aligned
- *   workspace     device, >= kitty_shared_workspace_bytes(cfg, B, n_prefix, max_pages),
- *                 16-byte aligned; calls that may overlap need one each
+ *   workspace     device, >= kitty_shared_workspace_bytes(cfg, B, n_prefix, max_pages) of the
+ *                 same cfg (its plan hints, decode_total_pages: the sequences' own pages, set
+ *                 the splits), 16-byte aligned; calls that may overlap need one each
  * Other arguments, layouts and status codes as for kitty_decode_attention.  A prefix page
  * id out of range sets KITTY_ST_BAD_PAGE and its tokens are left out.  A sequence is not
  * affected by what prefix pages hold that it does not share.  A prefix page with a stored

@@ -28,7 +28,9 @@ inline cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, s
   lc.stream = s;
   lc.attrs = attr;
   lc.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, kernel, P(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, P(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // reported here, not by a later call
+  return e;
 }
 
 template <class... P, class... A>

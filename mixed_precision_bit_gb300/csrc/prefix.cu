@@ -20,12 +20,16 @@
 //   Keys    step * code, exact (a step has 7 significant bits, a code 2 or 4); the page's
 //           channel minima as one more row, so that Q K^T also gives q.M, which the
 //           softmax adds to the page's 32 scores;
-//   Values  step * code, exact, transposed; each token's four group minima as four more
+//   Values  step * (code - half the largest code), exact, transposed; the middles of each
+//           token's four groups (minimum + half the largest code * step) as four more
 //           channels, which the end adds to the channels of their group; and a channel of
 //           ones, whose column of O is the sum of the rounded p.
-// So the only roundings are p to fp16 and, for 8-bit boosted Keys, step * code to fp16; and
-// with the sum taken over the rounded p, theirs shift an output by at most 2^-11 of
-// sum p |v - out|.
+// So the roundings are p to fp16, a group's middle to fp16 (2^-11 of it at most, once) and, for
+// 8-bit boosted Keys, step * code to fp16; with the sum taken over the rounded p, theirs shift
+// an output by at most 2^-11 of sum p |v - out|.  Why middles: codes from 0 and minima, which
+// are exact, are sums that grow with the context and cancel, and the products' fp32
+// accumulation rounds them one way: 16000 tokens a block left outputs off by 3.6e-3 of their
+// RMS, all to one side.  Centered, both sums stay near the output's size.
 //
 // What bounds it.  Packed, 128 sequences of 64/8 heads behind 32768 tokens (32 x 4 blocks of 86
 // tiles): 1.7 us a tile of both lanes; of the issue slots of the SMs in use 64% are taken (97.6 M
@@ -76,7 +80,7 @@ struct PackedFmt {
   static constexpr bool kPacked = true, kBf16 = false, kPair = false;
   static constexpr int W = W_, V = V_, kPages = 3, kTok = 96;
   static constexpr int kS = 112;          // columns of S: 96 scores, 3 of q.M (16 is the granule)
-  static constexpr int kO = 144;          // columns of O: 128 channels, 4 group minima, the sum of p
+  static constexpr int kO = 144;          // columns of O: 128 channels, 4 group middles, the sum of p
   static constexpr int kKHalf = kS * 128, kKBytes = 2 * kKHalf;
   static constexpr int kSlab = kO * 64;   // a page's Values: [channel][64 bytes]
   static constexpr int kVBytes = kPages * kSlab;
@@ -174,14 +178,15 @@ __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) { return h2_bi
 // Both halves' codes of class K of a plane word as fp16 integers.  2-bit planes: class
 // K = token or channel block 0..3, at bits 2K + 2; 4-bit planes: K = 0, 1, at bits 4K + 2.  A
 // code under the exponent of 1024 reads 1024 + code * 2^shift; one fused multiply-add
-// takes both off, exactly.
-template <int BITS, int K>
+// takes both off, exactly.  CENTERED: minus half the largest code, as exact.
+template <int BITS, int K, bool CENTERED = false>
 __device__ __forceinline__ uint32_t codes(uint32_t x) {
   constexpr int shift = BITS * K + 2;
   constexpr uint32_t mask = (((1u << BITS) - 1u) << shift) * 0x00010001u;
   const uint32_t y = (x & mask) | 0x64006400u;
   constexpr uint32_t inv = ((15u - shift) << 10) * 0x00010001u;             // 2^-shift
-  constexpr uint32_t off = ((25u - shift) << 10 | 0x8000u) * 0x00010001u;  // -1024 * 2^-shift
+  constexpr uint32_t half = CENTERED ? ((1u << BITS) - 1u) << (shift - 1) : 0u;  // in the mantissa's units
+  constexpr uint32_t off = ((25u - shift) << 10 | 0x8000u | half) * 0x00010001u;  // -1024 * 2^-shift - half
   return h2_bits(__hfma2(bits_h2(y), bits_h2(inv), bits_h2(off)));
 }
 
@@ -297,7 +302,7 @@ __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page,
 }
 
 // A page's Value part (staged at raw: plane, steps, minima) to its slab, channels as rows of
-// 32 tokens, the four groups' minima as rows 128 .. 131.  (Rolled over pairs of groups: loading
+// 32 tokens, the four groups' middles as rows 128 .. 131.  (Rolled over pairs of groups: loading
 // warps, softmax and products share one instruction cache; with everything unrolled the
 // first page of a block took 4000 to 8700 cycles, each later one 2200 to 3300.)
 template <class F>
@@ -331,24 +336,26 @@ __device__ __forceinline__ void put_values(uint32_t raw, uint32_t slab, int32_t*
           for (int mc = 0; mc < V / 2; ++mc) {
             const uint32_t y = w[V * G + V / 2 * kt + mc], x = h ? __funnelshift_r(y, y, 8) : y;
             if (V == 2) {
-              sts32(at, h2mul(codes<2, 0>(x), s));
-              sts32(at + 512, h2mul(codes<2, 1>(x), s));
-              sts32(at + 1024, h2mul(codes<2, 2>(x), s));
-              sts32(at + 1536, h2mul(codes<2, 3>(x), s));
+              sts32(at, h2mul(codes<2, 0, true>(x), s));
+              sts32(at + 512, h2mul(codes<2, 1, true>(x), s));
+              sts32(at + 1024, h2mul(codes<2, 2, true>(x), s));
+              sts32(at + 1536, h2mul(codes<2, 3, true>(x), s));
             } else {
-              sts32(at + 1024 * mc, h2mul(codes<4, 0>(x), s));
-              sts32(at + 1024 * mc + 512, h2mul(codes<4, 1>(x), s));
+              sts32(at + 1024 * mc, h2mul(codes<4, 0, true>(x), s));
+              sts32(at + 1024 * mc + 512, h2mul(codes<4, 1, true>(x), s));
             }
           }
         }
       }
     }
   }
-  if (r < 4) {  // group r's minima of the tokens of column qq
-    const uint4 m4 = lds128(vm + 64 * r + 16 * qq);
-    const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
+  if (r < 4) {  // group r's middles of the tokens of column qq
+    const uint4 m4 = lds128(vm + 64 * r + 16 * qq), s4 = lds128(vs + 64 * r + 16 * qq);
+    const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w}, S[4] = {s4.x, s4.y, s4.z, s4.w};
+    const uint32_t half = V == 2 ? 0x3E003E00u : 0x47804780u;  // 1.5, 7.5
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sts32(slab + (kD + r) * 64 + ((i ^ sw) << 4) + 4 * qq, m[i]);
+    for (int i = 0; i < 4; ++i)
+      sts32(slab + (kD + r) * 64 + ((i ^ sw) << 4) + 4 * qq, h2_bits(__hfma2(bits_h2(S[i]), bits_h2(half), bits_h2(m[i]))));
   }
   if (step_too_large<V>(lds32(vs + 4 * lane)) || step_too_large<V>(lds32(vs + 128 + 4 * lane)))
     set_status(d_status, KITTY_ST_RANGE);
@@ -493,7 +500,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     if (p.prefix_pages != nullptr) my_pages = p.prefix_pages[b];
   }
   if (tid < kRows) sh.row[tid] = real ? (int)part_row : -1;
-  if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's minima
+  if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's middles
     const uint32_t at = vst + (tid / (4 * F::kPages)) * F::kVBytes + (tid / 4 % F::kPages) * F::kSlab + (kD + 4) * 64;
     sts128(at + 16 * (tid & 3), make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u));
     fence_async_shared();

@@ -138,9 +138,10 @@ int workspace(const kitty_cfg* cfg, bool packed, int B, int n_prefix, int max_pa
   const int rc = check_shared(cfg, packed, B, n_prefix, max_pages);
   if (rc != KITTY_OK) return rc;
   if (!bytes) return KITTY_ERR_INVALID_ARG;
-  *bytes = B == 0 ? 0
-                  : prefix_bytes(cfg, prefix_plan(cfg, packed, B, n_prefix, max_pages), B) + (packed ? decode_partial_bytes(cfg, B, max_pages)
-                                                             : f16kv_partial_bytes(cfg, B, max_pages));
+  *bytes = 0;
+  if (B == 0) return KITTY_OK;
+  *bytes = prefix_bytes(cfg, prefix_plan(cfg, packed, B, n_prefix, max_pages), B) +
+           (packed ? decode_partial_bytes(cfg, B, max_pages) : f16kv_partial_bytes(cfg, B, max_pages));
   return KITTY_OK;
 }
 

@@ -123,6 +123,28 @@ def test_two_calls_at_once(kind):
         assert all(torch.equal(x, y) for x, y in zip(outs, want))
 
 
+@pytest.mark.parametrize("kind", [Packed, Plain16])
+def test_the_merge_waits_for_a_prefix_that_ends_last(kind):
+    """Hardly any own tokens: their kernel has long ended when the prefix's does, in a graph and
+    in direct calls, with a workspace that holds NaN before each."""
+    import torch
+    own = dict(own=[0] * 3, tails=[1, 0, 2]) if kind is Packed else dict(lens=[1, 0, 2])
+    c = kind(Hkv=1, Hq=4, dt=BF16, n_prefix=6000, shared=None, seed=45, **own)
+    c.cfg.decode_total_pages = 1 << 20   # a hint far too high: the prefix on few blocks
+    ws = c.workspace()
+    out = torch.zeros(c.B, c.Hq, D, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(out, ws=ws)
+    ref, _ = c.oracle()
+    for step in range(6):
+        ws.fill_(float("nan"))
+        out.zero_()
+        g.replay() if step % 2 else c.call(out, ws=ws)
+        torch.cuda.synchronize()
+        assert attn_error(out.cpu().numpy().astype(np.float64), ref)[0] <= 0, step
+
+
 def test_16_bit_offsets_beyond_32_bits():
     """Prefix and own pages more than 4 GiB into the pool."""
     import torch
