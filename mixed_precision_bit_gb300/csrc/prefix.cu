@@ -231,8 +231,8 @@ __device__ __forceinline__ bool put_keys(uint32_t raw, uint32_t stage, int page,
         if (W == 2) {
           sts32(at, h2mul(codes<2, 0>(x), S));
           sts32(at + 1024, h2mul(codes<2, 1>(x), S));
-          sts32(at + 2048, h2mul(codes<2, 2>(x), S));
-          sts32(at + 3072, h2mul(codes<2, 3>(x), S));
+          sts32(at + 2 * 1024, h2mul(codes<2, 2>(x), S));
+          sts32(at + 3 * 1024, h2mul(codes<2, 3>(x), S));
         } else {
           sts32(at + 2048 * mt, h2mul(codes<4, 0>(x), S));
           sts32(at + 2048 * mt + 1024, h2mul(codes<4, 1>(x), S));

@@ -4,10 +4,10 @@ each sequence's prefix pages followed by its own: within the decode's 2e-3 of th
 at most 2^-11 of it, and the sum of the softmax is that of the rounded ones: an output is off
 by sum p d (v - out) with |d| <= 2^-11 and random signs, 2^-11 / sqrt(3) = 2.8e-4 of the output
 RMS (which is that of sum p v with random v): 7 deviations.  16-bit pages keep p in two parts
-(2^-17 or less).  Key
-steps times codes, Key minima and Value steps times centered codes are exact in fp16 for 2- and
-4-bit codes; a Value group's middle is rounded once, by 2^-11 of it, again with random signs
-over the tokens and no larger than v itself: sqrt(2) of the above at most, 5 deviations."""
+(2^-17 or less).  Key steps times codes, Key minima and Value steps times centered codes are
+exact in fp16 for 2- and 4-bit codes; a Value group's middle is rounded once, by 2^-11 of it,
+again with random signs over the tokens and no larger than v itself: sqrt(2) of the above at
+most, 5 deviations."""
 
 import numpy as np
 import pytest
