@@ -9,9 +9,11 @@
 //   p = 2^(s - m)      one thread a row: its scores from tensor memory, the running maximum
 //                      and sum in registers, p back over S as the next product's operand
 //   O += P V           tcgen05.mma with P in tensor memory, fp32 in tensor memory
-// m is not the maximum itself: it is set 2^6 above the first page's, and moves only when a
-// score passes it by more than 2^8 (p then stays <= 256, well inside fp16), so that O is
-// hardly ever rescaled: a rescale costs the lane about a tile's time.
+// m is not the maximum itself: it is set 2^4 below the first tile's, and moves only when a score
+// passes it by more than 2^15, so that O is hardly ever rescaled (a rescale costs the lane about
+// a tile's time) and p <= 32768 stays inside fp16.  It is set below because p has fp16's range
+// downwards, too: what is 2^-25 and less becomes 0, and 15000 tokens of 2^-19 of one large one
+// each are 3% of its sum.  Here they would have to be 2^-29 of it.
 // Warps: 4 a lane for the softmax, one a lane issuing products, the rest loading.  While one
 // lane's softmax runs, the tensor cores work on the other's products.
 //
@@ -71,8 +73,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8;               // and the next: one a lane
 constexpr int kLoadWarp = 10;
 constexpr float kFloor = -1.0e30f;        // a row without a score yet
-constexpr float kSlack = 8.f;             // log2 units the maximum may lag behind ..
-constexpr float kMargin = 6.f;            // .. or run ahead, when it is set
+constexpr float kSlack = 15.f;            // log2 units that a score may pass m by
+constexpr float kMargin = -4.f;           // m against the maximum, when it is set
 
 // Packed pages: Key planes of W bits, Values of V bits.
 template <int W_, int V_>

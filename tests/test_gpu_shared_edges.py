@@ -123,6 +123,31 @@ def test_two_calls_at_once(kind):
         assert all(torch.equal(x, y) for x, y in zip(outs, want))
 
 
+@pytest.mark.parametrize("gap", [17, 19, 21])
+@pytest.mark.parametrize("dt", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("kind", [Packed, Plain16])
+def test_one_large_score_before_many_small_ones(kind, dt, gap):
+    """The first token's score is `gap` log2 units above 30000 others: each weighs 2^-gap of it,
+    together up to a quarter.  On one block (a hint of many own pages), within the 2e-3."""
+    from tests.kitty_cases import dev16
+    n = 960
+    own = dict(own=[0], tails=[1]) if kind is Packed else dict(lens=[1])
+    c = kind(Hkv=1, Hq=1, dt=dt, n_prefix=n, shared=None, seed=46, **own)
+    c.cfg.decode_total_pages = 1 << 20
+    q = synth.from_bits(c.q, dt).astype(np.float64).reshape(D)
+    k = np.random.default_rng(1).standard_normal((n * 32, 1, D)) * 1e-3
+    k[0, 0] = q * gap / ((q * q).sum() * c.sm * np.log2(np.e))
+    k = synth.to_bits(k, dt)
+    if kind is Packed:
+        from mixed_precision_bit_gb300 import kitty
+        kitty.quantize_pages(c.cfg, dev16(k), dev16(c.v[:n * 32]), dev32(c.ids[:n]), c.pool, c.pool_pages)
+    else:
+        c.host[c.prefix, 0, 0] = k.reshape(n, 32, D)
+        c.pool.copy_(dev16(c.host))
+    ref, _ = c.oracle()
+    assert attn_error(c.run("f32"), ref)[0] <= 0
+
+
 @pytest.mark.parametrize("kind", [Packed, Plain16])
 def test_the_merge_waits_for_a_prefix_that_ends_last(kind):
     """Hardly any own tokens: their kernel has long ended when the prefix's does, in a graph and
