@@ -442,7 +442,8 @@ int kitty_append_rope(const kitty_cfg* cfg, const kitty_rope* rope, const void* 
  * Tokens of a page id out of range are skipped (KITTY_ST_BAD_PAGE) and their sequence is not
  * advanced; a sequence without room for its n tokens (KITTY_ST_TABLE_FULL, or
  * KITTY_ST_BAD_LEN for a length outside the table) appends nothing; starts out of order:
- * KITTY_ST_BAD_SEQ. */
+ * KITTY_ST_BAD_SEQ, and a sequence whose tokens are not all its own (token t is that of the
+ * sequence whose index is the number of entries seq_start[1..B] <= t) is not advanced. */
 int kitty_f16kv_append_rope(const kitty_cfg* cfg, const kitty_rope* rope, const void* q,
                             int64_t q_stride, const void* k_new, int64_t k_stride,
                             const void* v_new, int64_t v_stride, int32_t n_tokens, void* q_out,

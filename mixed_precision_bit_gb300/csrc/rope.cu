@@ -136,13 +136,31 @@ __global__ void __launch_bounds__(B::kThreads, B::kBlocks) f16kv_append_rope_ker
 }
 
 // After a ragged append: one warp a sequence enters its new pages in the block table
-// and, if every one of them is a page, advances its length.
+// and, if every one of its tokens was its own and has a page, advances its length.
+// A token goes to the sequence whose index is the number of ends at or before it; that
+// number rises with the token, so a sequence's tokens are all its own if the first and
+// the last are.  With starts out of order some are not: reported, not advanced.
 __global__ void __launch_bounds__(128) f16kv_append_rope_finish(const Append16 p, int n_tokens) {
   grid_wait();
   const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= p.B) return;
-  const int first = p.seq_start[b], n = p.seq_start[b + 1] - first;
-  if (first < 0 || n <= 0 || first > n_tokens - n) return;
+  const int first = p.seq_start[b], end = p.seq_start[b + 1];
+  if (first == end) return;
+  bool mine = first >= 0 && first < end && end <= n_tokens;
+  if (mine) {
+    int c0 = 0, c1 = 0;  // ends at or before the first and the last token
+    for (int s = lane; s < p.B; s += 32) {
+      const int e = p.seq_start[s + 1];
+      c0 += e <= first;
+      c1 += e < end;
+    }
+    mine = __reduce_add_sync(0xFFFFFFFFu, c0) == b && __reduce_add_sync(0xFFFFFFFFu, c1) == b;
+  }
+  if (!mine) {
+    if (lane == 0) set_status(p.d_status, KITTY_ST_BAD_SEQ);
+    return;
+  }
+  const int n = end - first;
   const int before = length_before(p, b, n, false);
   if (before < 0) return;
   bool ok = true;
