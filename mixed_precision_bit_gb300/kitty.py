@@ -358,21 +358,41 @@ class Rope:
         f = np.ascontiguousarray(inv_freq, np.float64)
         turns = np.zeros(f.size, np.uint64)
         _chk("kitty_rope_turns", load().kitty_rope_turns(f.ctypes.data, f.size, turns.ctypes.data))
-        for w in (q_weight, k_weight):
-            if w is not None and (w.numel() != D or w.element_size() != 2):
-                raise ValueError("kitty: norm weights are 16-bit [%d]" % D)
         self.rot_dim, self.layout, self.amplitude, self.eps = 2 * f.size, layout, amplitude, eps
         self.q_weight, self.k_weight = q_weight, k_weight
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
-        self._c = _Rope(self.rot_dim, layout, amplitude, eps, _ptr(self.turns), _ptr(q_weight),
-                        _ptr(k_weight))
-        self._ref = ctypes.byref(self._c)
+        for w in (q_weight, k_weight):
+            self._check_weight(w)
+
+    @staticmethod
+    def _check_weight(w):
+        if w is not None and (w.numel() != D or w.element_size() != 2):
+            raise ValueError("kitty: norm weights are 16-bit [%d]" % D)
+        _ptr(w)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_ref", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
 
     def ref(self, dev: int):
-        for t in (self.turns, self.q_weight, self.k_weight):
-            if t is not None:
-                _here(t, dev)
-        return self._ref
+        """A reference to the C structure of the fields as they are, kept until one changes, a
+        tensor's memory moves or the device does."""
+        t, q, k = self.turns, self.q_weight, self.k_weight
+        at = (dev, t.data_ptr(), q is not None and q.data_ptr(), k is not None and k.data_ptr())
+        r = self.__dict__.get("_ref")
+        if r is None or r[0] != at:
+            for w in (q, k):
+                self._check_weight(w)
+            if t.element_size() != 8 or not 0 <= self.rot_dim <= 2 * t.numel():
+                raise ValueError("kitty: turns are 64-bit, one of each pair (got %s, %s, rot_dim %d)"
+                                 % (tuple(t.shape), t.dtype, self.rot_dim))
+            c = _Rope(self.rot_dim, self.layout, self.amplitude, self.eps, _dense(t, dev),
+                      _dense(q, dev), _dense(k, dev))
+            r = self.__dict__["_ref"] = (at, ctypes.byref(c))
+        return r[1]
 
 
 def _device():

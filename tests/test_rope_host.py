@@ -217,3 +217,42 @@ def test_config_reference_follows_its_fields():
     assert cfg.ref() is first
     cfg.n_hi = 16
     assert cfg.ref() is not first and cfg.ref()._obj.n_hi == 16
+
+
+def test_rope_reference_follows_its_fields():
+    """A weight that is replaced, or whose memory moves, is the one that calls get."""
+    import torch
+    weights = [_OnDevice(torch.ones(128, dtype=torch.bfloat16) * i) for i in range(3)]
+    rope = K.Rope(K.rope_frequencies(64)[0], q_weight=weights[0], device="cpu")
+    rope.turns = _OnDevice(rope.turns)
+    first = rope.ref(0)
+    assert rope.ref(0) is first and first._obj.q_weight == weights[0].data_ptr() and first._obj.k_weight is None
+    rope.q_weight = weights[1]
+    assert rope.ref(0)._obj.q_weight == weights[1].data_ptr()
+    rope.k_weight = weights[0]
+    assert rope.ref(0)._obj.k_weight == weights[0].data_ptr()
+    weights[1]._t.data = torch.zeros(128, dtype=torch.bfloat16)
+    assert rope.ref(0)._obj.q_weight == weights[1].data_ptr()
+    rope.amplitude, rope.eps, rope.layout, rope.rot_dim = 0.5, 0.25, K.ROPE_INTERLEAVED, 32
+    c = rope.ref(0)._obj
+    assert (c.amplitude, c.eps, c.layout, c.rot_dim) == (0.5, 0.25, 1, 32)
+    rope.q_weight = None
+    assert rope.ref(0)._obj.q_weight is None
+    # what a later assignment may not be
+    for name, bad in (("q_weight", _OnDevice(torch.zeros(64, dtype=torch.int16))), ("k_weight", _OnDevice(torch.zeros(128))),
+                      ("q_weight", torch.zeros(128, dtype=torch.int16)), ("rot_dim", 66),
+                      ("q_weight", _OnDevice(torch.zeros(256, dtype=torch.int16)[::2])),
+                      ("k_weight", _OnDevice(torch.zeros(128, dtype=torch.int16), 1))):
+        keep = getattr(rope, name)
+        setattr(rope, name, bad)
+        with pytest.raises(ValueError):
+            rope.ref(0)
+        setattr(rope, name, keep)
+    rope.ref(0)
+    with pytest.raises(ValueError):
+        rope.ref(1)                                       # another device is current
+    # one table kept alive by the structure's owner: no reference into a freed object
+    import copy
+    again = copy.copy(rope)
+    again.eps = 0.5
+    assert rope.ref(0)._obj.eps == 0.25 and again.ref(0)._obj.eps == 0.5
