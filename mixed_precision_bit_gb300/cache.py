@@ -49,6 +49,7 @@ class _SharedPrefix:
             if t.shape != rows or t.element_size() != 2:
                 raise ValueError("a prefix is 16-bit [pages * %d, %d, %d] (got %s, %s)"
                                  % (PAGE, *rows[1:], tuple(t.shape), t.dtype))
+            kitty._same_type(t, self.cfg.in_dtype)
         pages = np.full(self.B, n, np.int32) if pages_of is None else np.asarray(pages_of, np.int32)
         if pages.shape != (self.B,) or (pages < 0).any() or (pages > n).any():
             raise ValueError("pages_of: one count in [0, %d] for each of %d sequences" % (n, self.B))
@@ -210,6 +211,9 @@ class LayerCache(_SharedPrefix):
         if k.shape != (T, self.cfg.num_kv_heads, D) or v.shape != k.shape:
             raise ValueError("k, v: [%d, %d, %d] (got %s, %s)"
                              % (T, self.cfg.num_kv_heads, D, tuple(k.shape), tuple(v.shape)))
+        if v.element_size() != 2:  # the binding checks the other rows
+            raise ValueError("v: 16-bit values (got %s)" % v.dtype)
+        kitty._same_type(v, self.cfg.in_dtype)
         start = np.concatenate([[0], np.cumsum(lens)])
         n_pages, tails = lens // PAGE, lens % PAGE
         pos = np.concatenate([np.arange(n) for n in lens]) if T else np.zeros(0)

@@ -365,9 +365,11 @@ class Rope:
             self._check_weight(w)
 
     @staticmethod
-    def _check_weight(w):
+    def _check_weight(w, in_dtype=None):
         if w is not None and (w.numel() != D or w.element_size() != 2):
             raise ValueError("kitty: norm weights are 16-bit [%d]" % D)
+        if in_dtype is not None and w is not None:
+            _same_type(w, in_dtype)
         _ptr(w)
 
     def __setattr__(self, name, value):
@@ -377,15 +379,15 @@ class Rope:
     def __getstate__(self):
         return {k: v for k, v in self.__dict__.items() if k != "_ref"}
 
-    def ref(self, dev: int):
+    def ref(self, dev: int, in_dtype: int = None):
         """A reference to the C structure of the fields as they are, kept until one changes, a
-        tensor's memory moves or the device does."""
+        tensor's memory moves, or the device or the rows' type does."""
         t, q, k = self.turns, self.q_weight, self.k_weight
-        at = (dev, t.data_ptr(), q is not None and q.data_ptr(), k is not None and k.data_ptr())
+        at = (dev, in_dtype, t.data_ptr(), q is not None and q.data_ptr(), k is not None and k.data_ptr())
         r = self.__dict__.get("_ref")
         if r is None or r[0] != at:
             for w in (q, k):
-                self._check_weight(w)
+                self._check_weight(w, in_dtype)
             if t.element_size() != 8 or not 0 <= self.rot_dim <= 2 * t.numel():
                 raise ValueError("kitty: turns are 64-bit, one of each pair (got %s, %s, rot_dim %d)"
                                  % (tuple(t.shape), t.dtype, self.rot_dim))
@@ -421,7 +423,21 @@ def _dense(t, dev: int):
     return t.data_ptr()
 
 
-def _rows(t, n: int, heads: int, dev: int):
+_other_types = {}  # by a configuration's input type: the 16-bit type that is not its own
+
+
+def _same_type(t, in_dtype: int):
+    """16-bit values are the configuration's type, or integers that hold its bits; as the
+    other 16-bit type they would be read as other numbers."""
+    if not _other_types:
+        import torch
+        _other_types.update({F16: torch.bfloat16, BF16: torch.float16})
+    if t.dtype is _other_types.get(in_dtype):
+        raise ValueError("kitty: %s values where the configuration has %s"
+                         % (t.dtype, "bfloat16" if in_dtype == BF16 else "float16"))
+
+
+def _rows(t, n: int, heads: int, dev: int, in_dtype: int = None):
     """(device address, elements from token to token) of rows [n, heads, 128]: 16-bit, each
     token's heads dense, any stride between tokens."""
     if t is None:
@@ -429,12 +445,24 @@ def _rows(t, n: int, heads: int, dev: int):
     if t.shape != (n, heads, D) or t.element_size() != 2:
         raise ValueError("kitty: expected 16-bit rows [%d, %d, %d] (got %s, %s)"
                          % (n, heads, D, tuple(t.shape), t.dtype))
+    _same_type(t, in_dtype)
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and heads > 1) or t.get_device() != dev:
         _here(t, dev)
         raise ValueError("kitty: the heads of a token must be contiguous (strides %s)" % (t.stride(),))
     # the stride between tokens of one token says nothing
     return t.data_ptr(), s0 if n > 1 else heads * D
+
+
+def _tail(t, cfg: Config, B: int, dev: int):
+    """Address of tails [>= B, Hkv, 32, 128], 16-bit (None: null)."""
+    if t is None:
+        return None
+    if t.element_size() != 2 or t.numel() < B * cfg.num_kv_heads * 32 * D:
+        raise ValueError("kitty: tails are 16-bit [%d, %d, 32, %d] (got %s, %s)"
+                         % (B, cfg.num_kv_heads, D, tuple(t.shape), t.dtype))
+    _same_type(t, cfg.in_dtype)
+    return _dense(t, dev)
 
 
 def _ints(name: str, t, n: int, dev: int):
@@ -469,15 +497,15 @@ def norm_rope(cfg: Config, rope: Rope, q, k, positions, q_out, k_out, stream=Non
     """Per-head norms and the position rotation of queries q [n, Hq, 128] and keys k
     [n, Hkv, 128] at positions [n] into q_out and k_out (which may be q and k); q or k may
     be None.  Rows may be slices of a joint projection (any token stride)."""
-    dev, n = _device(), positions.numel()
+    dev, n, dt = _device(), positions.numel(), cfg.in_dtype
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("kitty: rows in need rows out")
-    qp, qs = _rows(q, n, cfg.num_q_heads, dev)
-    kp, ks = _rows(k, n, cfg.num_kv_heads, dev)
-    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev)
-    ko, kos = _rows(k_out, n, cfg.num_kv_heads, dev)
+    qp, qs = _rows(q, n, cfg.num_q_heads, dev, dt)
+    kp, ks = _rows(k, n, cfg.num_kv_heads, dev, dt)
+    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev, dt)
+    ko, kos = _rows(k_out, n, cfg.num_kv_heads, dev, dt)
     _chk("kitty_norm_rope", load().kitty_norm_rope(
-        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, _ints("positions", positions, n, dev), n, qo, qos,
+        cfg.ref(), rope.ref(dev, dt), qp, qs, kp, ks, _ints("positions", positions, n, dev), n, qo, qos,
         ko, kos, _raw_stream(stream, dev)))
 
 
@@ -486,15 +514,15 @@ def append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, tail_k, tail_v,
                 pool_pages: int, pos_base=None, counted: bool = False, status=None, stream=None):
     """append_token with norm and rotation on the way (kitty_append_rope): the rotated query
     rows go to q_out (q and q_out may be None), the rotated key into the tail."""
-    dev, B = _device(), tail_len.numel()
-    qp, qs = _rows(q, B, cfg.num_q_heads, dev)
-    qo, qos = _rows(q_out, B, cfg.num_q_heads, dev)
-    kp, ks = _rows(k_new, B, cfg.num_kv_heads, dev)
-    vp, vs = _rows(v_new, B, cfg.num_kv_heads, dev)
+    dev, B, dt = _device(), tail_len.numel(), cfg.in_dtype
+    qp, qs = _rows(q, B, cfg.num_q_heads, dev, dt)
+    qo, qos = _rows(q_out, B, cfg.num_q_heads, dev, dt)
+    kp, ks = _rows(k_new, B, cfg.num_kv_heads, dev, dt)
+    vp, vs = _rows(v_new, B, cfg.num_kv_heads, dev, dt)
     table, max_pages = _table(block_table, B, dev)
     _chk("kitty_append_rope", load().kitty_append_rope(
-        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, vp, vs, qo, qos, _dense(tail_k, dev),
-        _dense(tail_v, dev), _ints("tail_len", tail_len, B, dev), _dense(run_sum, dev),
+        cfg.ref(), rope.ref(dev, dt), qp, qs, kp, ks, vp, vs, qo, qos, _tail(tail_k, cfg, B, dev),
+        _tail(tail_v, cfg, B, dev), _ints("tail_len", tail_len, B, dev), _dense(run_sum, dev),
         _dense(run_sumsq, dev), _dense(run_count, dev),
         _ints("flush_page_ids", flush_page_ids, B, dev), table, max_pages,
         _ints("num_pages", num_pages, B, dev), _dense(pool, dev), pool_pages,
@@ -508,14 +536,14 @@ def f16kv_append_rope(cfg: Config, rope: Rope, q, k_new, v_new, q_out, pool, poo
     """Norm, rotation and append into the 16-bit paged cache (kitty_f16kv_append_rope): one
     token a sequence, or the runs that seq_start [B + 1] marks; rows behind the last run
     are left alone."""
-    dev, B, n = _device(), ctx_len.numel(), k_new.shape[0]
-    qp, qs = _rows(q, n, cfg.num_q_heads, dev)
-    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev)
-    kp, ks = _rows(k_new, n, cfg.num_kv_heads, dev)
-    vp, vs = _rows(v_new, n, cfg.num_kv_heads, dev)
+    dev, B, n, dt = _device(), ctx_len.numel(), k_new.shape[0], cfg.in_dtype
+    qp, qs = _rows(q, n, cfg.num_q_heads, dev, dt)
+    qo, qos = _rows(q_out, n, cfg.num_q_heads, dev, dt)
+    kp, ks = _rows(k_new, n, cfg.num_kv_heads, dev, dt)
+    vp, vs = _rows(v_new, n, cfg.num_kv_heads, dev, dt)
     table, max_pages = _table(block_table, B, dev)
     _chk("kitty_f16kv_append_rope", load().kitty_f16kv_append_rope(
-        cfg.ref(), rope.ref(dev), qp, qs, kp, ks, vp, vs, n, qo, qos, _dense(pool, dev), pool_pages,
+        cfg.ref(), rope.ref(dev, dt), qp, qs, kp, ks, vp, vs, n, qo, qos, _dense(pool, dev), pool_pages,
         table, max_pages, _ints("ctx_len", ctx_len, B, dev),
         _ints("new_page_ids", new_page_ids, n, dev), _ints("seq_start", seq_start, B + 1, dev),
         _ints("pos_base", pos_base, B, dev), int(counted), B, _dense(status, dev),
@@ -591,6 +619,7 @@ def _attended(cfg, q, out, B, dev):
     if q.shape != shape or q.element_size() != 2 or out.shape != shape:
         raise ValueError("kitty: q (16-bit) and out must be [%d, %d, %d] (got %s, %s)"
                          % (*shape, tuple(q.shape), tuple(out.shape)))
+    _same_type(q, cfg.in_dtype)
     return _dense(q, dev), _dense(out, dev)
 
 
@@ -607,7 +636,7 @@ def decode_attention_shared(cfg: Config, q, pool, pool_pages: int, prefix_table,
     _chk("kitty_decode_attention_shared", load().kitty_decode_attention_shared(
         cfg.ref(), qp, _dense(pool, dev), pool_pages, _ints("prefix_table", prefix_table, 0, dev),
         prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev), table, max_pages,
-        _ints("num_pages", num_pages, B, dev), _dense(tail_k, dev), _dense(tail_v, dev),
+        _ints("num_pages", num_pages, B, dev), _tail(tail_k, cfg, B, dev), _tail(tail_v, cfg, B, dev),
         _ints("tail_len", tail_len, B, dev), float(sm_scale), op, _out_dtype(out),
         _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))
 

@@ -256,3 +256,72 @@ def test_rope_reference_follows_its_fields():
     again = copy.copy(rope)
     again.eps = 0.5
     assert rope.ref(0)._obj.eps == 0.25 and again.ref(0)._obj.eps == 0.5
+
+
+def test_rows_of_the_other_16_bit_type_are_refused():
+    import torch
+    bf, h, raw = (torch.zeros(3, 2, 128, dtype=t) for t in (torch.bfloat16, torch.float16, torch.int16))
+    for own, other, dt in ((bf, h, K.BF16), (h, bf, K.F16)):
+        K._rows(_OnDevice(own), 3, 2, 0, dt)
+        K._rows(_OnDevice(raw), 3, 2, 0, dt)              # the bits, as the caches hold them
+        cfg = K.Config(num_kv_heads=1, num_q_heads=2, in_dtype=dt)
+        out = _OnDevice(torch.zeros(3, 2, 128))
+        K._attended(cfg, _OnDevice(own), out, 3, 0)
+        with pytest.raises(ValueError, match="configuration has"):
+            K._rows(_OnDevice(other), 3, 2, 0, dt)
+        with pytest.raises(ValueError, match="configuration has"):
+            K._attended(cfg, _OnDevice(other), out, 3, 0)
+        rope = K.Rope(K.rope_frequencies(64)[0], q_weight=_OnDevice(own[0, 0]), device="cpu")
+        rope.turns = _OnDevice(rope.turns)
+        rope.ref(0, dt)
+        with pytest.raises(ValueError, match="configuration has"):
+            rope.ref(0, K.F16 + K.BF16 - dt)              # the same weights under the other configuration
+        rope.k_weight = _OnDevice(other[0, 0])
+        with pytest.raises(ValueError, match="configuration has"):
+            rope.ref(0, dt)
+
+
+def test_calls_pass_their_configuration_s_type():
+    """Every binding of rows refuses the other type before it launches (the other arguments are
+    on the device that is asked for)."""
+    import torch
+    from unittest import mock
+    z = lambda *s, t=torch.int32: _OnDevice(torch.zeros(s, dtype=t))  # noqa: E731
+    rows = lambda h, t=torch.bfloat16: _OnDevice(torch.zeros(3, h, 128, dtype=t))  # noqa: E731
+    cfg = K.Config(num_kv_heads=1, num_q_heads=2, in_dtype=K.BF16)
+    rope = K.Rope(K.rope_frequencies(64)[0], device="cpu")
+    rope.turns = z(32, t=torch.int64)
+    tail = lambda B=3, t=torch.int16: z(B, 1, 32, 128, t=t)  # noqa: E731
+    good = dict(q=rows(2), k=rows(1), v=rows(1), qo=rows(2), ko=rows(1), qw=None)
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    def calls(q, k, v, qo, ko, qw):
+        rope.q_weight = qw
+        yield lambda: K.norm_rope(cfg, rope, q, k, z(3), qo, ko, stream=0)
+        yield lambda: K.append_rope(cfg, rope, q, k, v, qo, tail(), tail(), z(3), None, None, None, z(3), z(3, 2), z(3),
+                                    z(8), 1, stream=0)
+        yield lambda: K.f16kv_append_rope(cfg, rope, q, k, v, qo, z(8), 1, z(3, 2), z(3), z(3), stream=0)
+
+    with mock.patch.object(K, "_device", lambda: 0), mock.patch.object(K, "load", Lib):
+        for call in calls(**good):
+            call()
+        for name in good:
+            bad = _OnDevice(torch.zeros(128, dtype=torch.float16)) if name == "qw" else \
+                rows(2 if name in ("q", "qo") else 1, torch.float16)
+            for i, call in enumerate(calls(**{**good, name: bad})):
+                if (name, i) in (("v", 0), ("ko", 1), ("ko", 2)):
+                    continue                              # not an argument of that call
+                with pytest.raises(ValueError, match="configuration has"):
+                    call()
+        for bad in (tail(2), tail(t=torch.float16), tail(t=torch.int32)):
+            for tails in ((bad, tail()), (tail(), bad)):
+                rope.q_weight = None
+                with pytest.raises(ValueError):
+                    K.append_rope(cfg, rope, None, good["k"], good["v"], None, *tails, z(3), None, None, None, z(3),
+                                  z(3, 2), z(3), z(8), 1, stream=0)
+                with pytest.raises(ValueError):
+                    K.decode_attention_shared(cfg, good["q"], z(8), 1, z(1), None, z(3, 2), z(3), *tails, z(3), 1.0,
+                                              rows(2), stream=0)

@@ -132,3 +132,20 @@ def test_prefill_refuses_lengths_that_do_not_fit():
         with pytest.raises(ValueError):
             lc.prefill_rope(None, None, k, v, lens, None)
     assert lc.alloc.free_count == 16
+
+
+def test_caches_refuse_rows_of_the_other_16_bit_type():
+    import torch
+    from mixed_precision_bit_gb300.cache import F16LayerCache, LayerCache
+    rows = lambda n, t: torch.zeros(n, 2, 128, dtype=t)  # noqa: E731
+    for kind in (LayerCache, F16LayerCache):
+        lc = kind(_cfg(in_dtype=K.BF16), 3, 4, 16, device="cpu")
+        for k, v in ((torch.float16, torch.bfloat16), (torch.bfloat16, torch.float16)):
+            with pytest.raises(ValueError, match="configuration has"):
+                lc.share_prefix(rows(32, k), rows(32, v))
+        assert lc.alloc.free_count == 16 and lc.prefix is None
+    lc = LayerCache(_cfg(in_dtype=K.F16), 3, 4, 16, device="cpu")
+    for t, match in ((torch.bfloat16, "configuration has"), (torch.float32, "16-bit")):
+        with pytest.raises(ValueError, match=match):
+            lc.prefill_rope(None, None, rows(3, torch.float16), rows(3, t), [1, 1, 1], None)
+    assert lc.alloc.free_count == 16
