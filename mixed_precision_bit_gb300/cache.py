@@ -73,13 +73,28 @@ class _SharedPrefix:
             self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.pool.device)
 
     def drop_prefix(self):
-        """Forget the shared prefix and give its pages back: between batches, as the tokens of
-        the sequences stand behind it.  Graphs captured with the prefix are not to be replayed
-        any more."""
+        """Forget the shared prefix and give its pages back: between batches (clear), as the tokens
+        of the sequences stand behind it.  Running statistics of the sequences that saw it start
+        afresh.  Graphs captured with the prefix are not to be replayed any more."""
         if self.prefix is not None:
             self.alloc.free(self.prefix.cpu().numpy())
+            self._forget_statistics(self.h_prefix > 0)
             self.prefix = self.prefix_pages = self.pos_base = None
             self.h_prefix = 0
+
+    def clear(self):
+        """Empty the sequences, between batches: every page but the shared prefix's goes back to
+        the allocator (those of a flush that was planned and not made, too), and lengths and
+        running statistics start afresh, behind the prefix if there is one.  On the current
+        stream."""
+        self.alloc.alloc(self.alloc.free_count)  # so that all pages are in use
+        keep = [] if self.prefix is None else self.prefix.cpu().numpy()
+        self.alloc.free(np.setdiff1d(np.arange(self.pool_pages), keep))
+        self.block_table.fill_(-1)
+        self._forget_tokens()
+
+    def _forget_statistics(self, seqs):
+        """Nothing to forget without running statistics."""
 
     def _prefix_tokens(self) -> int:
         return int(np.sum(self.h_prefix)) * PAGE
@@ -191,11 +206,37 @@ class LayerCache(_SharedPrefix):
             kitty.quantize_pages(self.cfg, k_pages, v_pages, self.prefix, self.pool, self.pool_pages,
                                  status=self.status, **run)
         if run:
-            sees = torch.from_numpy(pages > 0).to(dev)
-            for mine, theirs in ((self.run_sum, one[0]), (self.run_sumsq, one[1]), (self.run_count, one[2])):
-                shape = (-1,) + (1,) * (mine.dim() - 1)
-                mine.copy_(torch.where(sees.view(shape), theirs.expand_as(mine), mine))
+            self._prefix_stats = one
+            self._start_statistics()
         return ids
+
+    _prefix_stats = None  # running statistics of the shared prefix: sums, sums of squares, counts
+
+    def _stats(self):
+        return () if self.run_sum is None else (self.run_sum, self.run_sumsq, self.run_count)
+
+    def _start_statistics(self):
+        """Statistics of sequences without tokens: the prefix's where they see it, else none."""
+        for mine in self._stats():
+            mine.zero_()
+        if self.prefix is not None:
+            sees = torch.from_numpy(np.nonzero(self.h_prefix)[0]).to(self.pool.device)
+            for mine, theirs in zip(self._stats(), self._prefix_stats or ()):
+                mine.index_copy_(0, sees, theirs.expand_as(mine)[:sees.numel()])
+
+    def _forget_statistics(self, seqs):
+        at = torch.from_numpy(np.nonzero(seqs)[0]).to(self.pool.device)
+        for mine in self._stats():
+            mine.index_fill_(0, at, 0)
+        self._prefix_stats = None
+
+    def _forget_tokens(self):
+        self.num_pages.zero_()
+        self.tail_len.zero_()
+        self.h_tail[:] = 0
+        self.h_pages[:] = 0
+        self._start_statistics()
+        self.set_plan_hint()
 
     def prefill_rope(self, rope: kitty.Rope, q, k, v, lens, q_out):
         """Prompts straight from the projections: q [T, Hq, D], k, v [T, Hkv, D] 16-bit (any
@@ -439,6 +480,10 @@ class F16LayerCache(_SharedPrefix):
         kitty.f16kv_append_rope(self.cfg, rope, q, k, v, q_out, self.pool, self.pool_pages,
                                 self.block_table, self.ctx_len, ids, seq_start=start,
                                 pos_base=self.pos_base, status=self.status)
+
+    def _forget_tokens(self):
+        self.ctx_len.zero_()
+        self.h_len[:] = 0
 
     def append_rope(self, rope: kitty.Rope, q, k_new, v_new, new_page_ids, q_out, stream=None):
         """append from the projections, as LayerCache.append_rope."""

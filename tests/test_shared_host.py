@@ -149,3 +149,49 @@ def test_caches_refuse_rows_of_the_other_16_bit_type():
         with pytest.raises(ValueError, match=match):
             lc.prefill_rope(None, None, rows(3, torch.float16), rows(3, t), [1, 1, 1], None)
     assert lc.alloc.free_count == 16
+
+
+def test_cleared_caches_have_their_pages_and_no_tokens():
+    """clear gives back the pages of the sequences, of flushes that were planned and not made, and
+    of a prefill over another; the prefix keeps its own."""
+    import torch
+    from mixed_precision_bit_gb300.cache import F16LayerCache, LayerCache
+    for rank in (K.RANK_PAGE, K.RANK_RUNNING):
+        for kind in (LayerCache, F16LayerCache):
+            lc = kind(_cfg(rank_mode=rank), 3, 4, 16, device="cpu")
+            packed = kind is LayerCache
+            ids = lc.alloc.alloc(2)
+            lc._set_prefix(ids, np.array([2, 0, 2], np.int32), True)
+            if packed and rank:
+                lc._prefix_stats = [torch.full((1,) + t.shape[1:], 3, dtype=t.dtype) for t in lc._stats()]
+            lc.alloc.alloc(3)                             # an earlier prefill's, and a planned flush's
+            lc.block_table[1, :2] = 7
+            if packed:
+                lc.h_pages[:], lc.h_tail[:] = [0, 2, 0], [31, 5, 0]
+                lc.num_pages[1], lc.tail_len[0] = 2, 31
+                for t in lc._stats():
+                    t.fill_(9)
+                lc.plan_flush()
+            else:
+                lc.h_len[:] = [64, 5, 0]
+                lc.ctx_len[0] = 64
+                lc.plan_flush()
+            lc.clear()
+            assert lc.alloc.free_count == 14 and lc.kv_tokens() == lc._prefix_tokens() == 4 * 32
+            assert (lc.block_table == -1).all()
+            assert sorted(lc.alloc.alloc(14).tolist() + ids.tolist()) == list(range(16))
+            lc.alloc.free(np.setdiff1d(np.arange(16), ids))
+            if packed:
+                assert not lc.num_pages.any() and not lc.tail_len.any()
+                for t in lc._stats():
+                    assert (t[0] == 3).all() and (t[1] == 0).all() and (t[2] == 3).all()
+                    t.fill_(9)
+            else:
+                assert not lc.ctx_len.any()
+            lc.drop_prefix()
+            assert lc.alloc.free_count == 16 and lc.kv_tokens() == 0
+            if packed:
+                for t in lc._stats():                     # of those that saw it
+                    assert (t[0] == 0).all() and (t[1] == 9).all() and (t[2] == 0).all()
+            lc.clear()
+            assert lc.alloc.free_count == 16 and not (packed and any(t.any() for t in lc._stats()))
