@@ -55,6 +55,19 @@ class _SharedPrefix:
             raise ValueError("pages_of: one count in [0, %d] for each of %d sequences" % (n, self.B))
         return n, pages
 
+    def _install_prefix(self, ids, pages, pages_of, write):
+        """The prefix of these pages, once write(page ids on the device) has been accepted: a
+        refusal leaves the cache without one, its pages free."""
+        try:
+            self._set_prefix(ids, pages, pages_of)
+            if ids.size:
+                write(self.prefix)
+        except BaseException:
+            self.prefix = self.prefix_pages = self.pos_base = None
+            self.h_prefix = 0
+            self.alloc.free(ids)
+            raise
+
     def _set_prefix(self, ids, pages, pages_of):
         dev = self.pool.device
         self.prefix = torch.from_numpy(ids.astype(np.int32)).to(dev)
@@ -201,10 +214,8 @@ class LayerCache(_SharedPrefix):
             run = dict(seq_of_page=torch.zeros(n, dtype=torch.int32, device=dev), n_seqs=1,
                        run_sum=one[0], run_sumsq=one[1], run_count=one[2])
         ids = self.alloc.alloc(n)
-        self._set_prefix(ids, pages, pages_of)
-        if n:
-            kitty.quantize_pages(self.cfg, k_pages, v_pages, self.prefix, self.pool, self.pool_pages,
-                                 status=self.status, **run)
+        self._install_prefix(ids, pages, pages_of, lambda at: kitty.quantize_pages(
+            self.cfg, k_pages, v_pages, at, self.pool, self.pool_pages, status=self.status, **run))
         if run:
             self._prefix_stats = one
             self._start_statistics()
@@ -444,10 +455,8 @@ class F16LayerCache(_SharedPrefix):
         """As LayerCache.share_prefix (any pages_of)."""
         n, pages = self._prefix_plan(k_pages, v_pages, pages_of)
         ids = self.alloc.alloc(n)
-        self._set_prefix(ids, pages, pages_of)
-        if ids.size:
-            kitty.f16kv_write_pages(self.cfg, k_pages, v_pages, self.prefix, self.pool,
-                                    self.pool_pages, status=self.status)
+        self._install_prefix(ids, pages, pages_of, lambda at: kitty.f16kv_write_pages(
+            self.cfg, k_pages, v_pages, at, self.pool, self.pool_pages, status=self.status))
         return ids
 
     def plan_extend(self, lens):
@@ -476,10 +485,16 @@ class F16LayerCache(_SharedPrefix):
         for x, heads in ((q, Hq), (q_out, Hq), (k, Hkv), (v, Hkv)):  # before pages are taken
             if x is not None and x.shape != (T, heads, D):
                 raise ValueError("expected rows [%d, %d, %d] (got %s)" % (T, heads, D, tuple(x.shape)))
-        ids, start = (torch.from_numpy(x).to(self.pool.device) for x in self.plan_extend(lens))
-        kitty.f16kv_append_rope(self.cfg, rope, q, k, v, q_out, self.pool, self.pool_pages,
-                                self.block_table, self.ctx_len, ids, seq_start=start,
-                                pos_base=self.pos_base, status=self.status)
+        plan = self.plan_extend(lens)
+        try:
+            ids, start = (torch.from_numpy(x).to(self.pool.device) for x in plan)
+            kitty.f16kv_append_rope(self.cfg, rope, q, k, v, q_out, self.pool, self.pool_pages,
+                                    self.block_table, self.ctx_len, ids, seq_start=start,
+                                    pos_base=self.pos_base, status=self.status)
+        except BaseException:  # nothing was appended: the plan is taken back
+            self.alloc.free(plan[0][plan[0] >= 0])
+            self.h_len -= np.asarray(lens, np.int64)
+            raise
 
     def _forget_tokens(self):
         self.ctx_len.zero_()

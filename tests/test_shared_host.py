@@ -195,3 +195,34 @@ def test_cleared_caches_have_their_pages_and_no_tokens():
                     assert (t[0] == 0).all() and (t[1] == 9).all() and (t[2] == 0).all()
             lc.clear()
             assert lc.alloc.free_count == 16 and not (packed and any(t.any() for t in lc._stats()))
+
+
+@pytest.mark.parametrize("rank", [K.RANK_PAGE, K.RANK_RUNNING])
+def test_a_prefix_that_the_page_write_refuses_is_not_installed(rank):
+    """The binding refuses host memory and rows with gaps (here everything is on the host): the
+    cache is as before, and a corrected call is not refused for a prefix that is not there."""
+    import torch
+    from mixed_precision_bit_gb300.cache import F16LayerCache, LayerCache
+    rows = torch.zeros(32, 4, 128, dtype=torch.int16)
+    for kind in (LayerCache, F16LayerCache):
+        lc = kind(_cfg(rank_mode=rank), 3, 4, 16, device="cpu")
+        for k in (rows[:, :2].contiguous(), rows[:, :2]):  # a slice of a joint projection, too
+            for _ in range(2):
+                with pytest.raises(ValueError, match="tensor arguments must be"):
+                    lc.share_prefix(k, k, pages_of=[1, 0, 1])
+                assert lc.alloc.free_count == 16 and lc.kv_tokens() == 0
+                assert lc.prefix is None and lc.prefix_pages is None and lc.pos_base is None
+                assert np.sum(lc.h_prefix) == 0
+
+
+def test_a_refused_extension_takes_no_pages():
+    import torch
+    lc = _caches()[1]
+    rows = lambda h, t=torch.int16: torch.zeros(40, h, 128, dtype=t)  # noqa: E731
+    rope = K.Rope(K.rope_frequencies(64)[0], device="cpu")
+    for q, k, v, q_out in ((rows(8), rows(2), rows(2), rows(8)),              # host memory
+                           (None, rows(2), rows(2, torch.float32), None),     # not 16-bit
+                           (None, rows(4)[:, ::2], rows(2), None)):           # heads with gaps
+        with pytest.raises((ValueError, RuntimeError, AssertionError)):
+            lc.extend_rope(rope, q, k, v, [33, 0, 7], q_out)
+        assert lc.alloc.free_count == 16 and list(lc.h_len) == [0, 0, 0]
