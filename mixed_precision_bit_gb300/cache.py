@@ -81,9 +81,22 @@ class _SharedPrefix:
         if self.prefix is None:
             return
         need = max(self._shared_bytes(self.cfg, self.B, self.prefix.numel(), self.max_pages), 16)
-        ws = getattr(self, "shared_workspace", None)
-        if ws is None or ws.numel() < need:
-            self.shared_workspace = torch.empty(need, dtype=torch.uint8, device=self.pool.device)
+        self.shared_workspace = self._grown(self.shared_workspace, need)
+
+    shared_workspace = None
+
+    def _grown(self, ws, need):
+        """A workspace of at least `need` bytes: ws, or a new one, of at least twice its size.
+        The old one stays allocated as long as the cache, because a captured step writes its
+        partials there; doubling keeps all of them together below twice the last one's size."""
+        have = 0 if ws is None else ws.numel() * ws.element_size()
+        if have >= need:
+            return ws
+        if ws is not None:
+            self._outgrown = (*self._outgrown, ws)
+        return torch.empty((max(need, 2 * have) + 3) // 4, dtype=torch.float32, device=self.pool.device)
+
+    _outgrown = ()
 
     def drop_prefix(self):
         """Forget the shared prefix and give its pages back: between batches (clear), as the tokens
@@ -187,14 +200,14 @@ class LayerCache(_SharedPrefix):
     def set_plan_hint(self, total_pages=None, max_pages=None):
         """Give the decode split planner the batch's total and largest page counts
         (default: the host mirror's) on this cache's own copy of the config, and
-        grow the workspace if that plan needs more.  Any values are correct;
-        close ones balance the splits better."""
+        grow the workspaces if that plan needs more.  Any values are correct;
+        close ones balance the splits better.  Steps that were captured before keep
+        their plan and their workspaces."""
         total = int(self.h_pages.sum()) if total_pages is None else int(total_pages)
         mx = int(self.h_pages.max()) if max_pages is None and self.B else int(max_pages or 0)
         self.cfg = dataclasses.replace(self.cfg, decode_total_pages=total, decode_max_pages=mx)
-        need = kitty.decode_workspace_bytes(self.cfg, self.B, self.max_pages)
-        if need > self.workspace.numel() * 4:
-            self.workspace = torch.empty(need // 4, dtype=torch.float32, device=self.pool.device)
+        self.workspace = self._grown(self.workspace,
+                                     kitty.decode_workspace_bytes(self.cfg, self.B, self.max_pages))
         self._size_shared()
 
     def share_prefix(self, k_pages, v_pages, pages_of=None):

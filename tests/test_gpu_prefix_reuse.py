@@ -140,3 +140,38 @@ def test_prefix_pages_and_what_follows_them_against_the_oracle(rank):
     for x, y in zip(_stats(lc), stats):
         assert np.array_equal(x.cpu().numpy(), y)
     assert int(lc.status.item()) == 0
+
+
+@pytest.mark.parametrize("prefix", [False, True], ids=["own", "shared"])
+def test_a_captured_step_keeps_its_workspace(prefix):
+    """Replayed after hints that grew the workspaces, with other tensors allocated since: the
+    bytes of the first replay, and the other tensors untouched."""
+    import torch
+    from mixed_precision_bit_gb300 import kitty
+    from mixed_precision_bit_gb300.cache import LayerCache
+    cfg = kitty.Config(num_kv_heads=Hkv, num_q_heads=Hq, in_dtype=DT, n_hi=32)
+    lc = LayerCache(cfg, B, 400, 20)
+    if prefix:
+        _share(lc, 4, 1)
+    _prefill(lc, 10)
+    q = torch.randn(B, Hq, D, device="cuda").bfloat16()
+    out = torch.empty(B, Hq, D, device="cuda")
+    lc.attend(q, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lc.attend(q, out)
+    g.replay()
+    first = out.clone()
+    held = (lc.workspace, lc.shared_workspace)
+    addresses = [w.data_ptr() for w in held if w is not None]
+    del held
+    lc.set_plan_hint(1200, 400)
+    assert addresses != [w.data_ptr() for w in (lc.workspace, lc.shared_workspace) if w is not None]
+    others = [torch.full((n,), 7.0, device="cuda") for n in (1 << 8, 1 << 12, 1 << 14, 1 << 16, 1 << 18) for _ in range(8)]
+    for o in others:
+        assert not any(o.data_ptr() <= a < o.data_ptr() + 4 * o.numel() for a in addresses)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, first)
+    assert all(bool((o == 7).all()) for o in others)

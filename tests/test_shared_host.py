@@ -226,3 +226,30 @@ def test_a_refused_extension_takes_no_pages():
         with pytest.raises((ValueError, RuntimeError, AssertionError)):
             lc.extend_rope(rope, q, k, v, [33, 0, 7], q_out)
         assert lc.alloc.free_count == 16 and list(lc.h_len) == [0, 0, 0]
+
+
+def test_outgrown_workspaces_stay_allocated():
+    """A captured step holds the addresses of the workspaces that it was captured with: a plan
+    that needs more gets new ones beside them, few and not much larger than needed."""
+    import gc
+    import weakref
+    import torch
+    from mixed_precision_bit_gb300.cache import LayerCache
+    lc = LayerCache(_cfg(), 3, 400, 1300, device="cpu")
+    lc._set_prefix(lc.alloc.alloc(40), np.full(3, 40, np.int32), None)
+    lc.set_plan_hint(3, 1)
+    old = {}
+    for total, most in ((3, 1), (30, 10), (300, 100), (900, 300), (30, 10), (1200, 400)):
+        for ws in (lc.workspace, lc.shared_workspace):
+            old[ws.data_ptr()] = weakref.ref(ws)
+        del ws
+        lc.set_plan_hint(total, most)
+        cfg = _cfg(decode_total_pages=total, decode_max_pages=most)
+        for ws, need in ((lc.workspace, K.decode_workspace_bytes(cfg, 3, 400)),
+                         (lc.shared_workspace, K.shared_workspace_bytes(cfg, 3, 40, 400))):
+            assert ws.numel() * ws.element_size() >= need
+        del ws
+        gc.collect()
+        assert all(r() is not None for r in old.values())
+    largest = lc.workspace.numel() + lc.shared_workspace.numel()
+    assert len(lc._outgrown) >= 2 and sum(w.numel() for w in lc._outgrown) < largest
