@@ -36,6 +36,7 @@ class _SharedPrefix:
     prefix_pages = None  # device int32 [B]: pages of it that each sequence sees; None: all
     pos_base = None      # device int32 [B]: positions ahead of a sequence's own tokens
     h_prefix = 0         # host mirror: pages that each sequence sees
+    epoch = 0            # counts what a step captured before cannot follow: prefixes and clears
 
     def _prefix_plan(self, k_pages, v_pages, pages_of):
         """(pages of the prefix, pages of it that each sequence sees), checked."""
@@ -67,6 +68,7 @@ class _SharedPrefix:
             self.h_prefix = 0
             self.alloc.free(ids)
             raise
+        self.epoch += 1
 
     def _set_prefix(self, ids, pages, pages_of):
         dev = self.pool.device
@@ -107,6 +109,7 @@ class _SharedPrefix:
             self._forget_statistics(self.h_prefix > 0)
             self.prefix = self.prefix_pages = self.pos_base = None
             self.h_prefix = 0
+            self.epoch += 1
 
     def clear(self):
         """Empty the sequences, between batches: every page but the shared prefix's goes back to
@@ -118,6 +121,7 @@ class _SharedPrefix:
         self.alloc.free(np.setdiff1d(np.arange(self.pool_pages), keep))
         self.block_table.fill_(-1)
         self._forget_tokens()
+        self.epoch += 1
 
     def _forget_statistics(self, seqs):
         """Nothing to forget without running statistics."""
@@ -598,7 +602,8 @@ class ServingStep:
     step are planned on the host while the graph of this one runs (the host
     mirrors of the layers run one step ahead between calls); two graphs read
     the plans from alternating pinned buffers.  Between run() calls the layers
-    must not be driven by other calls.
+    must not be driven by other calls; a layer whose prefix has changed, or that was
+    cleared, since the graphs were captured is refused (they attend what it had then).
     graphs=False: direct calls; the flush plan of layer l is made just before
     its block goes up, so planning overlaps the kernels of the layers before it.
     fused=False runs append then attend per layer.
@@ -636,6 +641,7 @@ class ServingStep:
             self.h_fl = [torch.empty((L, B), dtype=torch.int32).pin_memory() for _ in range(2)]
             self.d_fl = torch.empty((L, B), dtype=torch.int32, device=dev)
             self.graphs = [self._capture(p) for p in range(2)]
+            self._epochs = [lc.epoch for lc in layers]
             self._parity = 0
             self._planned = 0  # layers whose flushes of the pending step are planned
 
@@ -698,6 +704,10 @@ class ServingStep:
     def run(self):
         cur = torch.cuda.current_stream()
         if self.graphs is not None:
+            for l, lc in enumerate(self.layers):
+                if lc.epoch != self._epochs[l]:
+                    raise ValueError("layer %d was cleared, or its shared prefix changed, after the step was "
+                                     "captured: make a new ServingStep" % l)
             self._plan(self._parity)  # nothing left to do unless the look-ahead stopped
             self.graphs[self._parity].replay()
             self._parity ^= 1

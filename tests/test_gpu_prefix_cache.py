@@ -216,3 +216,55 @@ def test_captured_steps_behind_a_prefix(packed):
         assert torch.equal(out, out2) and torch.equal(r, r2), step
     assert torch.equal(caches[0].pool, caches[1].pool)
     assert all(int(lc.status.item()) == 0 for lc in caches)
+
+
+@pytest.mark.parametrize("change", ["share", "drop", "clear"])
+def test_serving_step_refuses_layers_that_it_was_not_captured_with(change):
+    """A step's graphs attend the prefix that the layers had when it was made: without it, or with
+    another, they would go on without a word.  Direct calls follow the layers."""
+    import torch
+    from mixed_precision_bit_gb300 import kitty
+    from mixed_precision_bit_gb300.cache import LayerCache, ServingStep
+    cfg = kitty.Config(num_kv_heads=Hkv, num_q_heads=Hq, in_dtype=synth.BF16, n_hi=32)
+    t = torch.bfloat16
+    pre, own = [[x.contiguous() for x in _rows(n * P, t, s)[1:]] for n, s in ((NP, 10), (B, 20))]
+    x = [[r.contiguous() for r in _rows(B, t, s)] for s in (30, 31)]
+
+    def layer(prefix):
+        lc = LayerCache(cfg, B, 5, NP + 5 * B)
+        if prefix:
+            lc.share_prefix(*pre)
+        return lc
+
+    layers = {g: [layer(change != "share") for _ in range(2)] for g in (True, False)}
+    srv = {g: ServingStep(layers[g], graphs=g) for g in (True, False)}
+    for g, lcs in layers.items():
+        for lc in lcs:
+            if change == "share":
+                lc.share_prefix(*pre)
+            elif change == "drop":
+                lc.drop_prefix()
+            else:
+                lc.clear()
+            lc.prefill(*own, np.ones(B, int))
+        for l in range(2):
+            for dst, r in zip((srv[g].q[l], srv[g].k_new[l], srv[g].v_new[l]), x[l]):
+                dst.copy_(r.view(torch.int16).cpu())
+    tails = [lc.tail_len.clone() for lc in layers[True]]
+    with pytest.raises(ValueError, match="new ServingStep"):
+        srv[True].run()
+    for lc, n in zip(layers[True], tails):                 # refused before anything was planned or run
+        assert torch.equal(lc.tail_len, n) and (lc.h_tail == 0).all()
+    got = {False: srv[False].run().clone()}
+    again = ServingStep(layers[True])
+    for l in range(2):
+        for dst, r in zip((again.q[l], again.k_new[l], again.v_new[l]), x[l]):
+            dst.copy_(r.view(torch.int16).cpu())
+    got[True] = again.run().clone()
+    assert torch.equal(got[True].view(torch.int16), got[False].view(torch.int16))
+    out = torch.empty(B, Hq, D, dtype=t, device="cuda")
+    for l in range(2):
+        lc = layer(change != "drop")
+        lc.prefill(*own, np.ones(B, int))
+        lc.step(x[l][1], x[l][2], torch.from_numpy(lc.plan_flush()).cuda(), x[l][0], out)
+        assert torch.equal(got[True][l].view(torch.int16), out.cpu().view(torch.int16)), l
