@@ -368,7 +368,7 @@ class Rope:
     def _check_weight(w, in_dtype=None):
         if w is not None and (w.numel() != D or w.element_size() != 2):
             raise ValueError("kitty: norm weights are 16-bit [%d]" % D)
-        if in_dtype is not None and w is not None:
+        if w is not None:
             _same_type(w, in_dtype)
         _ptr(w)
 
@@ -423,16 +423,22 @@ def _dense(t, dev: int):
     return t.data_ptr()
 
 
-_other_types = {}  # by a configuration's input type: the 16-bit type that is not its own
+class _RowTypes(dict):
+    """Types that 16-bit values may have, by the configuration's input type: its own, or integers
+    that hold its bits.  As the other 16-bit type they would be read as other numbers."""
+
+    def __missing__(self, in_dtype):
+        import torch
+        mine = {F16: (torch.float16,), BF16: (torch.bfloat16,)}.get(in_dtype, (torch.float16, torch.bfloat16))
+        self[in_dtype] = frozenset((*mine, torch.int16, torch.uint16))
+        return self[in_dtype]
+
+
+_row_types = _RowTypes()
 
 
 def _same_type(t, in_dtype: int):
-    """16-bit values are the configuration's type, or integers that hold its bits; as the
-    other 16-bit type they would be read as other numbers."""
-    if not _other_types:
-        import torch
-        _other_types.update({F16: torch.bfloat16, BF16: torch.float16})
-    if t.dtype is _other_types.get(in_dtype):
+    if t.element_size() == 2 and t.dtype not in _row_types[in_dtype]:
         raise ValueError("kitty: %s values where the configuration has %s"
                          % (t.dtype, "bfloat16" if in_dtype == BF16 else "float16"))
 
@@ -442,10 +448,10 @@ def _rows(t, n: int, heads: int, dev: int, in_dtype: int = None):
     token's heads dense, any stride between tokens."""
     if t is None:
         return None, 0
-    if t.shape != (n, heads, D) or t.element_size() != 2:
+    if t.shape != (n, heads, D) or t.dtype not in _row_types[in_dtype]:
+        _same_type(t, in_dtype)
         raise ValueError("kitty: expected 16-bit rows [%d, %d, %d] (got %s, %s)"
                          % (n, heads, D, tuple(t.shape), t.dtype))
-    _same_type(t, in_dtype)
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != D and heads > 1) or t.get_device() != dev:
         _here(t, dev)
@@ -458,11 +464,13 @@ def _tail(t, cfg: Config, B: int, dev: int):
     """Address of tails [>= B, Hkv, 32, 128], 16-bit (None: null)."""
     if t is None:
         return None
-    if t.element_size() != 2 or t.numel() < B * cfg.num_kv_heads * 32 * D:
+    if t.numel() < B * cfg.num_kv_heads * 32 * D or t.dtype not in _row_types[cfg.in_dtype]:
+        _same_type(t, cfg.in_dtype)
         raise ValueError("kitty: tails are 16-bit [%d, %d, 32, %d] (got %s, %s)"
                          % (B, cfg.num_kv_heads, D, tuple(t.shape), t.dtype))
-    _same_type(t, cfg.in_dtype)
-    return _dense(t, dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        _dense(t, dev)
+    return t.data_ptr()
 
 
 def _ints(name: str, t, n: int, dev: int):
@@ -616,10 +624,10 @@ def f16kv_shared_workspace_bytes(cfg: Config, B: int, n_prefix: int, max_pages: 
 def _attended(cfg, q, out, B, dev):
     """Addresses of q (16-bit) and out, both [B, Hq, 128]."""
     shape = (B, cfg.num_q_heads, D)
-    if q.shape != shape or q.element_size() != 2 or out.shape != shape:
+    if q.shape != shape or out.shape != shape or q.dtype not in _row_types[cfg.in_dtype]:
+        _same_type(q, cfg.in_dtype)
         raise ValueError("kitty: q (16-bit) and out must be [%d, %d, %d] (got %s, %s)"
                          % (*shape, tuple(q.shape), tuple(out.shape)))
-    _same_type(q, cfg.in_dtype)
     return _dense(q, dev), _dense(out, dev)
 
 
