@@ -34,7 +34,7 @@
 // RMS, all to one side.  Centered, both sums stay near the output's size.
 //
 // What bounds it.  Packed, 128 sequences of 64/8 heads behind 32768 tokens (32 x 4 blocks of 86
-// tiles): 1.7 us a tile of both lanes; of the issue slots of the SMs in use 64% are taken (97.6 M
+// tiles): 1.7 us a tile of both lanes; of the issue slots of the SMs in use 64% are taken (97.8 M
 // warp instructions, near half of them writing operands), the tensor pipe is busy 50%, memory
 // 2%.  Two blocks that share a tile's operands through a cluster would halve the writing for
 // batches of more than 256 rows; that is not done.  A few tiles a block: fixed costs, about
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
 // or within 2% of it at all five; one block on every SM, the choice without the own pages'
 // share: 64 x 8192 tokens 34.3 against 30.1 us, on 16-bit pages 41.3 against 31.9 us,
 // 128 x 32768 177 against 165 us):
-constexpr double kTileUs = 1.8;    // a tile of both lanes
+constexpr double kTileUs = 1.8;    // a tile of both lanes (1.7 packed, 2 on 16-bit pages)
 constexpr double kPathTiles = 7;   // start and end of a block, in tiles, on the critical path ..
 constexpr double kBlockTiles = 8.5;  // .. and of its SM's time
 PrefixPlan plan_for(int Hkv, int rows, int tiles, int sms, double own_us) {
