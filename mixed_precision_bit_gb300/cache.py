@@ -43,7 +43,7 @@ class _SharedPrefix:
         if self.prefix is not None:
             raise ValueError("the cache has a shared prefix (drop_prefix)")
         if self.kv_tokens():
-            raise ValueError("the sequences hold tokens already: their positions begin at the prefix's end")
+            raise ValueError("the sequences hold tokens already (clear): their positions begin at the prefix's end")
         n = k_pages.shape[0] // PAGE
         rows = (n * PAGE, self.cfg.num_kv_heads, D)
         for t in (k_pages, v_pages):
@@ -220,7 +220,8 @@ class LayerCache(_SharedPrefix):
         remainder is each sequence's own).  pages_of: how many of its pages each sequence sees
         (default: all); with running or sequence-wide ranking all or none of them, and those
         sequences' channel statistics go on from the prefix's.  Before the prefill or the first
-        append of the sequences, on the current stream; returns the page ids."""
+        append of the sequences, on the current stream; returns the page ids.  Steps that were
+        captured before do not attend it."""
         n, pages = self._prefix_plan(k_pages, v_pages, pages_of)
         dev, run = self.pool.device, {}
         if self.run_sum is not None:

@@ -144,13 +144,16 @@ __global__ void __launch_bounds__(128) f16kv_append_rope_finish(const Append16 p
   grid_wait();
   const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= p.B) return;
-  const int first = p.seq_start[b], end = p.seq_start[b + 1];
+  // all loads at once: what depends on the starts is arithmetic
+  const int first = p.seq_start[b], end = p.seq_start[b + 1], n = end - first;
+  const int e0 = lane < p.B ? p.seq_start[lane + 1] : 0;
+  const int before = length_before(p, b, n, false);
   if (first == end) return;
   bool mine = first >= 0 && first < end && end <= n_tokens;
   if (mine) {
     int c0 = 0, c1 = 0;  // ends at or before the first and the last token
     for (int s = lane; s < p.B; s += 32) {
-      const int e = p.seq_start[s + 1];
+      const int e = s == lane ? e0 : p.seq_start[s + 1];
       c0 += e <= first;
       c1 += e < end;
     }
@@ -160,8 +163,6 @@ __global__ void __launch_bounds__(128) f16kv_append_rope_finish(const Append16 p
     if (lane == 0) set_status(p.d_status, KITTY_ST_BAD_SEQ);
     return;
   }
-  const int n = end - first;
-  const int before = length_before(p, b, n, false);
   if (before < 0) return;
   bool ok = true;
   if (before % kPage != 0) {
