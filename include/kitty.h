@@ -59,6 +59,8 @@ extern "C" {
 #define KITTY_ST_TABLE_FULL 8 /* flush with num_pages == max_pages */
 #define KITTY_ST_BAD_SEQ 9    /* seq_of_page not non-decreasing in [0, n_seqs) */
 #define KITTY_ST_TIMEOUT 10   /* a bounded wait on an in-flight copy gave up */
+#define KITTY_ST_NO_PAGES 11  /* the stack of free pages holds too few for a sequence */
+#define KITTY_ST_BAD_TREE 12  /* a parent or a path entry that names no node it may */
 
 #define KITTY_F16 0
 #define KITTY_BF16 1
@@ -515,6 +517,146 @@ int kitty_f16kv_decode_shared(const kitty_cfg* cfg, const void* q, const void* p
                               int32_t max_pages, const int32_t* ctx_len, float sm_scale, void* out,
                               int32_t out_dtype, void* workspace, size_t workspace_bytes,
                               int32_t B, int32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------- drafted tokens
+ * A step of speculative decoding on either cache: each sequence has a tree of drafted
+ * tokens, which are attended in one call and whose accepted path goes into the cache;
+ * lengths and pages are decided on the device, where what is accepted is known.
+ *
+ * Rows.  Sequence b's nodes are the rows seq_start[b] .. seq_start[b+1] - 1 of n_tokens
+ * (seq_start device int32 [B + 1], rising from 0), at most KITTY_TREE_MAX_NODES of them, in
+ * any order that puts parents before children; none is fine.  Rows from seq_start[B] on are
+ * padding, neither read nor written.  A sequence whose starts are out of order or beyond
+ * n_tokens sets KITTY_ST_BAD_SEQ, one with too many nodes KITTY_ST_BAD_LEN; it is skipped. */
+#define KITTY_TREE_MAX_NODES 64
+
+/* Ancestor masks and positions.
+ *   parents    device int32 [n_tokens]: the node's parent as its place in its own tree, or -1
+ *              for a node that follows the cached tokens.  Anything but -1 .. the node's
+ *              own place - 1 sets KITTY_ST_BAD_TREE and counts as -1
+ *   lens       device int32 [B], num_pages device int32 [B] or NULL (0): sequence b's cache
+ *              holds 32 * num_pages[b] + lens[b] tokens (the packed cache's num_pages and
+ *              tail_len, or the 16-bit cache's ctx_len alone)
+ *   pos_base   device int32 [B] or NULL (0): positions before the cache's first token
+ *   visible    device uint64 [n_tokens], written: bit j of a node's mask is set for the node j
+ *              itself and its ancestors; may be NULL
+ *   positions  device int32 [n_tokens], written: pos_base + tokens held + the node's
+ *              depth (0 where the parent is -1), as kitty_norm_rope takes them; may be NULL */
+int kitty_tree_plan(const int32_t* parents, const int32_t* seq_start, int32_t n_tokens,
+                    const int32_t* num_pages, const int32_t* lens, const int32_t* pos_base,
+                    uint64_t* visible, int32_t* positions, int32_t B, int32_t* d_status,
+                    void* stream);
+
+/* Block tables and slot maps from lengths, with the free pages on the device.
+ * Sequence b is to have pages for
+ *   n_b = 32 * num_pages[b] + lens[b] + (seq_start[b+1] - seq_start[b]) + extra   tokens,
+ * ceil(n_b / 32) of them (partial = 1: a page that is begun counts, as in the 16-bit cache) or
+ * floor(n_b / 32) (partial = 0: full pages only, as in the packed cache).  held[b] is how many
+ * its row of the block table has.
+ *   more     pages are taken from the top of the stack, in order of sequences and of places
+ *            in the row.  The sequences are served in order until one does not fit: that
+ *            one and all later ones that need pages get none (KITTY_ST_NO_PAGES)
+ *   fewer    shrink = 1: the row's last pages go back on the stack, their entries become -1, in
+ *            the reverse order (later sequences first, and their last pages first), before
+ *            any are taken; shrink = 0: the row keeps them.  So what one call takes, a
+ *            later one gives back to where it was
+ *   lens, num_pages  as in kitty_tree_plan;  seq_start device int32 [B + 1] or NULL (no new tokens)
+ *   held       device int32 [B], updated
+ *   block_table  device int32 [B][max_pages], updated
+ *   free_ids   device int32 [pool_pages]: the stack, free_ids[0 .. *free_count), top last
+ *   free_count device int32, updated
+ *   slots      device int64 [n_tokens] or NULL (needs seq_start): of each new token the place that
+ *              it goes to, 32 * page id + place in the page (-1: its sequence has no page
+ *              there); rows from seq_start[B] on are left as they are
+ *   new_page_ids device int32 [n_tokens] or NULL (needs seq_start): the page id where the token
+ *              begins a page, else -1, as kitty_f16kv_append_rope takes them
+ * A sequence that needs more than max_pages (KITTY_ST_TABLE_FULL), whose lengths are negative or
+ * whose held is outside [0, max_pages] (KITTY_ST_BAD_LEN), or that would give back an id out of
+ * range (KITTY_ST_BAD_PAGE) keeps its row.  A free_count outside [0, pool_pages] sets
+ * KITTY_ST_BAD_LEN and nothing changes. */
+int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32_t* seq_start,
+                      int32_t n_tokens, int32_t extra, int32_t partial, int32_t shrink,
+                      int32_t* held, int32_t* block_table, int32_t max_pages, int32_t* free_ids,
+                      int32_t* free_count, int32_t pool_pages, int64_t* slots,
+                      int32_t* new_page_ids, int32_t B, int32_t* d_status, void* stream);
+
+/* Attention of the drafted tokens over the packed cache and over each other: for node i of
+ * sequence b, row t, and query head hq (kv head hq / (Hq/Hkv)),
+ *   out[t][hq] = softmax(sm_scale * q.k) . v over the prefix's pages, the num_pages[b] pages of
+ *   block_table[b], the tail_len[b] tail tokens, and the nodes j of b whose bit is set in
+ *   visible[t]; a row that sees nothing gives 0 and KITTY_ST_EMPTY.
+ *   q          device [n_tokens][Hq][128] 16-bit, q_stride elements from token to token, k and v
+ *              likewise [n_tokens][Hkv][128] (as in kitty_norm_rope; rotated already)
+ *   visible    device uint64 [n_tokens], bits of nodes that the tree has not are ignored; NULL:
+ *              every tree is a chain (node i sees the nodes 0 .. i)
+ *   max_nodes  most nodes of a tree, 1 .. KITTY_TREE_MAX_NODES
+ *   prefix_table, n_prefix, prefix_pages  as in kitty_decode_attention_shared; n_prefix = 0
+ *              without a shared prefix
+ *   out        device [n_tokens][Hq][128] of out_dtype, dense, 16-byte aligned
+ *   workspace  device, >= kitty_tree_workspace_bytes of the same sizes, 16-byte aligned; calls
+ *              that may overlap need one each
+ * Other arguments, layouts and status codes as for kitty_decode_attention; g = Hq/Hkv <= 32.
+ * The tensor cores take fp16: a query, or a tail's or a node's key or value that a query sees,
+ * beyond its range sets KITTY_ST_RANGE (NaN or Inf: KITTY_ST_NONFINITE), and the outputs of the
+ * rows that see it are then undefined; rows that do not see it are not affected. */
+int kitty_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
+                               int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
+                               size_t* bytes);
+int kitty_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_stride, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride, int32_t n_tokens,
+                         const int32_t* seq_start, const uint64_t* visible, int32_t max_nodes,
+                         const void* pool, int32_t pool_pages, const int32_t* prefix_table,
+                         int32_t n_prefix, const int32_t* prefix_pages,
+                         const int32_t* block_table, int32_t max_pages, const int32_t* num_pages,
+                         const void* tail_k, const void* tail_v, const int32_t* tail_len,
+                         float sm_scale, void* out, int32_t out_dtype, void* workspace,
+                         size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream);
+
+/* The same over 16-bit pages: sequence b's cache holds ctx_len[b] tokens (behind the prefix).
+ * Everything is taken in the input type; g <= 32. */
+int kitty_f16kv_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
+                                     int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
+                                     size_t* bytes);
+int kitty_f16kv_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_stride,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               int32_t n_tokens, const int32_t* seq_start,
+                               const uint64_t* visible, int32_t max_nodes, const void* pool,
+                               int32_t pool_pages, const int32_t* prefix_table, int32_t n_prefix,
+                               const int32_t* prefix_pages, const int32_t* block_table,
+                               int32_t max_pages, const int32_t* ctx_len, float sm_scale,
+                               void* out, int32_t out_dtype, void* workspace,
+                               size_t workspace_bytes, int32_t B, int32_t* d_status,
+                               void* stream);
+
+/* The accepted path into the packed cache: the rows seq_start[b] + path[b][i], i < path_len[b],
+ * of k and v (as in kitty_tree_attention) appended to sequence b as by kitty_append_token one
+ * after the other, except that the page of a tail that fills is the one that the block
+ * table holds at num_pages[b] already (kitty_page_tables).
+ *   path       device int32 [B][path_width], places in the tree; path_width <=
+ *              KITTY_TREE_MAX_NODES
+ *   path_len   device int32 [B], 0 .. path_width
+ *   counted    0: tail_len and num_pages advance.  1: they count the accepted tokens already
+ *              and are left as they are (layers that share one set of lengths)
+ * A sequence is appended to whole or not at all: KITTY_ST_BAD_TREE for a path entry outside its
+ * tree or a path_len out of range, KITTY_ST_TABLE_FULL and KITTY_ST_BAD_PAGE for the pages of
+ * its full tails, KITTY_ST_BAD_LEN for lengths out of range (a tail that is full already among
+ * them).  Values out of range are reported as by kitty_append_token. */
+int kitty_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
+                      const int32_t* path, int32_t path_width, const int32_t* path_len,
+                      void* tail_k, void* tail_v, int32_t* tail_len, float* run_sum,
+                      float* run_sumsq, int32_t* run_count, const int32_t* block_table,
+                      int32_t max_pages, int32_t* num_pages, void* pool, int32_t pool_pages,
+                      int32_t counted, int32_t B, int32_t* d_status, void* stream);
+
+/* The same into the 16-bit pages, at positions ctx_len[b] .. of the pages that the block table
+ * holds; counted as above, of ctx_len. */
+int kitty_f16kv_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
+                            const int32_t* path, int32_t path_width, const int32_t* path_len,
+                            void* pool, int32_t pool_pages, const int32_t* block_table,
+                            int32_t max_pages, int32_t* ctx_len, int32_t counted, int32_t B,
+                            int32_t* d_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libkitty.so")
 INCLUDE = os.path.join(ROOT, "include")
 
-CU = ["quantize.cu", "decode.cu", "fp16kv.cu", "rope.cu", "shared.cu", "prefix.cu"]
+CU = ["quantize.cu", "decode.cu", "fp16kv.cu", "rope.cu", "shared.cu", "prefix.cu", "tree.cu",
+      "tree_attend.cu"]
 HEADERS = ["kitty_common.cuh", "quant_tile.cuh", "host_common.h", "rope.cuh", "grid_dep.cuh",
            "partials.h", "prefix.h", "tcgen05.cuh"]
 CPP = ["host.cpp"]

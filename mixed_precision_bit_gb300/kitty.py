@@ -18,11 +18,12 @@ OK = 0
 ERR = {-1: "KITTY_ERR_INVALID_ARG", -2: "KITTY_ERR_UNSUPPORTED", -3: "KITTY_ERR_CUDA",
        -4: "KITTY_ERR_WORKSPACE", -5: "KITTY_ERR_OOM"}
 ST = dict(OK=0, EMPTY=1, RANGE=2, NONFINITE=3, BAD_PAGE=4, BAD_LEN=5, TAIL_FULL=6,
-          BAD_FLUSH=7, TABLE_FULL=8, BAD_SEQ=9, TIMEOUT=10)
+          BAD_FLUSH=7, TABLE_FULL=8, BAD_SEQ=9, TIMEOUT=10, NO_PAGES=11, BAD_TREE=12)
 F16, BF16, F32 = 0, 1, 2
 RANK_PAGE, RANK_RUNNING, RANK_SEQUENCE = 0, 1, 2
 D = 128  # channels of a head
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+MAX_NODES = 64  # drafted tokens of a tree
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
 
 
@@ -99,7 +100,9 @@ EXPORTS = ("kitty_abi_version", "kitty_page_bytes", "kitty_avg_bits", "kitty_all
            "kitty_f16kv_decode", "kitty_rope_frequencies", "kitty_rope_turns", "kitty_norm_rope",
            "kitty_append_rope", "kitty_f16kv_append_rope", "kitty_shared_workspace_bytes",
            "kitty_decode_attention_shared", "kitty_f16kv_shared_workspace_bytes",
-           "kitty_f16kv_decode_shared")
+           "kitty_f16kv_decode_shared", "kitty_tree_plan", "kitty_page_tables",
+           "kitty_tree_workspace_bytes", "kitty_tree_attention", "kitty_f16kv_tree_workspace_bytes",
+           "kitty_f16kv_tree_attention", "kitty_tree_commit", "kitty_f16kv_tree_commit")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -161,6 +164,22 @@ def load():
                                                          ctypes.c_float, P, i32, P, sz, i32, P, P]),
             "kitty_f16kv_decode": (ctypes.c_int, [C, P, P, i32, P, i32, P, ctypes.c_float, P, i32,
                                                   P, sz, i32, P, P]),
+            "kitty_tree_plan": (ctypes.c_int, [P, P, i32, P, P, P, P, P, i32, P, P]),
+            "kitty_page_tables": (ctypes.c_int, [P, P, P, i32, i32, i32, i32, P, P, i32, P, P, i32, P, P,
+                                                 i32, P, P]),
+            "kitty_tree_workspace_bytes": (ctypes.c_int, [C, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]),
+            "kitty_f16kv_tree_workspace_bytes": (ctypes.c_int, [C, i32, i32, i32, i32, i32,
+                                                                ctypes.POINTER(sz)]),
+            "kitty_tree_attention": (ctypes.c_int, [C, P, i64, P, i64, P, i64, i32, P, P, i32, P, i32, P,
+                                                    i32, P, P, i32, P, P, P, P, ctypes.c_float, P, i32, P,
+                                                    sz, i32, P, P]),
+            "kitty_f16kv_tree_attention": (ctypes.c_int, [C, P, i64, P, i64, P, i64, i32, P, P, i32, P, i32,
+                                                          P, i32, P, P, i32, P, ctypes.c_float, P, i32, P,
+                                                          sz, i32, P, P]),
+            "kitty_tree_commit": (ctypes.c_int, [C, P, i64, P, i64, i32, P, P, i32, P, P, P, P, P, P, P, P,
+                                                 i32, P, P, i32, i32, i32, P, P]),
+            "kitty_f16kv_tree_commit": (ctypes.c_int, [C, P, i64, P, i64, i32, P, P, i32, P, P, i32, P, i32,
+                                                       P, i32, i32, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -663,3 +682,149 @@ def f16kv_decode_shared(cfg: Config, q, pool, pool_pages: int, prefix_table, pre
         prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev), table, max_pages,
         _ints("ctx_len", ctx_len, B, dev), float(sm_scale), op, _out_dtype(out),
         _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))
+
+
+# ------------------------------------------------------------------ drafted tokens
+def _longs(name: str, t, n: int, dev: int):
+    """Address of a dense 64-bit integer array of at least n entries (None: null)."""
+    if t is None:
+        return None
+    if t.element_size() != 8 or t.is_floating_point() or t.is_complex() or t.numel() < n:
+        raise ValueError("kitty: %s must be 64-bit integers, %d entries (got %s, %s)"
+                         % (name, n, tuple(t.shape), t.dtype))
+    if t.get_device() != dev or not t.is_contiguous():
+        _dense(t, dev)
+    return t.data_ptr()
+
+
+def tree_plan(parents, seq_start, lens, visible, positions, num_pages=None, pos_base=None, status=None,
+              stream=None):
+    """Ancestor masks (visible, 64-bit [n]) and positions (int32 [n]) of the drafted trees whose
+    parents [n] are given as places in the own tree, -1 for a node that follows the cached tokens
+    (kitty_tree_plan); seq_start [B + 1] marks the sequences' rows.  visible or positions may be
+    None."""
+    dev, n, B = _device(), parents.numel(), lens.numel()
+    _chk("kitty_tree_plan", load().kitty_tree_plan(
+        _ints("parents", parents, n, dev), _ints("seq_start", seq_start, B + 1, dev), n,
+        _ints("num_pages", num_pages, B, dev), _ints("lens", lens, B, dev),
+        _ints("pos_base", pos_base, B, dev), _longs("visible", visible, n, dev),
+        _ints("positions", positions, n, dev), B, _dense(status, dev), _raw_stream(stream, dev)))
+
+
+def page_tables(lens, held, block_table, free_ids, free_count, num_pages=None, seq_start=None,
+                extra: int = 0, partial: bool = True, shrink: bool = False, slots=None,
+                new_page_ids=None, status=None, stream=None):
+    """Pages for 32 * num_pages + lens tokens of each sequence, the new ones that seq_start [B + 1]
+    marks and `extra` more, from the stack free_ids[:free_count] on the device into the block
+    table, whose rows hold `held` pages; shrink: those beyond go back (kitty_page_tables).  slots
+    (64-bit) and new_page_ids (int32), one entry a new token, may be None."""
+    dev, B = _device(), lens.numel()
+    table, max_pages = _table(block_table, B, dev)
+    n = max((t.numel() for t in (slots, new_page_ids) if t is not None), default=0)
+    if seq_start is not None and n == 0:
+        n = 0x7FFFFFFF  # no rows are written: any starts will do
+    _chk("kitty_page_tables", load().kitty_page_tables(
+        _ints("num_pages", num_pages, B, dev), _ints("lens", lens, B, dev),
+        _ints("seq_start", seq_start, B + 1, dev), n, extra, int(partial), int(shrink),
+        _ints("held", held, B, dev), table, max_pages, _ints("free_ids", free_ids, 0, dev),
+        _ints("free_count", free_count, 1, dev), free_ids.numel(), _longs("slots", slots, n, dev),
+        _ints("new_page_ids", new_page_ids, n, dev), B, _dense(status, dev), _raw_stream(stream, dev)))
+
+
+def _tree_bytes(name, cfg, B, n_tokens, max_nodes, n_prefix, max_pages):
+    n = ctypes.c_size_t()
+    _chk(name, getattr(load(), name)(cfg.ref(), B, n_tokens, max_nodes, n_prefix, max_pages, ctypes.byref(n)))
+    return n.value
+
+
+def tree_workspace_bytes(cfg: Config, B: int, n_tokens: int, max_nodes: int, max_pages: int,
+                         n_prefix: int = 0) -> int:
+    return _tree_bytes("kitty_tree_workspace_bytes", cfg, B, n_tokens, max_nodes, n_prefix, max_pages)
+
+
+def f16kv_tree_workspace_bytes(cfg: Config, B: int, n_tokens: int, max_nodes: int, max_pages: int,
+                               n_prefix: int = 0) -> int:
+    return _tree_bytes("kitty_f16kv_tree_workspace_bytes", cfg, B, n_tokens, max_nodes, n_prefix, max_pages)
+
+
+def _tree_rows(cfg, q, k, v, out, dev):
+    """(rows, the addresses and strides of q, k, v, the address of out [n, Hq, 128])."""
+    n = q.shape[0]
+    if out.shape != (n, cfg.num_q_heads, D):
+        raise ValueError("kitty: out must be [%d, %d, %d] (got %s)" % (n, cfg.num_q_heads, D, tuple(out.shape)))
+    return n, (*_rows(q, n, cfg.num_q_heads, dev, cfg.in_dtype), *_rows(k, n, cfg.num_kv_heads, dev, cfg.in_dtype),
+               *_rows(v, n, cfg.num_kv_heads, dev, cfg.in_dtype)), _dense(out, dev)
+
+
+def tree_attention(cfg: Config, q, k, v, seq_start, visible, max_nodes: int, pool, pool_pages: int,
+                   block_table, num_pages, tail_k, tail_v, tail_len, sm_scale: float, out,
+                   prefix_table=None, prefix_pages=None, workspace=None, status=None, stream=None):
+    """Attention of drafted tokens q [n, Hq, 128] to their sequences' cached tokens and to the
+    drafted tokens k, v [n, Hkv, 128] of their masks (kitty_tree_attention); seq_start [B + 1]
+    marks the sequences' rows, visible (64-bit [n]; None: chains) which nodes each sees."""
+    dev, B = _device(), num_pages.numel()
+    n, rows, op = _tree_rows(cfg, q, k, v, out, dev)
+    table, max_pages = _table(block_table, B, dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _chk("kitty_tree_attention", load().kitty_tree_attention(
+        cfg.ref(), *rows, n, _ints("seq_start", seq_start, B + 1, dev), _longs("visible", visible, n, dev),
+        max_nodes, _dense(pool, dev), pool_pages, _ints("prefix_table", prefix_table, 0, dev),
+        0 if prefix_table is None else prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev),
+        table, max_pages, _ints("num_pages", num_pages, B, dev), _tail(tail_k, cfg, B, dev),
+        _tail(tail_v, cfg, B, dev), _ints("tail_len", tail_len, B, dev), float(sm_scale), op,
+        _out_dtype(out), _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))
+
+
+def f16kv_tree_attention(cfg: Config, q, k, v, seq_start, visible, max_nodes: int, pool, pool_pages: int,
+                         block_table, ctx_len, sm_scale: float, out, prefix_table=None, prefix_pages=None,
+                         workspace=None, status=None, stream=None):
+    """tree_attention over 16-bit pages (kitty_f16kv_tree_attention)."""
+    dev, B = _device(), ctx_len.numel()
+    n, rows, op = _tree_rows(cfg, q, k, v, out, dev)
+    table, max_pages = _table(block_table, B, dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _chk("kitty_f16kv_tree_attention", load().kitty_f16kv_tree_attention(
+        cfg.ref(), *rows, n, _ints("seq_start", seq_start, B + 1, dev), _longs("visible", visible, n, dev),
+        max_nodes, _dense(pool, dev), pool_pages, _ints("prefix_table", prefix_table, 0, dev),
+        0 if prefix_table is None else prefix_table.numel(), _ints("prefix_pages", prefix_pages, B, dev),
+        table, max_pages, _ints("ctx_len", ctx_len, B, dev), float(sm_scale), op, _out_dtype(out),
+        _dense(workspace, dev), ws_bytes, B, _dense(status, dev), _raw_stream(stream, dev)))
+
+
+def _path(path, path_len, B, dev):
+    """(address, entries a row, address of the counts) of accepted paths [>= B, width]."""
+    if path.dim() != 2 or path.shape[0] < B:
+        raise ValueError("kitty: paths must be [%d, width] (got %s)" % (B, tuple(path.shape)))
+    return _ints("path", path, 0, dev), path.shape[1], _ints("path_len", path_len, B, dev)
+
+
+def tree_commit(cfg: Config, k, v, seq_start, path, path_len, tail_k, tail_v, tail_len, run_sum, run_sumsq,
+                run_count, block_table, num_pages, pool, pool_pages: int, counted: bool = False,
+                status=None, stream=None):
+    """The accepted drafted tokens, rows path[b, :path_len[b]] of each sequence's in k, v
+    [n, Hkv, 128], into the packed cache (kitty_tree_commit); full tails are quantized into the
+    pages that the block table holds behind num_pages already (page_tables)."""
+    dev, n, B, dt = _device(), k.shape[0], tail_len.numel(), cfg.in_dtype
+    kp, ks = _rows(k, n, cfg.num_kv_heads, dev, dt)
+    vp, vs = _rows(v, n, cfg.num_kv_heads, dev, dt)
+    table, max_pages = _table(block_table, B, dev)
+    _chk("kitty_tree_commit", load().kitty_tree_commit(
+        cfg.ref(), kp, ks, vp, vs, n, _ints("seq_start", seq_start, B + 1, dev), *_path(path, path_len, B, dev),
+        _tail(tail_k, cfg, B, dev), _tail(tail_v, cfg, B, dev), _ints("tail_len", tail_len, B, dev),
+        _dense(run_sum, dev), _dense(run_sumsq, dev), _dense(run_count, dev), table, max_pages,
+        _ints("num_pages", num_pages, B, dev), _dense(pool, dev), pool_pages, int(counted), B,
+        _dense(status, dev), _raw_stream(stream, dev)))
+
+
+def f16kv_tree_commit(cfg: Config, k, v, seq_start, path, path_len, pool, pool_pages: int, block_table, ctx_len,
+                      counted: bool = False, status=None, stream=None):
+    """The accepted drafted tokens into the 16-bit pages that the block table holds
+    (kitty_f16kv_tree_commit)."""
+    dev, n, B, dt = _device(), k.shape[0], ctx_len.numel(), cfg.in_dtype
+    kp, ks = _rows(k, n, cfg.num_kv_heads, dev, dt)
+    vp, vs = _rows(v, n, cfg.num_kv_heads, dev, dt)
+    table, max_pages = _table(block_table, B, dev)
+    _chk("kitty_f16kv_tree_commit", load().kitty_f16kv_tree_commit(
+        cfg.ref(), kp, ks, vp, vs, n, _ints("seq_start", seq_start, B + 1, dev), *_path(path, path_len, B, dev),
+        _dense(pool, dev), pool_pages, table, max_pages, _ints("ctx_len", ctx_len, B, dev), int(counted), B,
+        _dense(status, dev), _raw_stream(stream, dev)))
