@@ -959,7 +959,8 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The 16-bit pool as rows of 128 channels; boxes of 32 rows by 64 channels, swizzled.
+}  // namespace
+
 bool pool_map(CUtensorMap* map, const void* pool, uint64_t rows) {
   static std::atomic<EncodeTiled> encode{nullptr};
   EncodeTiled f = encode.load();
@@ -978,6 +979,8 @@ bool pool_map(CUtensorMap* map, const void* pool, uint64_t rows) {
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <class F>
 int launch(const PrefixArgs& a, const PrefixPlan& pl, const CUtensorMap& map, cudaStream_t s) {

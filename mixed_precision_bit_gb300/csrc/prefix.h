@@ -1,6 +1,7 @@
 // The prefix kernel of the shared-prefix decode: its arguments, plan and launch.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,5 +34,8 @@ PrefixPlan prefix_plan(const kitty_cfg* cfg, bool packed, int B, int n_prefix, i
 // have started.
 int prefix_launch(const kitty_cfg* cfg, bool packed, const PrefixArgs& args, const PrefixPlan& plan,
                   cudaStream_t stream);
+
+// A 16-bit pool as `rows` rows of 128 channels; boxes of 32 rows by 64 channels, swizzled.
+bool pool_map(CUtensorMap* map, const void* pool, uint64_t rows);
 
 }  // namespace kitty

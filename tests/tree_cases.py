@@ -100,11 +100,14 @@ class Base:
 
     def answer(self, rounding=1.0):
         """(outputs [T, Hq, 128] in 64 bits, how far each may be off).  What is rounded: a probability
-        to fp16 or to two halves of a type (2^-11 of it at most), a dequantized Value to fp16 (2^-11),
+        to fp16 or to two halves of a type (2^-11 of it at most); the middle of a group of Values to fp16
+        (2^-11 of it, which is no more than the group's largest Value), a tail's or a node's Value times 2^-4
+        at least to fp16 (exact, or off by half a step of the smallest numbers: 2^-25 * 2^4);
         for 8-bit boosted Keys step * code (2^-11); the fp32 sums of a score move it by less than 2^-19 of
-        the sum of its products' magnitudes (8 chunks of 16 exact products, each sum cut off at 2^-23), so
-        a weight by the exponential of that; and since the weights sum to 1,
-          |out' - out| <= sum p (2^-11 + expm1(d)) |v - out| exp(max d) + 2^-11 sum p |v|."""
+        the sum of its products' magnitudes (8 chunks of 16 exact products, each sum cut off at 2^-23; on
+        packed pages q . (step * code) and q . minimum are formed apart), so a weight by the
+        exponential of that; and since the weights sum to 1,
+          |out' - out| <= sum p (2^-11 + expm1(d)) |v - out| exp(max d) + 2^-11 sum p max|v| + 2^-21."""
         Hq, Hkv, g = self.Hq, self.Hkv, self.Hq // self.Hkv
         x = synth.from_bits(self.rows, self.dt).astype(np.float64)
         out = np.zeros((int(self.start[-1]), Hq, D))
@@ -115,27 +118,29 @@ class Base:
                 continue
             seen = sees(self.visible, self.start, b)
             for h in range(Hkv):
-                k, v, part = self.cached(b, h)
+                k, v, part, size, most = self.cached(b, h)
                 c = k.shape[0]
                 k = np.concatenate([k, x[lo:lo + n, Hq + h]])
                 v = np.concatenate([v, x[lo:lo + n, Hq + Hkv + h]])
                 part = np.concatenate([part, np.zeros((n, D))])
+                size = np.concatenate([size, np.abs(x[lo:lo + n, Hq + h])])
+                most = np.concatenate([most, np.abs(x[lo:lo + n, Hq + Hkv + h])])
                 q = x[lo:lo + n, h * g:(h + 1) * g].reshape(n * g, D)
                 on = np.concatenate([np.ones((n, c), bool), seen], 1).repeat(g, 0)
                 with np.errstate(invalid="ignore"):
-                    k, v, part = (np.where(np.isfinite(y), y, 0.0) for y in (k, v, part))
+                    k, v, part, size, most = (np.where(np.isfinite(y), y, 0.0) for y in (k, v, part, size, most))
                 s = np.where(on, SM * (q @ k.T), -np.inf)
                 m = s.max(1, initial=-np.inf, keepdims=True)
                 p = np.where(on, np.exp(s - np.where(np.isfinite(m), m, 0)), 0.0)
                 total = p.sum(1, keepdims=True)
                 p = np.divide(p, total, out=np.zeros_like(p), where=total > 0)
                 o = p @ v
-                d = SM * (2.0 ** -19 * (np.abs(q) @ np.abs(k).T) + 2.0 ** -11 * (np.abs(q) @ part.T))
+                d = SM * (2.0 ** -19 * (np.abs(q) @ size.T) + 2.0 ** -11 * (np.abs(q) @ part.T))
                 grow = np.exp(np.where(on, d, 0).max(1, initial=0.0))
                 rows = slice(lo, lo + n), slice(h * g, (h + 1) * g)
                 out[rows] = o.reshape(n, g, D)
                 e = np.stack([((p[i] * (rounding * 2.0 ** -11 + np.expm1(d[i]))) @ np.abs(v - o[i])) * grow[i]
-                              + rounding * 2.0 ** -11 * (p[i] @ np.abs(v)) for i in range(n * g)])
+                              + rounding * 2.0 ** -11 * (p[i] @ most) + 2.0 ** -21 for i in range(n * g)])
                 off[rows] = e.reshape(n, g, D)
         return out, off
 
@@ -190,12 +195,13 @@ class PackedTree(Base):
                              **self.prefix_args())
 
     def cached(self, b, h):
-        """Keys, Values, and of each Key the part that is rounded to fp16, of what b holds."""
+        """Keys, Values, of each Key the part that is rounded to fp16, the magnitudes whose products a
+        score sums, and the largest Value of each Value's group, of what b holds."""
         if not hasattr(self, "_pages"):
             self._pages, self._blobs = {}, self.pool.cpu().numpy().reshape(self.pool_pages, self.Hkv, -1)
         ids = np.concatenate([self.prefix[:self.n_prefix if self.shared is None else self.shared[b]],
                               self.bt[b, :self.own[b]]])
-        ks, vs, parts = [np.zeros((0, D))], [np.zeros((0, D))], [np.zeros((0, D))]
+        ks, vs, parts, sizes, mosts = ([np.zeros((0, D))] for _ in range(5))
         for pid in ids:
             if (pid, h) not in self._pages:
                 blob = self._blobs[pid, h]
@@ -204,14 +210,18 @@ class PackedTree(Base):
                 if self.lo_bit == 4 and self.n_hi:
                     ch = np.asarray(oracle.page_channels(blob, self.n_hi, 4), int)
                     part[:, ch] = (k - k.min(0))[:, ch]
-                self._pages[pid, h] = k, v, part
-            for lst, y in zip((ks, vs, parts), self._pages[pid, h]):
+                # (the token of a channel's minimum has code 0)
+                self._pages[pid, h] = (k, v, part, np.abs(k.min(0)) + (k - k.min(0)),
+                                       np.abs(v).reshape(P, 4, 32).max(2).repeat(32, 1))
+            for lst, y in zip((ks, vs, parts, sizes, mosts), self._pages[pid, h]):
                 lst.append(y)
         n = self.tails[b]
         for lst, y in ((ks, self.tail_k), (vs, self.tail_v)):
             lst.append(synth.from_bits(y[b, h, :n], self.dt).astype(np.float64))
         parts.append(np.zeros((n, D)))
-        return np.concatenate(ks), np.concatenate(vs), np.concatenate(parts)
+        sizes.append(np.abs(ks[-1]))
+        mosts.append(np.abs(vs[-1]))
+        return tuple(np.concatenate(x) for x in (ks, vs, parts, sizes, mosts))
 
 
 class Plain16Tree(Base):
@@ -264,7 +274,7 @@ class Plain16Tree(Base):
         x = synth.from_bits(self.host[ids, h], self.dt).astype(np.float64)  # [pages, 2, 32, 128]
         n += P * (len(ids) - (n + P - 1) // P)
         k, v = x[:, 0].reshape(-1, D)[:n], x[:, 1].reshape(-1, D)[:n]
-        return k, v, np.zeros_like(k)
+        return k, v, np.zeros_like(k), np.abs(k), np.abs(v)
 
 
 def half_step(x, out_dtype):
