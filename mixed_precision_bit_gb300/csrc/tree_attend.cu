@@ -4,8 +4,8 @@
 //   out[t][hq] = softmax(sm_scale * q . [K_prefix; K_b; K_tree]) . [V_prefix; V_b; V_tree]
 //
 // Rows.  The query heads of a kv head over the nodes of a sequence's tree, node by node: n * g
-// rows that see the same cached tokens.  One block takes up to N of them (N = 16, 32, 64, 128 by
-// the largest tree) and a share of the sequence's tiles of 128 tokens.  Tokens are the
+// rows that see the same cached tokens.  One block takes up to N of them (N = 16, 32, 64 by the
+// largest tree) and a share of the sequence's tiles of 128 tokens.  Tokens are the
 // products' 128 rows and query rows their N columns, so that a product costs what the rows
 // need: 16 rows an eighth of 128.  Per tile
 //   S^T = K Q^T         128 x N x 128, fp32 in tensor memory
@@ -14,6 +14,15 @@
 // The reference m of a row is set 2^4 below its maximum over the first tile and moves only when a
 // score passes it by more than 2^15: what p loses below 2^-25 is 2^-29 of the largest then.
 // A row decides by its own scores, so its bytes do not depend on the others.
+//
+// Even and odd tiles are two pipelines with warps, references and outputs of their own, which share
+// the products' warp and are joined at the end.  Every kind of work has its warps, and what bounds
+// the block is the rate at which their instructions come: it was 3400 cycles a tile of 64 rows with
+// the loops unrolled (120 KB of code) and is 2500 with loops of a few dozen instructions
+// (94 KB, most of it run once; scores 16 columns at a time, a page's Keys in quarters).
+// Measured, 8 kv heads of 2-bit pages: 64 sequences x 8192 tokens x 16 nodes x 4 heads 335 us (411
+// TFLOP/s, 1.3 TB/s), 8 x 32768 x 64 nodes x 8 heads 863 us (638 TFLOP/s); of 16-bit pages: 32 x
+// 8192 x 16 x 4 210 us (5.1 TB/s).
 //
 // Packed pages (four to a tile) are staged whole by bulk copies and dequantized straight into
 // tensor memory: the planes' fragment order is that of 16-row stores of 128 bits, whose
@@ -49,14 +58,17 @@ namespace {
 
 constexpr int kMaxNodes = KITTY_TREE_MAX_NODES;
 constexpr int kTile = 128, kTilePages = 4;
-constexpr int kSoftmaxWarps = 8;  // two groups of four, each with half of the rows
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kFetchWarp = 17, kBiasWarp = 18, kSumWarp = 19;
-constexpr int kTreeThreads = 640;
-constexpr int kMaxRaw = 4;        // staged tiles of packed pages
+// Warps: of each kind one half for the even tiles and one for the odd ones.  Softmax (a thread a
+// token), the Keys' operand (a warp a page), the Values' (a warp a group of channels), q.M, the sums;
+// then one that issues products and one that requests copies.  16-bit pages have no use for the
+// operands' but for the loose tokens, and one of q.M's requests the Values.
+constexpr int kSoftmaxWarps = 8, kKeyWarp = 8, kValueWarp = 16, kBiasWarp = 24, kSumWarp = 26, kMmaWarp = 30, kFetchWarp = 31;
+constexpr int kTreeThreads = 1024;
+constexpr int kMaxRaw = 4;        // staged tiles of packed pages: 2 or 4 (a warp sees every other one)
 constexpr int kFlags = 16;        // tiles whose page flags are kept
 constexpr int kLoose = 96;        // loose tokens: 32 of the tail, 64 nodes
 constexpr int kLoosePitch = 272;
-constexpr uint32_t kTreeWaitPolls = 1u << 22;
+constexpr uint32_t kTreeWaitPolls = 1u << 20;
 constexpr float kFloor = -1.0e30f;
 constexpr float kSlack = 15.f;    // log2 units that a score may pass m by
 constexpr float kMargin = -4.f;   // m against the maximum, when it is set
@@ -86,29 +98,32 @@ template <int W_, int V_, int N_>
 struct PackedTree {
   static constexpr bool kPacked = true, kBf16 = false, kPair = false;
   static constexpr int W = W_, V = V_, N = N_;
-  static constexpr int kOps = N == 128 ? 1 : 2;  // stages of the Key and Value operands
-  static constexpr int kVCol = 64 * kOps, kSCol = 128 * kOps;
+  static constexpr int kOpCols = 256;  // Keys' operands (two of 64 columns), then the Values'
 };
 // 16-bit pages.
 template <bool BF, int N_>
 struct PlainTree {
   static constexpr bool kPacked = false, kBf16 = BF, kPair = true;
   static constexpr int W = 0, V = 0, N = N_;
-  static constexpr int kOps = 2;
-  static constexpr int kVCol = 0, kSCol = 0;
+  static constexpr int kOpCols = 0;
 };
 template <class F>
 struct Sizes {
-  static constexpr int N = F::N, C = N / 2;           // rows; columns of a softmax group
+  static constexpr int N = F::N;
   static constexpr int kQHalf = N * 128, kQ = 2 * kQHalf;
-  static constexpr int kPBlock = kTile * 128;          // 64 rows of 128 tokens
-  static constexpr int kPHalf = kPBlock * (N > 64 ? 2 : 1), kP = kPHalf * (F::kPair ? 2 : 1);
-  static constexpr int kOCol = F::kSCol + 2 * N, kCols = kOCol + N;
+  static constexpr int kPHalf = kTile * 128, kP = kPHalf * (F::kPair ? 2 : 1);  // 128 tokens of 64 rows
+  static constexpr int kSCol = F::kOpCols, kOCol = kSCol + 2 * N, kCols = kOCol + 2 * N;
   static constexpr int kHalf16 = kTile * 128, kTile16 = 2 * kHalf16;  // a 16-bit tile of Keys or Values
   static constexpr int kSpread = F::kPacked ? 512 * F::W : 0;         // a page's low codes in base-plane order
-  static constexpr int kFixed = kQ + 2 * kP + (F::kPacked ? 2 * kLoose * kLoosePitch + 4 * kSpread + F::kOps * 1024
-                                                         : 2 * F::kOps * kTile16);
+  static constexpr int kPs = F::kPacked ? 4 : 2;                      // tiles whose p are kept
+  static constexpr int kFixed = kQ + kPs * kP + (F::kPacked ? 2 * kLoose * kLoosePitch + 8 * kSpread + 4 * 1024
+                                                         : 4 * kTile16);
 };
+
+// Shared memory of a block of packed pages without its staged tiles, and with `stages` of them.
+constexpr int kSharedMost = 227 * 1024;
+template <class F>
+constexpr int fixed_bytes() { return 1024 + Sizes<F>::kFixed; }
 
 struct Held {  // of one sequence
   int first, n;              // its drafted rows
@@ -153,13 +168,27 @@ __device__ __forceinline__ Held held_of(const TreeParams& p, int b) {
 }
 
 // ------------------------------------------------------------- small pieces
-__device__ __forceinline__ bool wait_lanes(bool need, uint32_t a, uint32_t parity, uint32_t polls, volatile int* abort) {
-  bool done = !need;
-  for (uint32_t i = 0;; ++i) {
-    done = done || mbar_try(a, parity);
-    if (__all_sync(0xFFFFFFFFu, done)) return true;
-    const bool stop = i >= polls || *abort != 0;
-    if (__any_sync(0xFFFFFFFFu, stop)) break;
+// One poll of a barrier phase, in which the hardware may suspend the thread for a while.  (With a time
+// given it becomes a loop of naps: 5000 of 11300 instructions a tile were polls and their votes.)
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Whole warp: waits for a phase, at most `polls` polls; false when it, or another warp of the block, has
+// given up.
+__device__ __forceinline__ bool wait_phase(uint64_t& bar, int parity, uint32_t polls, volatile int* abort) {
+  const uint32_t a = smem_u32(&bar), ph = (uint32_t)parity;
+#pragma unroll 1
+  for (uint32_t i = 0; i < polls; ++i) {
+    if (__all_sync(0xFFFFFFFFu, try_phase(a, ph))) return true;
+    if (*abort != 0) return false;
   }
   *abort = 1;
   return false;
@@ -214,13 +243,10 @@ __host__ __device__ constexpr uint32_t two(uint32_t half) { return half * 0x0001
 
 // 16 lanes (rows) of tensor memory: the register pair (2i, 2i + 1) of lane (r, qq) goes to column
 // 4i + qq of rows r and r + 8.
-__device__ __forceinline__ void tmem_st_frag(uint32_t a, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_frag(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -247,6 +273,24 @@ __device__ __forceinline__ void tmem_load(uint32_t a, uint32_t (&x)[C]) {
   for (int k = 0; k < C; ++k) pin(x[k]);
 }
 
+// D(16x8 f32) = A(16x16 f16) * B(16x8 f16), warp-wide, where A's rows 8 .. 15 are zeros.
+__device__ __forceinline__ void mma_rows8(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
+      "{%9,%9,%9,%9};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// (a, b) = (a, b) * scale + (c, d)
+__device__ __forceinline__ void fma2(uint32_t& a, uint32_t& b, uint64_t scale, uint32_t c, uint32_t d) {
+  uint64_t e, s;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(e) : "r"(a), "r"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "r"(c), "r"(d));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(e), "l"(scale), "l"(s));
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(e));
+}
+
 // Or over the 128 threads of a softmax group, which all come here.
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
@@ -263,6 +307,16 @@ __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.s
 // ------------------------------------------------------------- packed Keys
 // A code at bits 2 + sh of a 16-bit half under the exponent of 16 reads 16 + code * 2^(sh - 4).
 constexpr uint32_t k16 = two(0x4C00);
+// (x & mask) | 16.0: one instruction, if both constants are in registers (the compiler made two of it).
+struct Codes {
+  uint32_t sixteen;
+  __device__ __forceinline__ Codes() { asm volatile("mov.b32 %0, %1;" : "=r"(sixteen) : "n"(k16)); }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t mask) const {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(sixteen));
+    return y;
+  }
+};
 
 // The low codes of a page's boosted channels, spread into base-plane order at `to` (512 W bytes,
 // zeros where a channel has none).  Whole warp.
@@ -275,7 +329,7 @@ __device__ __forceinline__ void spread_low(uint32_t raw, uint32_t to, int n_hi) 
   __syncwarp();
   const uint32_t kch = raw + 512 * W + 4 * W * n_hi + 512, plane = raw + 512 * W + 2 * W * nx * lane;
   const uint32_t mine = to + 64 * W * r;  // the lanes of this lane's tokens
-#pragma unroll 2
+#pragma unroll 1
   for (int js = 0; js < nx; ++js) {
     const uint32_t ids = lds32(kch + 16 * js + 4 * qq);
 #pragma unroll
@@ -285,7 +339,7 @@ __device__ __forceinline__ void spread_low(uint32_t raw, uint32_t to, int n_hi) 
       x = __funnelshift_r(x, x, 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t c = (ids >> (8 * i)) & 127u, byte = (x >> (8 * (2 * (i & 1) + (i >> 1)))) & 255u;
+        const uint32_t c = (ids >> (8 * i)) & 127u, byte = x >> (8 * (2 * (i & 1) + (i >> 1)));
         // word of channel c: lane (r, (c & 7) / 2), k-step c / 16 (W = 4: and mt); its byte there
         sts8(mine + 16 * W * ((c & 7) >> 1) + 2 * W * (c >> 4) + 4 * mt + 2 * (c & 1) + ((c >> 3) & 1), byte);
       }
@@ -295,90 +349,88 @@ __device__ __forceinline__ void spread_low(uint32_t raw, uint32_t to, int n_hi) 
 }
 
 // A page's Keys, staged at raw, to the 32 lanes of tensor memory at `to`: 64 columns of channel pairs.
-// (For spread words bytes are not rotated: they are rotated as they are taken.)
+// (Spread words are not rotated as a plane's are: that is done here.)
 template <int W>
 __device__ __forceinline__ void put_keys(uint32_t raw, uint32_t to, uint32_t spread, int n_hi, int32_t* d_status) {
   const int lane = threadIdx.x & 31, qq = lane & 3;
-  const uint32_t ks = raw + 512 * W + 4 * W * n_hi, sq = ks + 4 * qq;
+  const uint32_t ks = raw + 512 * W + 4 * W * n_hi;
   const bool boosted = n_hi > 0;
+  const Codes at16;
   if (boosted) spread_low<W>(raw, spread, n_hi);
+#pragma unroll 1
+  for (int part = 0; part < 4; ++part) {
+  const uint32_t sq = ks + 64 * part + 4 * qq;
+  uint32_t w[W], lo[W];  // of two k-steps
 #pragma unroll
-  for (int jc = 0; jc < 8; jc += 4) {  // four k-steps: 32 columns
-    uint32_t w[2 * W], lo[2 * W];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-      const uint4 a = lds128(raw + 16 * W * lane + 2 * W * jc + 16 * i);
-      w[4 * i] = a.x;
-      w[4 * i + 1] = a.y;
-      w[4 * i + 2] = a.z;
-      w[4 * i + 3] = a.w;
-      if (boosted) {
-        const uint4 c = lds128(spread + 16 * W * lane + 2 * W * jc + 16 * i);
-        lo[4 * i] = c.x;
-        lo[4 * i + 1] = c.y;
-        lo[4 * i + 2] = c.z;
-        lo[4 * i + 3] = c.w;
-      }
+  for (int i = 0; i < W / 2; ++i) {
+    const uint2 a = lds64(raw + 16 * W * lane + 4 * W * part + 8 * i);
+    w[2 * i] = a.x;
+    w[2 * i + 1] = a.y;
+    if (boosted) {
+      const uint2 c = lds64(spread + 16 * W * lane + 4 * W * part + 8 * i);
+      lo[2 * i] = c.x;
+      lo[2 * i + 1] = c.y;
     }
-    uint32_t a[2][16];
+  }
+  uint32_t a[2][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t S[2] = {lds32(sq + 32 * (jc + j)), lds32(sq + 32 * (jc + j) + 16)};
-      const uint32_t T[2] = {h2mul(S[0], two(0xCC00)), h2mul(S[1], two(0xCC00))};  // -16 S
-      if (W == 2) {
-        if (!boosted) {
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t S[2] = {lds32(sq + 32 * j), lds32(sq + 32 * j + 16)};
+    const uint32_t T[2] = {h2mul(S[0], two(0xCC00)), h2mul(S[1], two(0xCC00))};  // -16 S
+    if (W == 2) {
+      if (!boosted) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = h ? __funnelshift_r(w[j], w[j], 8) : w[j];
-            uint32_t* o0 = &a[0][2 * (2 * j + h)];
-            uint32_t* o1 = &a[1][2 * (2 * j + h)];
-            o0[0] = h2fma((x & two(0x000C)) | k16, S[h], T[h]);
-            o0[1] = h2fma((x & two(0x0030)) | k16, S[h], T[h]);
-            o1[0] = h2fma((x & two(0x00C0)) | k16, S[h], T[h]);
-            o1[1] = h2fma((x & two(0x0300)) | k16, S[h], T[h]);
-          }
-        } else {
-          // 4-bit codes at bits 2 and 6: of the tokens' blocks 0, 2 and of 1, 3.  lo: not rotated.
-          const uint32_t y = __funnelshift_l(lo[j], lo[j], 2), up = __funnelshift_l(w[j], w[j], 2);
-          const uint32_t A = (up & 0x33333333u) | (y & 0xCCCCCCCCu);
-          const uint32_t B = (w[j] & 0x33333333u) | (lo[j] & 0xCCCCCCCCu);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t xa = h ? __funnelshift_r(A, A, 8) : A, xb = h ? __funnelshift_r(B, B, 8) : B;
-            uint32_t* o0 = &a[0][2 * (2 * j + h)];
-            uint32_t* o1 = &a[1][2 * (2 * j + h)];
-            o0[0] = h2fma((xa & two(0x003C)) | k16, S[h], T[h]);
-            o0[1] = h2fma((xb & two(0x003C)) | k16, S[h], T[h]);
-            o1[0] = h2fma((xa & two(0x03C0)) | k16, S[h], T[h]);
-            o1[1] = h2fma((xb & two(0x03C0)) | k16, S[h], T[h]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = h ? __funnelshift_r(w[j], w[j], 8) : w[j];
+          uint32_t* o0 = &a[0][2 * (2 * j + h)];
+          uint32_t* o1 = &a[1][2 * (2 * j + h)];
+          o0[0] = h2fma(at16(x, two(0x000C)), S[h], T[h]);
+          o0[1] = h2fma(at16(x, two(0x0030)), S[h], T[h]);
+          o1[0] = h2fma(at16(x, two(0x00C0)), S[h], T[h]);
+          o1[1] = h2fma(at16(x, two(0x0300)), S[h], T[h]);
         }
       } else {
+        // 4-bit codes at bits 2 and 6: of the tokens' blocks 0, 2 and of 1, 3.  lo: not rotated.
+        const uint32_t y = __funnelshift_l(lo[j], lo[j], 2), up = __funnelshift_l(w[j], w[j], 2);
+        const uint32_t A = (up & 0x33333333u) | (y & 0xCCCCCCCCu);
+        const uint32_t B = (w[j] & 0x33333333u) | (lo[j] & 0xCCCCCCCCu);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t x0 = w[(2 * j + mt) % (2 * W)];
-          const uint32_t l0 = boosted ? __funnelshift_l(lo[(2 * j + mt) % (2 * W)], lo[(2 * j + mt) % (2 * W)], 2) : 0;
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t xa = h ? __funnelshift_r(A, A, 8) : A, xb = h ? __funnelshift_r(B, B, 8) : B;
+          uint32_t* o0 = &a[0][2 * (2 * j + h)];
+          uint32_t* o1 = &a[1][2 * (2 * j + h)];
+          o0[0] = h2fma(at16(xa, two(0x003C)), S[h], T[h]);
+          o0[1] = h2fma(at16(xb, two(0x003C)), S[h], T[h]);
+          o1[0] = h2fma(at16(xa, two(0x03C0)), S[h], T[h]);
+          o1[1] = h2fma(at16(xb, two(0x03C0)), S[h], T[h]);
+        }
+      }
+    } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = h ? __funnelshift_r(x0, x0, 8) : x0;
-            uint32_t* o = &a[mt][2 * (2 * j + h)];
-            o[0] = h2fma((x & two(0x003C)) | k16, S[h], T[h]);
-            o[1] = h2fma((x & two(0x03C0)) | k16, S[h], T[h]);
-            if (boosted) {  // + S / 16 * low code, rounded once
-              const uint32_t l = h ? __funnelshift_r(l0, l0, 8) : l0, s = h2mul(S[h], two(0x2C00));
-              o[0] = h2fma(h2add((l & two(0x003C)) | k16, two(0xCC00)), s, o[0]);
-              o[1] = h2fma(h2add((l & two(0x03C0)) | k16, two(0xCC00)), s, o[1]);
-            }
+      for (int mt = 0; mt < 2; ++mt) {
+        const uint32_t x0 = w[(2 * j + mt) % W];
+        const uint32_t l0 = boosted ? __funnelshift_l(lo[(2 * j + mt) % W], lo[(2 * j + mt) % W], 2) : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = h ? __funnelshift_r(x0, x0, 8) : x0;
+          uint32_t* o = &a[mt][2 * (2 * j + h)];
+          o[0] = h2fma(at16(x, two(0x003C)), S[h], T[h]);
+          o[1] = h2fma(at16(x, two(0x03C0)), S[h], T[h]);
+          if (boosted) {  // + S / 16 * low code, rounded once
+            const uint32_t l = h ? __funnelshift_r(l0, l0, 8) : l0, s = h2mul(S[h], two(0x2C00));
+            o[0] = h2fma(h2add(at16(l, two(0x003C)), two(0xCC00)), s, o[0]);
+            o[1] = h2fma(h2add(at16(l, two(0x03C0)), two(0xCC00)), s, o[1]);
           }
         }
       }
     }
-    tmem_st_frag(to + 8 * jc, a[0]);
-    tmem_st_frag(to + 8 * jc + (16u << 16), a[1]);
+  }
+  tmem_st_frag(to + 16 * part, a[0]);
+  tmem_st_frag(to + 16 * part + (16u << 16), a[1]);
   }
   const uint2 s4 = lds64(ks + 8 * lane);  // steps that times 16 leave fp16
-  const float2 s0 = __half22float2(bits_h2(s4.x)), s1 = __half22float2(bits_h2(s4.y));
-  if (!(fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)) <= 4094.f)) set_status(d_status, KITTY_ST_RANGE);
+  const uint32_t top = __vmaxu2(s4.x, s4.y);
+  if (max(top & 0xFFFFu, top >> 16) >= 0x6C00u) set_status(d_status, KITTY_ST_RANGE);  // 4096 and more
 }
 
 // What a token's scores carry: its Keys are k * 2^key_exp.
@@ -396,61 +448,57 @@ __device__ __forceinline__ int value_exp(int lane) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// Two pages' Values of channel group G (staged at raw, one `stride` behind the other): their
-// centered codes times steps to 16 + 16 lanes of tensor memory at `to` (16 columns a page), the
-// groups' middles to `mids` (a page's [group][64 bytes], 256 bytes a page).
+// A page's Values of channel group G, staged at raw: their centered codes times steps to 16 + 16
+// lanes of tensor memory at `to` (16 columns), the groups' middles to `mids` ([group][64 bytes]).
 template <int V>
-__device__ __forceinline__ void put_values(uint32_t raw, int stride, uint32_t to, uint32_t mids, int G, int n_hi, int W,
-                                           int there, int32_t* d_status) {
+__device__ __forceinline__ void put_values(uint32_t raw, uint32_t to, uint32_t mids, int G, int n_hi, int W, int32_t* d_status) {
   const int lane = threadIdx.x & 31, r = lane >> 2, qq = lane & 3;
-  uint32_t a[2][16];
+  uint32_t a[2][8];
   uint32_t top = 0;
+  const Codes at16;
+  const uint32_t vb = raw + 512 * W + 4 * W * n_hi + 512 + n_hi, vs = vb + 512 * V, vm = vs + 256;
+  uint32_t w[V];
+  if (V == 2) {
+    const uint2 x = lds64(vb + 32 * lane + 8 * G);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    const uint4 x = lds128(vb + 64 * lane + 16 * G);
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2 % V] = x.z;
+    w[3 % V] = x.w;
+  }
+  const uint4 s4 = lds128(vs + 64 * G + 16 * qq), m4 = lds128(vm + 64 * G + 16 * qq);
+  const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w}, M[4] = {m4.x, m4.y, m4.z, m4.w};
+  constexpr uint32_t mid = V == 2 ? two(0x3E00) : two(0x4780);  // 1.5, 7.5
 #pragma unroll
-  for (int page = 0; page < 2; ++page) {
-    const uint32_t vb = raw + page * stride + 512 * W + 4 * W * n_hi + 512 + n_hi, vs = vb + 512 * V, vm = vs + 256;
-    uint32_t w[V];
+  for (int i = 0; i < 4; ++i) {
+    const int kt = i >> 1, h = i & 1;
+    top = __vmaxu2(top, S[i]);
+    uint32_t* o0 = &a[0][2 * i];
+    uint32_t* o1 = &a[1][2 * i];
     if (V == 2) {
-      const uint2 x = lds64(vb + 32 * lane + 8 * G);
-      w[0] = x.x;
-      w[1] = x.y;
+      const uint32_t x = h ? __funnelshift_r(w[kt], w[kt], 8) : w[kt];
+      // 16 + 1.5 * 2^e, e = -4, -2, 0, 2
+      o0[0] = h2mul(h2add(at16(x, two(0x000C)), two(0xCC06)), S[i]);
+      o0[1] = h2mul(h2add(at16(x, two(0x0030)), two(0xCC18)), S[i]);
+      o1[0] = h2mul(h2add(at16(x, two(0x00C0)), two(0xCC60)), S[i]);
+      o1[1] = h2mul(h2add(at16(x, two(0x0300)), two(0xCD80)), S[i]);
     } else {
-      const uint4 x = lds128(vb + 64 * lane + 16 * G);
-      w[0] = x.x;
-      w[1] = x.y;
-      w[2 % V] = x.z;
-      w[3 % V] = x.w;
-    }
-    const uint4 s4 = lds128(vs + 64 * G + 16 * qq), m4 = lds128(vm + 64 * G + 16 * qq);
-    const uint32_t S[4] = {s4.x, s4.y, s4.z, s4.w}, M[4] = {m4.x, m4.y, m4.z, m4.w};
-    constexpr uint32_t mid = V == 2 ? two(0x3E00) : two(0x4780);  // 1.5, 7.5
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int kt = i >> 1, h = i & 1;
-      if ((there >> page) & 1) top = __vmaxu2(top, S[i]);
-      uint32_t* o0 = &a[0][2 * (4 * page + i)];
-      uint32_t* o1 = &a[1][2 * (4 * page + i)];
-      if (V == 2) {
-        const uint32_t x = h ? __funnelshift_r(w[kt], w[kt], 8) : w[kt];
-        // 16 + 1.5 * 2^e, e = -4, -2, 0, 2
-        o0[0] = h2mul(h2add((x & two(0x000C)) | k16, two(0xCC06)), S[i]);
-        o0[1] = h2mul(h2add((x & two(0x0030)) | k16, two(0xCC18)), S[i]);
-        o1[0] = h2mul(h2add((x & two(0x00C0)) | k16, two(0xCC60)), S[i]);
-        o1[1] = h2mul(h2add((x & two(0x0300)) | k16, two(0xCD80)), S[i]);
-      } else {
-#pragma unroll
-        for (int mc = 0; mc < 2; ++mc) {
-          const uint32_t y = w[(2 * kt + mc) % V], x = h ? __funnelshift_r(y, y, 8) : y;
-          uint32_t* o = mc ? o1 : o0;
-          // 16 + 7.5 * 2^e, e = -4, 0
-          o[0] = h2mul(h2add((x & two(0x003C)) | k16, two(0xCC1E)), S[i]);
-          o[1] = h2mul(h2add((x & two(0x03C0)) | k16, two(0xCDE0)), S[i]);
-        }
+      for (int mc = 0; mc < 2; ++mc) {
+        const uint32_t y = w[(2 * kt + mc) % V], x = h ? __funnelshift_r(y, y, 8) : y;
+        uint32_t* o = mc ? o1 : o0;
+        // 16 + 7.5 * 2^e, e = -4, 0
+        o[0] = h2mul(h2add(at16(x, two(0x003C)), two(0xCC1E)), S[i]);
+        o[1] = h2mul(h2add(at16(x, two(0x03C0)), two(0xCDE0)), S[i]);
       }
     }
-    if (r == 0)
-      sts128(mids + 256 * page + 64 * G + 16 * qq,
-             make_uint4(h2fma(S[0], mid, M[0]), h2fma(S[1], mid, M[1]), h2fma(S[2], mid, M[2]), h2fma(S[3], mid, M[3])));
   }
+  if (r == 0)
+    sts128(mids + 64 * G + 16 * qq,
+           make_uint4(h2fma(S[0], mid, M[0]), h2fma(S[1], mid, M[1]), h2fma(S[2], mid, M[2]), h2fma(S[3], mid, M[3])));
   tmem_st_frag(to, a[0]);
   tmem_st_frag(to + (16u << 16), a[1]);
   if (max(top & 0xFFFFu, top >> 16) > 0x6FFFu) set_status(d_status, KITTY_ST_RANGE);  // 8192 and more
@@ -470,9 +518,12 @@ __device__ __forceinline__ int mag_code(uint32_t m, bool packed, int in_dtype) {
   return KITTY_ST_OK;
 }
 
-struct Bars {
+struct Bars {  // by tile parity
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];  // operands
-  uint64_t sfull[2], sempty[2], bias[2], pfull[2], pempty[2], sums, drain;
+  uint64_t sfull[2], sempty[2];
+  // by tile: q.M may be two of a pipeline's tiles ahead, the sums one behind (16-bit pages: 0 and 1)
+  uint64_t bias[4], bfree[4], pfull[4], pempty[4], mfull[4];
+  uint64_t sums, drain;
   uint64_t raw[kMaxRaw], freed[kMaxRaw], loose[2];  // loose[1]: 16-bit pages, room for their Values
 };
 
@@ -484,21 +535,21 @@ struct alignas(16) Shared {
   uint32_t any[2];             // nodes that some node sees
   int loose;                   // parts of the loose tokens that are there
   uint8_t flags[kFlags];       // pages that are there, by tile
-  float m[N], f[2][N];         // reference of each row; factor of its move, by tile parity
-  int moved[2][2];             // by tile parity and softmax group
-  alignas(16) float bias[2][4][N];   // q.M of each page, by tile parity
-  alignas(16) float shift[kSoftmaxWarps][N / 2];
-  float top[kSoftmaxWarps][N / 2];   // maxima of a warp's tokens
-  float sum[N], mid[4][N];
+  int moved[4];                // by tile: whether its references moved
+  float m[2][N], f[2][N];      // by pipeline: reference of each row; factor of its last move
+  alignas(16) float bias[4][4][N];   // q.M of each page
+  alignas(16) float shift[kSoftmaxWarps][N];
+  float top[kSoftmaxWarps][N];       // maxima of a warp's tokens
+  alignas(8) float sum[2][N], mid[2][4][N];
+  float weight[2][N], total[N];      // of the two pipelines' outputs; a row's sum
   int row[N];                  // output row (token, query head); -1: none
   unsigned long long sees[N];
 };
 
-
 template <class F>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap map) {
   using Z = Sizes<F>;
-  constexpr int N = F::N, C = Z::C;
+  constexpr int N = F::N;
   extern __shared__ uint8_t dyn[];
   __shared__ Shared<N> sh;
   grid_trigger();
@@ -524,24 +575,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   const bool has_loose = t0 + n == tiles;
   volatile int* abort = &sh.abort;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  const uint32_t qs = base, ps = qs + Z::kQ, ops = ps + 2 * Z::kP;  // ops: 16-bit tiles (Keys, then Values)
-  const uint32_t loose = ops, spread = loose + 2 * kLoose * kLoosePitch, mids = spread + 4 * Z::kSpread;
-  const uint32_t raws = mids + F::kOps * 1024;
+  const uint32_t qs = base, ps = qs + Z::kQ, ops = ps + Z::kPs * Z::kP;  // ops: 16-bit tiles (Keys, then Values)
+  const uint32_t loose = ops, spread = loose + 2 * kLoose * kLoosePitch, mids = spread + 8 * Z::kSpread;
+  const uint32_t raws = mids + 4 * 1024;
   Bars& bar = sh.bars;
   auto a_of = [&](uint64_t& x) { return smem_u32(&x); };
+  // place of tile i's p (and q.M, middles), and the parity of its use
+  constexpr int kP2 = Z::kPs == 4 ? 2 : 1;
+  auto at4 = [&](int i) { return i & (Z::kPs - 1); };
+  auto turn4 = [&](int i) { return (i >> kP2) & 1; };
+  auto wait = [&](uint64_t& x, int parity) { return wait_phase(x, parity, p.wait_polls, abort); };
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.kfull[i], F::kPacked ? 4 : 1);
       mbar_init(&bar.vfull[i], F::kPacked ? 4 : 1);
       mbar_init(&bar.kempty[i], 1);
-      mbar_init(&bar.vempty[i], F::kPacked ? 2 : 1);
+      mbar_init(&bar.vempty[i], 1);
       mbar_init(&bar.sfull[i], 1);
-      mbar_init(&bar.sempty[i], kSoftmaxWarps);
-      mbar_init(&bar.bias[i], 1);
-      mbar_init(&bar.pfull[i], kSoftmaxWarps);
-      mbar_init(&bar.pempty[i], 2);
+      mbar_init(&bar.sempty[i], 4);
     }
-    mbar_init(&bar.sums, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar.bias[i], 1);
+      mbar_init(&bar.bfree[i], 4);
+      mbar_init(&bar.pfull[i], 4);
+      mbar_init(&bar.pempty[i], 3);  // the products, and the sums of each half of the rows
+      mbar_init(&bar.mfull[i], 4);
+    }
+    mbar_init(&bar.sums, 4);
     mbar_init(&bar.drain, 1);
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&bar.raw[i], 1);
@@ -574,7 +634,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   }
   if (tid < N) {
     sh.row[tid] = tid < R ? out_row(tid) : -1;
-    sh.m[tid] = kFloor;
+    sh.m[0][tid] = sh.m[1][tid] = kFloor;
   }
   tc_fence_before();
   __syncthreads();
@@ -613,167 +673,189 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 
   if (wid < kSoftmaxWarps) {
     // =========================================================== softmax
-    const int h = wid >> 2, g = wid & 3, id = 1 + h, col = h * C;
+    const int h = wid >> 2, g = wid & 3, id = 1 + h;
     const float sc = p.sm_log2;
     const float sc_page = F::kPacked ? sc * pow2(-key_exp<F>(lane, p.n_hi > 0)) : sc;
     const uint32_t shift_at = smem_u32(sh.shift[wid]);
     const int token = 32 * g + lane;
-    const uint32_t prow = ps + (N > 64 ? h * Z::kPBlock : 0) + token * 128;
+    const uint32_t prow0 = ps + token * 128, S = tmem + Z::kSCol + h * N + quad;
+    const int node = (token - 32) & 63;  // of a loose token that is one (masked: in range for the others, too)
+    constexpr int U = F::kPacked ? 16 : N < 32 ? N : 32;  // rows at a time
+    // what is added to each row's scaled score: q.M of the page, less the reference
+    auto fill = [&](int i, bool with_m) {
+      __syncwarp();
+#pragma unroll
+      for (int c = lane; c < N; c += 32) {
+        const float bias = F::kPacked ? sh.bias[i & 3][g][c] * sc : 0.f;
+        sts32(shift_at + 4 * c, with_m ? bias - sh.m[h][c] : bias);  // read by lds128 alone
+      }
+      __syncwarp();
+    };
     bool ok = true;
-    int i = 0;
-    for (; i < n; ++i) {
-      const int st = i & 1;
-      ok = wait_lanes(lane < (F::kPacked ? 3 : 2), lane == 0 ? a_of(bar.sfull[st]) : lane == 1 ? a_of(bar.pempty[st]) : a_of(bar.bias[st]),
-                      lane == 1 ? ((i >> 1) & 1) ^ 1 : (i >> 1) & 1, p.wait_polls, abort);
+    for (int i = h; i < n; i += 2) {
+      const int u = (i >> 1) & 1;
+      ok = !F::kPacked || wait(bar.bias[i & 3], (i >> 2) & 1);
+      fill(i, true);
+      ok = ok && wait(bar.pempty[at4(i)], turn4(i) ^ 1) && wait(bar.sfull[h], u);
+      const uint32_t prow = prow0 + at4(i) * Z::kP;
       tc_fence_after();
       const bool special = has_loose && i == n - 1;
-      const bool there = (there_of(i) >> g) & 1;
+      const bool there = (there_of(i) >> g) & 1, masks = special && there, in = lane < loose_count(g);
       const float scl = special ? sc : sc_page;
-      const uint32_t S = tmem + F::kSCol + st * N + col + quad;
-      uint32_t x[C];
-      tmem_load<C>(S, x);
-      // y = x * scl + shift of the row, masked
-      const bool in = lane < loose_count(g);
-      const int node = (token - 32) & 63;  // of a loose token that is one (masked: in range for the others, too)
-      auto scores = [&](bool with_m) {
-        for (int c = lane; c < C; c += 32) {
-          const float bias = F::kPacked ? sh.bias[st][g][col + c] * sc : 0.f;
-          sts32(shift_at + 4 * c, with_m ? bias - sh.m[col + c] : bias);  // read by lds128 alone
-        }
-        __syncwarp();
+      // U rows' scores from tensor memory: scaled, shifted, masked
+      auto scores = [&](int c0, uint32_t (&x)[U]) {
+        tmem_load<U>(S + c0, x);
         const uint64_t scl2 = f2pack(scl, scl);
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const uint4 s4 = lds128(shift_at + 4 * c);
-          uint64_t e;
-          asm("mov.b64 %0, {%1, %2};" : "=l"(e) : "r"(x[c]), "r"(x[c + 1]));
-          uint64_t s2;
-          asm("mov.b64 %0, {%1, %2};" : "=l"(s2) : "r"(s4.x), "r"(s4.y));
-          asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(e), "l"(scl2), "l"(s2));
-          asm("mov.b64 {%0, %1}, %2;" : "=r"(x[c]), "=r"(x[c + 1]) : "l"(e));
-          asm("mov.b64 %0, {%1, %2};" : "=l"(e) : "r"(x[c + 2]), "r"(x[c + 3]));
-          asm("mov.b64 %0, {%1, %2};" : "=l"(s2) : "r"(s4.z), "r"(s4.w));
-          asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(e), "l"(scl2), "l"(s2));
-          asm("mov.b64 {%0, %1}, %2;" : "=r"(x[c + 2]), "=r"(x[c + 3]) : "l"(e));
+        for (int c = 0; c < U; c += 4) {
+          const uint4 s4 = lds128(shift_at + 4 * (c0 + c));
+          fma2(x[c], x[c + 1], scl2, s4.x, s4.y);
+          fma2(x[c + 2], x[c + 3], scl2, s4.z, s4.w);
         }
-        if (!there) {
+        if (masks) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) x[c] = __float_as_uint(-INFINITY);
-        } else if (special) {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const bool on = g == 0 || ((sh.sees[col + c] >> node) & 1ull) != 0;
-            if (!in || !on) x[c] = __float_as_uint(-INFINITY);
-          }
+          for (int c = 0; c < U; ++c)
+            if (!in || (g > 0 && ((sh.sees[c0 + c] >> node) & 1ull) == 0)) x[c] = __float_as_uint(-INFINITY);
         }
-        __syncwarp();
       };
-      scores(true);
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < C; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
-      bool slow = group_any(id, i == 0 || top > kSlack || !ok);
-      if (slow) {
-        if (group_any(id, !ok)) {
-          ok = false;
-          break;
-        }
-        tmem_load<C>(S, x);
-        scores(false);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const float mx = warp_max(__uint_as_float(x[c]));
-          if (lane == 0) sh.top[wid][c] = mx;
-        }
-        group_sync(id);
-        bool moves = false;
-        const int c = tid & 127;  // a thread a row
-        if (c < C) {
-          const float mx = fmaxf(fmaxf(sh.top[4 * h][c], sh.top[4 * h + 1][c]), fmaxf(sh.top[4 * h + 2][c], sh.top[4 * h + 3][c]));
-          const float m = sh.m[col + c];
-          const bool set = (i == 0 && mx > kFloor) || mx > m + kSlack;
-          const float nm = set ? mx + kMargin : m;
-          sh.m[col + c] = nm;
-          sh.f[st][col + c] = i > 0 && set ? ex2a(m - nm) : 1.f;
-          moves = i > 0 && set;
-        }
-        moves = group_any(id, moves);
-        if (moves) {  // the outputs so far, once the products so far are done
-          ok = wait_lanes(lane == 0, a_of(bar.pempty[1 - st]), ((i - 1) >> 1) & 1, p.wait_polls, abort);
-          tc_fence_after();
-          const uint32_t O = tmem + Z::kOCol + col + quad;
+      bool moves = false, leave = false;
+      for (int pass = 0;; ++pass) {
+        // p of the tile by the references as they are (a token that is not there is not multiplied)
+        float top = -INFINITY;
+        if (there) {
 #pragma unroll 1
-          for (int c = 0; c < C; c += 8) {
-            uint32_t y[8];
-            tmem_load<8>(O + c, y);
+          for (int c0 = 0; c0 < N; c0 += U) {
+            uint32_t x[U];
+            scores(c0, x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * sh.f[st][col + c + k]);
-            tmem_st8(O + c, y);
-          }
-          tmem_wait_st();
-          if (group_any(id, !ok)) {
-            ok = false;
-            break;
-          }
-        }
-        if (lane == 0 && g == 0) sh.moved[st][h] = moves;
-        tmem_load<C>(S, x);
-        scores(true);
-      } else if (lane == 0 && g == 0) {
-        sh.moved[st][h] = 0;
-      }
-      // the scores and their bias have been read
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_s(a_of(bar.sempty[st]));
+            for (int c = 0; c < U; c += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
 #pragma unroll
-      for (int c = 0; c < C; c += 8) {
-        uint32_t w[4], rest[4];
+            for (int c = 0; c < U; c += 8) {
+              uint32_t w[4], rest[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float e0 = ex2a(__uint_as_float(x[c + 2 * k])), e1 = ex2a(__uint_as_float(x[c + 2 * k + 1]));
-          if (F::kBf16) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(e0, e1);
-            w[k] = *reinterpret_cast<const uint32_t*>(&y);
-            const __nv_bfloat162 z = __floats2bfloat162_rn(e0 - __uint_as_float(w[k] << 16), e1 - __uint_as_float(w[k] & 0xFFFF0000u));
-            rest[k] = *reinterpret_cast<const uint32_t*>(&z);
-          } else {
-            const __half2 y = __floats2half2_rn(e0, e1);
-            w[k] = h2_bits(y);
-            if (F::kPair) {
-              const float2 z = __half22float2(y);
-              rest[k] = h2_bits(__floats2half2_rn(e0 - z.x, e1 - z.y));
+              for (int k = 0; k < 4; ++k) {
+                const float e0 = ex2a(__uint_as_float(x[c + 2 * k])), e1 = ex2a(__uint_as_float(x[c + 2 * k + 1]));
+                if (F::kBf16) {
+                  const __nv_bfloat162 y = __floats2bfloat162_rn(e0, e1);
+                  w[k] = *reinterpret_cast<const uint32_t*>(&y);
+                  const __nv_bfloat162 z = __floats2bfloat162_rn(e0 - __uint_as_float(w[k] << 16), e1 - __uint_as_float(w[k] & 0xFFFF0000u));
+                  rest[k] = *reinterpret_cast<const uint32_t*>(&z);
+                } else {
+                  const __half2 y = __floats2half2_rn(e0, e1);
+                  w[k] = h2_bits(y);
+                  if (F::kPair) {
+                    const float2 z = __half22float2(y);
+                    rest[k] = h2_bits(__floats2half2_rn(e0 - z.x, e1 - z.y));
+                  }
+                }
+              }
+              const uint32_t at = prow + ((((c0 + c) / 8) ^ (token & 7)) << 4);
+              sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+              if (F::kPair) sts128(at + Z::kPHalf, make_uint4(rest[0], rest[1], rest[2], rest[3]));
             }
           }
         }
-        const int chunk = ((N > 64 ? 0 : col) + c) / 8;
-        const uint32_t at = prow + st * Z::kP + ((chunk ^ (token & 7)) << 4);
-        sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
-        if (F::kPair) sts128(at + Z::kPHalf, make_uint4(rest[0], rest[1], rest[2], rest[3]));
+        // a score that passes its reference by too much (always to be set at the first tile): the
+        // group moves the references, and the tile's p are formed again
+        if (pass == 1 || !group_any(id, i == h || top > kSlack || !ok)) break;
+        // (a move is of what the tiles before have left: their products and sums are done, then)
+        if (i > h) ok = ok && wait(bar.pempty[at4(i - 2)], turn4(i - 2));
+        leave = group_any(id, !ok);
+        if (leave) break;
+        fill(i, false);
+#pragma unroll 1
+        for (int c0 = 0; c0 < N; c0 += U) {
+          uint32_t x[U];
+          scores(c0, x);
+#pragma unroll
+          for (int c = 0; c < U; ++c) {
+            const float mx = warp_max(there ? __uint_as_float(x[c]) : -INFINITY);
+            if (lane == 0) sh.top[wid][c0 + c] = mx;
+          }
+        }
+        group_sync(id);
+        const int c = tid & 127;  // a thread a row
+        if (c < N) {
+          const float mx = fmaxf(fmaxf(sh.top[4 * h][c], sh.top[4 * h + 1][c]), fmaxf(sh.top[4 * h + 2][c], sh.top[4 * h + 3][c]));
+          const float m = sh.m[h][c];
+          const bool set = (i == h && mx > kFloor) || mx > m + kSlack;
+          const float nm = set ? mx + kMargin : m;
+          sh.m[h][c] = nm;
+          sh.f[h][c] = i > h && set ? ex2a(m - nm) : 1.f;
+          moves = i > h && set;
+        }
+        moves = group_any(id, moves);
+        if (moves) {  // the outputs so far
+          tc_fence_after();
+          const uint32_t O = tmem + Z::kOCol + h * N + quad;
+#pragma unroll 1
+          for (int k0 = 0; k0 < N; k0 += 8) {
+            uint32_t y[8];
+            tmem_load<8>(O + k0, y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * sh.f[h][k0 + k]);
+            tmem_st8(O + k0, y);
+          }
+          tmem_wait_st();
+        }
+        fill(i, true);
       }
+      if (leave) {
+        ok = false;
+        break;
+      }
+      if (lane == 0 && g == 0) sh.moved[at4(i)] = moves;
+      // the scores and their bias have been read, p is written
+      tc_fence_before();
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_s(a_of(bar.pfull[st]));
+      if (lane == 0) {
+        mbar_arrive_s(a_of(bar.sempty[h]));
+        if (F::kPacked) mbar_arrive_s(a_of(bar.bfree[i & 3]));
+        mbar_arrive_s(a_of(bar.pfull[at4(i)]));
+      }
     }
-    // ---- outputs or partials: a thread a channel, a warp 32 channels of each row of its group
-    if (ok)
-      ok = wait_lanes(lane < 2, lane == 0 ? a_of(bar.pempty[(n - 1) & 1]) : a_of(bar.sums), lane == 0 ? ((n - 1) >> 1) & 1 : 0, p.wait_polls, abort);
-    if (ok) {
+    // ---- the last products and sums; then the weights of the two pipelines' outputs
+    const int last = n - 1 - ((n - 1 - h) & 1);  // this one's last tile, if it has one
+    if (ok) ok = (last < 0 || wait(bar.pempty[at4(last)], turn4(last))) && wait(bar.sums, 0);
+    tc_fence_after();
+    if (ok && wid < 2 && tid < N) {
+      const float l0 = sh.sum[0][tid], l1 = n > 1 ? sh.sum[1][tid] : 0.f;
+      const float m0 = l0 != 0.f ? sh.m[0][tid] : -INFINITY, m1 = l1 != 0.f ? sh.m[1][tid] : -INFINITY, m = fmaxf(m0, m1);
+      const float w0 = l0 != 0.f ? ex2a(m0 - m) : 0.f, w1 = l1 != 0.f ? ex2a(m1 - m) : 0.f;
+      sh.weight[0][tid] = w0;
+      sh.weight[1][tid] = w1;
+      sh.total[tid] = (l0 != 0.f ? l0 * w0 : 0.f) + (l1 != 0.f ? l1 * w1 : 0.f);
+      sh.m[0][tid] = m;
+    }
+    // all eight warps come here: both pipelines have ended, or none goes on
+    uint32_t failed;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, 5, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(failed)
+        : "r"((uint32_t)!ok)
+        : "memory");
+    if (failed == 0) {
+      // ---- outputs or partials: a thread a channel, a warp 32 channels of each row of its half
       tc_fence_after();
       const float scale = F::kPacked ? pow2(-value_exp<F>(lane)) : 1.f;
       const int ch = 32 * g + lane;
       bool empty = false;
-#pragma unroll
-      for (int c = 0; c < C; c += 8) {
-        if (col + c >= R) break;
-        uint32_t x[8];
-        tmem_load<8>(tmem + Z::kOCol + col + c + quad, x);
+#pragma unroll 1
+      for (int c = h * (N / 2); c < (h + 1) * (N / 2) && c < R; c += 8) {
+        uint32_t x[8], x1[8];
+        tmem_load<8>(tmem + Z::kOCol + c + quad, x);
+        tmem_load<8>(tmem + Z::kOCol + N + c + quad, x1);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int y = col + c + k, row = sh.row[y];
+          const int y = c + k, row = sh.row[y];
           if (row < 0) continue;
-          const float l = sh.sum[y];
-          const float o = l != 0.f ? __uint_as_float(x[k]) * scale + (F::kPacked ? sh.mid[g][y] : 0.f) : 0.f;
+          // (a weight of 0: that pipeline's outputs may be anything)
+          const float l = sh.total[y], w0 = sh.weight[0][y], w1 = sh.weight[1][y];
+          float o = 0.f;
+          if (w0 != 0.f) o = (__uint_as_float(x[k]) * scale + (F::kPacked ? sh.mid[0][g][y] : 0.f)) * w0;
+          if (w1 != 0.f) o += (__uint_as_float(x1[k]) * scale + (F::kPacked ? sh.mid[1][g][y] : 0.f)) * w1;
           if (p.splits == 1) {
             const float v = l != 0.f ? o / l : 0.f;
             const size_t at = (size_t)row * kD + ch;
@@ -784,7 +866,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           } else {
             float* part = p.ws + ((size_t)row * p.splits + split) * kPartialFloats;
             part[4 + ch] = o;
-            if (ch == 0) *reinterpret_cast<float2*>(part) = make_float2(l != 0.f ? sh.m[y] : -INFINITY, l);
+            if (ch == 0) *reinterpret_cast<float2*>(part) = make_float2(l != 0.f ? sh.m[0][y] : -INFINITY, l);
           }
         }
       }
@@ -793,37 +875,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     } else if (lane == 0) {
       set_status(p.d_status, KITTY_ST_TIMEOUT);
     }
-  } else if (wid < kMmaWarp) {
+  } else if (wid < kBiasWarp) {
     // =========================================================== operands
     const bool keys = wid < kValueWarp;
     const int g = wid & 3;
     bool ok = true;
     if constexpr (F::kPacked) {
-      int slot = 0, turn = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % F::kOps, use = i / F::kOps;
+      const int h = (wid >> 2) & 1;
+      int slot = h, turn = 0;
+      for (int i = h; i < n; i += 2) {
+        const int u = (i >> 1) & 1;
         const bool special = has_loose && i == n - 1;
-        const uint32_t empty = keys ? a_of(bar.kempty[st]) : a_of(bar.vempty[st]);
-        ok = wait_lanes(lane < 2, lane == 0 ? empty : special ? a_of(bar.loose[0]) : a_of(bar.raw[slot]),
-                        lane == 0 ? (use & 1) ^ 1 : special ? 0 : turn & 1, p.wait_polls, abort);
+        ok = wait(special ? bar.loose[0] : bar.raw[slot], special ? 0 : turn & 1) && wait(keys ? bar.kempty[h] : bar.vempty[h], u ^ 1);
+        if (!keys) ok = ok && wait(bar.pempty[at4(i)], turn4(i) ^ 1);  // the middles' place
         if (!ok) break;
         tc_fence_after();
-        const uint32_t to = tmem + (keys ? 0 : F::kVCol) + 64 * st + quad;
+        const uint32_t to = tmem + (keys ? 0 : 128) + 64 * h + quad;
         if (!special) {
           const uint32_t raw = raws + slot * (kTilePages * p.blob);
           const int there = sh.flags[i % kFlags];
           if (keys) {
-            if ((there >> g) & 1) put_keys<F::W>(raw + g * p.blob, to, spread + g * Z::kSpread, p.n_hi, p.d_status);
+            if ((there >> g) & 1) put_keys<F::W>(raw + g * p.blob, to, spread + (wid - kKeyWarp) * Z::kSpread, p.n_hi, p.d_status);
           } else {
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x)
-              if ((there >> (2 * x)) & 3)
-                put_values<F::V>(raw + 2 * x * p.blob, p.blob, to + 32 * x, mids + st * 1024 + 512 * x, g, p.n_hi, F::W, there >> (2 * x), p.d_status);
+            for (int x = 0; x < kTilePages; ++x)
+              if ((there >> x) & 1) put_values<F::V>(raw + x * p.blob, to + 16 * x, mids + at4(i) * 1024 + 256 * x, g, p.n_hi, F::W, p.d_status);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_s(a_of(bar.freed[slot]));
-          if (++slot == p.raw_stages) {
-            slot = 0;
+          slot += 2;
+          if (slot >= p.raw_stages) {
+            slot -= p.raw_stages;
             ++turn;
           }
         } else if (keys) {
@@ -831,7 +913,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           uint32_t mag = 0;
           const uint32_t src = loose + (32 * g + lane) * kLoosePitch;
           if (loose_count(g) > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 4; ++x) {
               uint32_t w[16];
 #pragma unroll
@@ -875,19 +957,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
               w[k] = h2_bits(__floats2half2_rn(f[0] * up, f[1] * up));
             }
             tmem_st16(to + 16 * x, w);
-            if (lane < 4) sts128(mids + st * 1024 + 256 * x + 64 * g + 16 * lane, make_uint4(0, 0, 0, 0));
+            if (lane < 4) sts128(mids + at4(i) * 1024 + 256 * x + 64 * g + 16 * lane, make_uint4(0, 0, 0, 0));
           }
           if (code != KITTY_ST_OK) set_status(p.d_status, code);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_s(keys ? a_of(bar.kfull[st]) : a_of(bar.vfull[st]));
+        if (lane == 0) {
+          mbar_arrive_s(keys ? a_of(bar.kfull[h]) : a_of(bar.vfull[h]));
+          if (!keys) mbar_arrive_s(a_of(bar.mfull[at4(i)]));
+        }
       }
     } else if (has_loose) {
       // the loose tokens' rows, swizzled as the tiled loads leave the others: 8 lanes a row half
       const int i = n - 1, st = i & 1;
-      ok = wait_lanes(lane == 0, a_of(bar.loose[keys ? 0 : 1]), 0, p.wait_polls, abort);
+      ok = wait(bar.loose[keys ? 0 : 1], 0);
       const uint32_t to = ops + (2 * st + (keys ? 0 : 1)) * Z::kTile16;
       if (ok) {
         int code = KITTY_ST_OK;
@@ -897,18 +982,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         const uint16_t* nodes = (keys ? p.k : p.v) + (size_t)hd.first * (keys ? p.k_stride : p.v_stride) + (size_t)kvh * kD;
         const size_t stride = keys ? p.k_stride : p.v_stride;
 #pragma unroll 1
-        for (int k0 = 0; k0 < kLoose * 16; k0 += 4 * 128) {
-          uint4 v[4];
+        for (int k0 = 0; k0 < kLoose * 16; k0 += 3 * 256) {
+          uint4 v[3];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = k0 + 128 * k + 32 * g + lane, t = at >> 4, c = at & 15, part = t >> 5;
+          for (int k = 0; k < 3; ++k) {
+            const int at = k0 + 256 * k + (tid & 255), t = at >> 4, c = at & 15, part = t >> 5;
             const bool on = t < kLoose && (part == 0 ? (t & 31) < hd.loose && in : loose_seen(part, t & 31));
             v[k] = on ? *reinterpret_cast<const uint4*>((part == 0 ? page + (size_t)t * kD : nodes + (size_t)(t - 32) * stride) + 8 * c)
                       : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = k0 + 128 * k + 32 * g + lane, t = at >> 4, c = at & 15;
+          for (int k = 0; k < 3; ++k) {
+            const int at = k0 + 256 * k + (tid & 255), t = at >> 4, c = at & 15;
             if (t >= 32) {  // not a number: reported, and kept from those that do not see it
               const int e = mag_code(mag2(mag2(mag2(mag2(0, v[k].x), v[k].y), v[k].z), v[k].w), false, p.in_dtype);
               if (e != KITTY_ST_OK) {
@@ -922,8 +1007,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         if (code != KITTY_ST_OK) set_status(p.d_status, code);
       }
       fence_async_shared();
-      group_sync(keys ? 3 : 4);
-      if (ok && g == 0 && lane == 0) mbar_arrive_s(keys ? a_of(bar.kfull[st]) : a_of(bar.vfull[st]));
+      asm volatile("barrier.cta.sync %0, 256;" ::"r"(keys ? 3 : 4) : "memory");
+      if (ok && (tid & 255) == 0) mbar_arrive_s(keys ? a_of(bar.kfull[st]) : a_of(bar.vfull[st]));
     }
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
@@ -932,79 +1017,84 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     constexpr uint32_t qk = mma_desc(F::kBf16, false, N);
     constexpr uint32_t pv = mma_desc(F::kBf16, true, N) | (F::kPacked ? 0u : 1u << 15);  // 16-bit Values: channels contiguous
     const uint64_t qdesc = smem_desc(qs, 16, 1024, kSwizzle128);
-    const uint64_t pdesc = smem_desc(ps, Z::kPBlock, 1024, kSwizzle128);
-    bool ok = true, started = false;
+    const uint64_t pdesc = smem_desc(ps, Z::kPHalf, 1024, kSwizzle128);
+    bool ok = true;
+    int started = 0;  // pipelines whose outputs have been begun
     auto scores = [&](int i) {
-      const int st = i & 1, op = i % F::kOps;
-      ok = wait_lanes(lane < 2, lane == 0 ? a_of(bar.kfull[op]) : a_of(bar.sempty[st]),
-                      lane == 0 ? (i / F::kOps) & 1 : ((i >> 1) & 1) ^ 1, p.wait_polls, abort);
+      const int st = i & 1;
+      ok = wait(bar.kfull[st], (i >> 1) & 1) && wait(bar.sempty[st], ((i >> 1) & 1) ^ 1);
       if (!ok) return;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t d = tmem + F::kSCol + st * N;
+        const uint32_t d = tmem + Z::kSCol + st * N;
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k) {
           const uint64_t qd = qdesc + (k >> 2) * (Z::kQHalf / 16) + 2 * (k & 3);
           if constexpr (F::kPacked) {
-            mma_ts(d, tmem + 64 * op + 8 * k, qd, qk, k > 0);
+            mma_ts(d, tmem + 64 * st + 8 * k, qd, qk, k > 0);
           } else {
-            const uint64_t kd = smem_desc(ops + 2 * op * Z::kTile16, 16, 1024, kSwizzle128);
+            const uint64_t kd = smem_desc(ops + 2 * st * Z::kTile16, 16, 1024, kSwizzle128);
             mma_ss(d, kd + (k >> 2) * (Z::kHalf16 / 16) + 2 * (k & 3), qd, qk, k > 0);
           }
         }
         mma_commit(a_of(bar.sfull[st]));
-        mma_commit(a_of(bar.kempty[op]));
+        mma_commit(a_of(bar.kempty[st]));
       }
       __syncwarp();
     };
     scores(0);
     for (int i = 0; ok && i < n; ++i) {
-      const int st = i & 1, op = i % F::kOps;
+      const int st = i & 1;
       if (i + 1 < n) {
         scores(i + 1);
         if (!ok) break;
       }
-      ok = wait_lanes(lane < 2, lane == 0 ? a_of(bar.pfull[st]) : a_of(bar.vfull[op]), lane == 0 ? (i >> 1) & 1 : (i / F::kOps) & 1,
-                      p.wait_polls, abort);
+      ok = wait(bar.vfull[st], (i >> 1) & 1) && wait(bar.pfull[at4(i)], turn4(i));
       if (!ok) break;
       tc_fence_after();
       const int there = there_of(i);
       if (elect_one()) {
-        const uint32_t d = tmem + Z::kOCol;
-        const uint64_t pd = pdesc + st * (Z::kP / 16);
-        bool acc = started;
-#pragma unroll 1
-        for (int g = 0; g < kTilePages; ++g) {
-          if (!((there >> g) & 1)) continue;
-#pragma unroll
-          for (int k = 2 * g; k < 2 * g + 2; ++k) {
-            if constexpr (F::kPacked) {
-              mma_ts(d, tmem + F::kVCol + 64 * op + 8 * k, pd + 128 * k, pv, acc);
-            } else {
-              const uint64_t vd = smem_desc(ops + (2 * op + 1) * Z::kTile16, Z::kHalf16, 1024, kSwizzle128) + 128 * k;
-              mma_ss(d, vd, pd + 128 * k, pv, acc);
-              mma_ss(d, vd, pd + Z::kPHalf / 16 + 128 * k, pv, true);
-            }
-            acc = true;
+        const uint32_t d = tmem + Z::kOCol + st * N, v = tmem + 128 + 64 * st;
+        const uint64_t pd = pdesc + at4(i) * (Z::kP / 16);
+        const uint64_t vd = smem_desc(ops + (2 * st + 1) * Z::kTile16, Z::kHalf16, 1024, kSwizzle128);
+        auto product = [&](int k, bool acc) {  // 16 tokens
+          if constexpr (F::kPacked) {
+            mma_ts(d, v + 8 * k, pd + 128 * k, pv, acc);
+          } else {
+            mma_ss(d, vd + 128 * k, pd + 128 * k, pv, acc);
+            mma_ss(d, vd + 128 * k, pd + Z::kPHalf / 16 + 128 * k, pv, true);
           }
+        };
+        const bool begun = (started >> st) & 1;
+        if (there == 15) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) product(k, begun || k > 0);
+        } else {
+          bool acc = begun;
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k)
+            if ((there >> (k >> 1)) & 1) {
+              product(k, acc);
+              acc = true;
+            }
         }
-        mma_commit(a_of(bar.vempty[op]));
-        mma_commit(a_of(bar.pempty[st]));
+        mma_commit(a_of(bar.vempty[st]));
+        mma_commit(a_of(bar.pempty[at4(i)]));
       }
-      started = started || there != 0;
+      if (there != 0) started |= 1 << st;
       __syncwarp();
     }
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
   } else if (!F::kPacked && (wid == kFetchWarp || wid == kBiasWarp)) {
     // =========================================================== tiled loads: a warp the Keys', one the Values'
-    const bool values = wid == kBiasWarp;
+    const bool values = wid != kFetchWarp;
     bool ok = true;
     int ids = -1;  // lane l: the id of page l of the eight tiles at hand
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t full = values ? a_of(bar.vfull[st]) : a_of(bar.kfull[st]);
-      ok = wait_lanes(true, values ? a_of(bar.vempty[st]) : a_of(bar.kempty[st]), ((i >> 1) & 1) ^ 1, p.wait_polls, abort);
+      ok = wait(values ? bar.vempty[st] : bar.kempty[st], ((i >> 1) & 1) ^ 1);
       if (!ok) break;
       if (has_loose && i == n - 1) {  // room for the loose tokens: this warp has followed every use of the stage
         if (elect_one()) mbar_arrive_s(a_of(bar.loose[values ? 1 : 0]));
@@ -1072,7 +1162,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const int there = __ballot_sync(0xFFFFFFFFu, in) & 15;
       if (lane < 4 && !in && (t0 + i) * kTilePages + lane < pages) set_status(p.d_status, KITTY_ST_BAD_PAGE);
       if constexpr (F::kPacked) {
-        ok = wait_lanes(lane == 0, a_of(bar.freed[slot]), (turn & 1) ^ 1, p.wait_polls, abort);
+        ok = wait(bar.freed[slot], (turn & 1) ^ 1);
         if (!ok) break;
         const uint32_t full = a_of(bar.raw[slot]);
         if (lane == 0) {
@@ -1092,116 +1182,128 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     }
     if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     __syncwarp();
-  } else if (wid == kBiasWarp) {
-    // =========================================================== q.M
+  } else if (wid < kSumWarp) {
+    // =========================================================== q.M: a page a row of the product
     if constexpr (F::kPacked) {
-      const int r = lane >> 2, qq = lane & 3;
+      constexpr int T = N / 8;  // tiles of eight rows
+      const int h = wid - kBiasWarp, r = lane >> 2, qq = lane & 3;
+      // eight rows' 32 channels of the queries: a matrix of eight channels a quarter warp
+      const uint32_t q_at[2] = {qs + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4),
+                                qs + (lane & 7) * 128 + (((4 + (lane >> 3)) ^ (lane & 7)) << 4)};
       bool ok = true;
-      int slot = 0, turn = 0;
-      const uint32_t km = 512 * F::W + 4 * F::W * p.n_hi + 256;
-      for (int i = 0; i < n; ++i) {
-        const int st = i & 1;
+      int slot = h, turn = 0;
+      for (int i = h; i < n; i += 2) {
         const bool special = has_loose && i == n - 1;
-        ok = wait_lanes(lane < (special ? 1 : 2), lane == 0 ? a_of(bar.sempty[st]) : a_of(bar.raw[slot]),
-                        lane == 0 ? ((i >> 1) & 1) ^ 1 : turn & 1, p.wait_polls, abort);
+        ok = (special || wait(bar.raw[slot], turn & 1)) && wait(bar.bfree[i & 3], ((i >> 2) & 1) ^ 1);
         if (!ok) break;
         if (special) {
-          for (int x = lane; x < 4 * N; x += 32) (&sh.bias[st][0][0])[x] = 0.f;
+          for (int x = lane; x < 4 * N; x += 32) (&sh.bias[i & 3][0][0])[x] = 0.f;
         } else {
           uint32_t M[16];
-          const uint32_t at = raws + (slot * kTilePages + (r & 3)) * p.blob + km + 64 * qq;
+          const uint32_t at = raws + (slot * kTilePages + (r & 3)) * p.blob + 512 * F::W + 4 * F::W * p.n_hi + 256 + 64 * qq;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 v = lds128(at + 16 * k);
-            M[4 * k] = r < 4 ? v.x : 0;
-            M[4 * k + 1] = r < 4 ? v.y : 0;
-            M[4 * k + 2] = r < 4 ? v.z : 0;
-            M[4 * k + 3] = r < 4 ? v.w : 0;
+            const uint4 v = r < 4 ? lds128(at + 16 * k) : make_uint4(0, 0, 0, 0);
+            M[4 * k] = v.x;
+            M[4 * k + 1] = v.y;
+            M[4 * k + 2] = v.z;
+            M[4 * k + 3] = v.w;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive_s(a_of(bar.freed[slot]));
-#pragma unroll 2
-          for (int nt = 0; nt < N / 8; ++nt) {
-            float c[4] = {}, d[4] = {};
-            const int row = 8 * nt + (lane & 7);
+          slot += 2;
+          if (slot >= p.raw_stages) {
+            slot -= p.raw_stages;
+            ++turn;
+          }
+#pragma unroll 1
+          for (int nt = 0; nt < T; ++nt) {
+            float x[4], y[4];
 #pragma unroll
             for (int jp = 0; jp < 4; ++jp) {
               uint32_t q4[4];
-              ldsm_x4(qs + (jp >> 1) * Z::kQHalf + row * 128 + (((4 * (jp & 1) + (lane >> 3)) ^ (row & 7)) << 4), q4);
+              ldsm_x4(q_at[jp & 1] + (jp >> 1) * Z::kQHalf + nt * 1024, q4);
               const uint32_t a0[4] = {M[4 * jp], 0u, M[4 * jp + 1], 0u}, a1[4] = {M[4 * jp + 2], 0u, M[4 * jp + 3], 0u};
-              mma_f16(c, a0, q4[0], q4[1]);
-              mma_f16(d, a1, q4[2], q4[3]);
+              if (jp == 0) {
+                mma_rows8(x, M[0], M[1], q4[0], q4[1]);
+                mma_rows8(y, M[2], M[3], q4[2], q4[3]);
+                continue;
+              }
+              mma_f16(x, a0, q4[0], q4[1]);
+              mma_f16(y, a1, q4[2], q4[3]);
             }
-            if (r < 4) *reinterpret_cast<float2*>(&sh.bias[st][r][8 * nt + 2 * qq]) = make_float2(c[0] + d[0], c[1] + d[1]);
-          }
-          if (++slot == p.raw_stages) {
-            slot = 0;
-            ++turn;
+            if (r < 4) *reinterpret_cast<float2*>(&sh.bias[i & 3][r][8 * nt + 2 * qq]) = make_float2(x[0] + y[0], x[1] + y[1]);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_s(a_of(bar.bias[st]));
+        if (lane == 0) mbar_arrive_s(a_of(bar.bias[i & 3]));
       }
       if (!ok && lane == 0) set_status(p.d_status, KITTY_ST_TIMEOUT);
     }
     __syncwarp();
   } else {
-    // =========================================================== sums of p, of p * middles
-    const int r = lane >> 2, qq = lane & 3;
-    float c[N / 8][4];
-#pragma unroll
-    for (int nt = 0; nt < N / 8; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-    constexpr uint32_t one = F::kBf16 ? two(0x3F80) : two(0x3C00);
+    // =========================================================== sums of p and of p * middles
+    constexpr int T = N < 32 ? 2 : N / 16;  // tiles of eight rows of a warp
+    const int h = (wid - kSumWarp) & 1, n0 = (wid - kSumWarp) / 2 * T, r = lane >> 2, qq = lane & 3;
+    const bool mine = n0 * 8 < N;  // (16 rows are one warp's)
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int st = i & 1, op = i % F::kOps;
-      ok = wait_lanes(lane < (F::kPacked ? 2 : 1), lane == 0 ? a_of(bar.pfull[st]) : a_of(bar.vfull[op]),
-                      lane == 0 ? (i >> 1) & 1 : (i / F::kOps) & 1, p.wait_polls, abort);
+    float c[T][4];  // (rows 8 .. 15 of the product are zeros)
+#pragma unroll
+    for (int nt = 0; nt < T; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+    constexpr uint32_t one = F::kBf16 ? two(0x3F80) : two(0x3C00);
+    // 16 tokens' p of 16 rows (two chunks of a token's 64): matrices of eight by eight
+    uint32_t p_at[T / 2];
+#pragma unroll
+    for (int np = 0; np < T / 2; ++np)
+      p_at[np] = ps + (8 * ((lane >> 3) & 1) + (lane & 7)) * 128 + (((n0 + 2 * np + (lane >> 4)) ^ (lane & 7)) << 4);
+    // page g of the stage at `at`
+    auto page_sums = [&](uint32_t at, uint4 a4) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const uint32_t a[4] = {kt ? a4.z : a4.x, 0u, kt ? a4.w : a4.y, 0u};
+#pragma unroll
+        for (int pr = 0; pr < (F::kPair ? 2 : 1); ++pr) {
+#pragma unroll
+          for (int np = 0; np < T / 2; ++np) {
+            uint32_t b4[4];
+            ldsm_x4_t(p_at[np] + at + pr * Z::kPHalf + kt * 2048, b4);
+            mma16<F::kBf16 ? KITTY_BF16 : KITTY_F16>(c[2 * np], a, b4[0], b4[1]);
+            mma16<F::kBf16 ? KITTY_BF16 : KITTY_F16>(c[2 * np + 1], a, b4[2], b4[3]);
+          }
+        }
+      }
+    };
+    for (int i = h; i < n; i += 2) {
+      ok = (!F::kPacked || wait(bar.mfull[at4(i)], turn4(i))) && wait(bar.pfull[at4(i)], turn4(i));
+      const uint32_t pi = at4(i) * Z::kP;
       if (!ok) break;
       const int there = there_of(i);
+      if (i > h && sh.moved[at4(i)] != 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (i > 0 && sh.moved[st][h]) {
-#pragma unroll
-          for (int nt = h * (N / 16); nt < (h + 1) * (N / 16); ++nt) {
-            c[nt][0] *= sh.f[st][8 * nt + 2 * qq];
-            c[nt][1] *= sh.f[st][8 * nt + 2 * qq + 1];
-          }
+        for (int nt = 0; nt < T; ++nt) {
+          c[nt][0] *= sh.f[h][8 * ((n0 + nt) % (N / 8)) + 2 * qq];
+          c[nt][1] *= sh.f[h][8 * ((n0 + nt) % (N / 8)) + 2 * qq + 1];
         }
-#pragma unroll 1
-      for (int g = 0; g < kTilePages; ++g) {
-        if (!((there >> g) & 1)) continue;
+      }
+      auto middles = [&](int g) {  // and, in row 4, ones
         uint4 a4 = make_uint4(0, 0, 0, 0);
-        if (F::kPacked && r < 4) a4 = lds128(mids + op * 1024 + 256 * g + 64 * r + 16 * qq);
+        if (F::kPacked && r < 4) a4 = lds128(mids + at4(i) * 1024 + 256 * g + 64 * r + 16 * qq);
         if (r == 4) a4 = make_uint4(one, one, one, one);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-          const uint32_t a[4] = {kt ? a4.z : a4.x, 0u, kt ? a4.w : a4.y, 0u};
-          const int token = 32 * g + 16 * kt + 8 * ((lane >> 3) & 1) + (lane & 7);
-#pragma unroll
-          for (int pr = 0; pr < (F::kPair ? 2 : 1); ++pr) {
-#pragma unroll
-            for (int np = 0; np < N / 16; ++np) {
-              const int chunk = 2 * np + (lane >> 4);
-              uint32_t b4[4];
-              ldsm_x4_t(ps + st * Z::kP + pr * Z::kPHalf + (chunk >> 3) * Z::kPBlock + token * 128 + (((chunk & 7) ^ (token & 7)) << 4), b4);
-              mma16<F::kBf16 ? KITTY_BF16 : KITTY_F16>(c[2 * np], a, b4[0], b4[1]);
-              mma16<F::kBf16 ? KITTY_BF16 : KITTY_F16>(c[2 * np + 1], a, b4[2], b4[3]);
-            }
-          }
-        }
-      }
+        return a4;
+      };
+#pragma unroll 1
+      for (int g = 0; g < kTilePages; ++g)
+        if (mine && ((there >> g) & 1)) page_sums(pi + g * 4096, middles(g));
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_s(a_of(bar.pempty[st]));
-        if (F::kPacked) mbar_arrive_s(a_of(bar.vempty[op]));
-      }
+      if (lane == 0) mbar_arrive_s(a_of(bar.pempty[at4(i)]));
     }
     if (ok) {
 #pragma unroll
-      for (int nt = 0; nt < N / 8; ++nt) {
-        if (r < 4) *reinterpret_cast<float2*>(&sh.mid[r][8 * nt + 2 * qq]) = make_float2(c[nt][0], c[nt][1]);
-        if (r == 4) *reinterpret_cast<float2*>(&sh.sum[8 * nt + 2 * qq]) = make_float2(c[nt][0], c[nt][1]);
+      for (int nt = 0; nt < T; ++nt) {
+        const int y = 8 * (n0 + nt) + 2 * qq;
+        if (!mine) break;
+        if (r < 4) *reinterpret_cast<float2*>(&sh.mid[h][r][y]) = make_float2(c[nt][0], c[nt][1]);
+        if (r == 4) *reinterpret_cast<float2*>(&sh.sum[h][y]) = make_float2(c[nt][0], c[nt][1]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_s(a_of(bar.sums));
@@ -1210,6 +1312,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     }
     __syncwarp();
   }
+
   __syncthreads();
   // after a wait that ran out: nothing may be in flight when the block's memory is given back
   if (*abort != 0 && elect_one()) {
@@ -1288,19 +1391,26 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
 }
 
 // ------------------------------------------------------------- plan
+// Room for staged tiles beside the rest of a block's shared memory.
+template <class F>
+constexpr int staged_room() { return kSharedMost - (int)((sizeof(Shared<F::N>) + 127) / 128 * 128) - fixed_bytes<F>(); }
+
+static_assert(2 * kTilePages * 7296 <= staged_room<PackedTree<4, 4, 64>>() && 2 * kTilePages * 4224 <= staged_room<PackedTree<2, 2, 64>>(),
+              "two staged tiles of the largest pages");
+
 struct TreePlan {
   int rows, units, splits;  // rows of a block, blocks of a (sequence, kv head), splits of its tiles
 };
 
-// Rows of a block: the least of 16, 32, 64, 128 (16-bit pages: 64) that holds the largest tree's.
+// Rows of a block: the least of 16, 32, 64 that holds the largest tree's.
 // Splits: a block has an SM to itself, so as many as make the last round of blocks end soonest, with
 // a block's time its tiles' and a fixed part.
 TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int n_prefix, int max_pages) {
   const int rows = max_nodes * (cfg->num_q_heads / cfg->num_kv_heads);
   TreePlan pl = {16, 1, 1};
-  while (pl.rows < rows && pl.rows < (packed ? 128 : 64)) pl.rows *= 2;
+  while (pl.rows < rows && pl.rows < 64) pl.rows *= 2;
   pl.units = (rows + pl.rows - 1) / pl.rows;
-  const double tile_us = packed ? (pl.rows <= 32 ? 0.5 : pl.rows == 64 ? 0.7 : 1.1) : 1.5, fixed_us = 4.0;
+  const double tile_us = packed ? (pl.rows <= 32 ? 0.8 : 1.2) : 1.5, fixed_us = 4.0;
   const double own = cfg->decode_total_pages > 0 && B > 0 ? (double)cfg->decode_total_pages / B : max_pages;
   const int tiles = (int)((n_prefix + std::min(own, (double)max_pages) + kTilePages - 1) / kTilePages) + 1;
   const long blocks = (long)pl.units * cfg->num_kv_heads * B;
@@ -1344,15 +1454,13 @@ template <class F>
 int launch_tree(TreeParams& p, const CUtensorMap& map, cudaStream_t s) {
   using Z = Sizes<F>;
   static_assert(Z::kCols <= 512, "fits tensor memory");
-  constexpr int kMost = 227 * 1024 - (int)((sizeof(Shared<F::N>) + 127) / 128 * 128);
-  constexpr int kFixed = 1024 + Z::kFixed;
-  static_assert(kFixed + (F::kPacked ? 4 * (F::W == 2 ? 4224 : F::V == 2 ? 6272 : 7296) : 0) <= kMost, "one stage at least");
+  constexpr int kMost = staged_room<F>() + fixed_bytes<F>();
   // one block an SM: two would wait for each other's tensor memory
-  static_assert(kFixed + (int)sizeof(Shared<F::N>) > 100 * 1024 || F::kPacked, "one block an SM");
-  int smem = kFixed;
+  static_assert(F::kPacked || fixed_bytes<F>() > 116 * 1024, "one block an SM");
+  int smem = fixed_bytes<F>();
   if (F::kPacked) {
-    p.raw_stages = std::min(kMaxRaw, (kMost - kFixed) / (kTilePages * p.blob));
-    smem = std::max(kFixed + p.raw_stages * kTilePages * p.blob, 116 * 1024);
+    p.raw_stages = kMaxRaw * kTilePages * p.blob <= staged_room<F>() ? kMaxRaw : 2;
+    smem = std::max(smem + p.raw_stages * kTilePages * p.blob, 116 * 1024);
   }
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;
@@ -1378,8 +1486,7 @@ int launch_packed(TreeParams& p, int rows, cudaStream_t s) {
   switch (rows) {
     case 16: return launch_tree<PackedTree<W, V, 16>>(p, map, s);
     case 32: return launch_tree<PackedTree<W, V, 32>>(p, map, s);
-    case 64: return launch_tree<PackedTree<W, V, 64>>(p, map, s);
-    default: return launch_tree<PackedTree<W, V, 128>>(p, map, s);
+    default: return launch_tree<PackedTree<W, V, 64>>(p, map, s);
   }
 }
 template <bool BF>
