@@ -12,6 +12,11 @@ Beside the calls on rotated keys there are those from the projections (prefill_r
 extend_rope, append_rope, step_rope: norms and rotation on the way), and a prefix that the
 sequences share (share_prefix: its pages are stored once and attended once a call for the
 whole batch).
+
+Drafted tokens, chains or trees of them, are checked in one call (plan_trees, attend_tree) and
+the accepted path is appended (reserve, commit_tree).  How many that are is known on the device
+alone, so the page allocator moves there meanwhile (pages_to_device, pages_to_host): a step of
+drafting needs nothing from the host and can be captured into a graph.
 """
 
 from __future__ import annotations
@@ -40,6 +45,7 @@ class _SharedPrefix:
 
     def _prefix_plan(self, k_pages, v_pages, pages_of):
         """(pages of the prefix, pages of it that each sequence sees), checked."""
+        self._host_plans()
         if self.prefix is not None:
             raise ValueError("the cache has a shared prefix (drop_prefix)")
         if self.kv_tokens():
@@ -104,6 +110,7 @@ class _SharedPrefix:
         """Forget the shared prefix and give its pages back: between batches (clear), as the tokens
         of the sequences stand behind it.  Running statistics of the sequences that saw it start
         afresh.  Graphs captured with the prefix are not to be replayed any more."""
+        self._host_plans()
         if self.prefix is not None:
             self.alloc.free(self.prefix.cpu().numpy())
             self._forget_statistics(self.h_prefix > 0)
@@ -116,6 +123,7 @@ class _SharedPrefix:
         the allocator (those of a flush that was planned and not made, too), and lengths and
         running statistics start afresh, behind the prefix if there is one.  On the current
         stream."""
+        self._host_plans()
         self.alloc.alloc(self.alloc.free_count)  # so that all pages are in use
         keep = [] if self.prefix is None else self.prefix.cpu().numpy()
         self.alloc.free(np.setdiff1d(np.arange(self.pool_pages), keep))
@@ -136,8 +144,76 @@ class _SharedPrefix:
         return self.prefix.numel() * (self.cfg.num_kv_heads * self.blob + 4)
 
 
-class LayerCache(_SharedPrefix):
+class _DraftedTrees:
+    """Trees of drafted tokens behind the sequences of a layer's cache, and the pages of their
+    accepted ones.  What both caches keep of it: _device_lens (device lengths: num_pages or None,
+    and tokens behind them), _partial (whether a last, partial page is one), _read_lens (host
+    mirrors from the device's lengths)."""
+
+    free_ids = None    # device int32 [pool_pages]: a stack of free pages; None: the host plans
+    free_count = None  # device int32 [1]: its height
+    held = None        # device int32 [B]: pages in each row of the block table
+    tree_workspace = None
+
+    def _host_plans(self):
+        if self.free_ids is not None:
+            raise ValueError("the cache's pages are planned on the device (pages_to_host)")
+
+    def pages_to_device(self):
+        """Hand the free pages to the device: from now on reserve takes them, lengths change by
+        commit_tree, and what the host plans (prefill, plan_flush, plan_extend, prefixes, clear)
+        is refused, until pages_to_host.  On the current stream."""
+        self._host_plans()
+        dev = self.pool.device
+        ids = np.full(self.pool_pages, -1, np.int32)
+        held = torch.from_numpy(self._held_pages().astype(np.int32)).to(dev)
+        n = self.alloc.free_count
+        ids[:n] = self.alloc.alloc(n)[::-1]  # the stack's top is the page that the host would take
+        self.free_count = torch.tensor([n], dtype=torch.int32, device=dev)
+        self.held = held
+        self.free_ids = torch.from_numpy(ids).to(dev)
+
+    def pages_to_host(self):
+        """Give back what no token needs, and let the host plan again: synchronises."""
+        if self.free_ids is None:
+            raise ValueError("the cache's pages are planned on the host")
+        self.reserve(0)
+        self._read_lens()
+        n = int(self.free_count.item())
+        self.alloc.free(self.free_ids[:n].cpu().numpy())
+        self.free_ids = self.free_count = self.held = None
+
+    def plan_trees(self, parents, seq_start, visible, positions, stream=None):
+        """kitty.tree_plan behind this cache's tokens: which nodes each drafted token sees
+        (visible) and where it stands (positions), from parents [n] and seq_start [B + 1]."""
+        num_pages, lens = self._device_lens()
+        kitty.tree_plan(parents, seq_start, lens, visible, positions, num_pages=num_pages,
+                        pos_base=self.pos_base, status=self.status, stream=stream)
+
+    def reserve(self, extra: int, stream=None):
+        """Pages for `extra` more tokens of each sequence, as many as a path may be long, on the
+        device; pages beyond them go back to the stack."""
+        if self.free_ids is None:
+            raise ValueError("the cache's pages are planned on the host (pages_to_device)")
+        num_pages, lens = self._device_lens()
+        kitty.page_tables(lens, self.held, self.block_table, self.free_ids, self.free_count,
+                          num_pages=num_pages, extra=extra, partial=self._partial, shrink=True,
+                          status=self.status, stream=stream)
+
+    def _tree_call(self, q, max_nodes, sm_scale):
+        """(scale, keywords) of a call for q [n, Hq, 128], with a workspace that its plan fits."""
+        need = self._tree_bytes(self.cfg, self.B, q.shape[0], max_nodes, self.max_pages,
+                                0 if self.prefix is None else self.prefix.numel())
+        self.tree_workspace = self._grown(self.tree_workspace, max(need, 16))
+        sm = 1.0 / math.sqrt(D) if sm_scale is None else sm_scale
+        return sm, dict(prefix_table=self.prefix, prefix_pages=self.prefix_pages,
+                        workspace=self.tree_workspace, status=self.status)
+
+
+class LayerCache(_DraftedTrees, _SharedPrefix):
     _shared_bytes = staticmethod(kitty.shared_workspace_bytes)
+    _tree_bytes = staticmethod(kitty.tree_workspace_bytes)
+    _partial = False  # what does not fill a page stands in the tail
 
     def __init__(self, cfg: kitty.Config, B: int, max_pages: int, pool_pages: int,
                  device="cuda"):
@@ -169,6 +245,7 @@ class LayerCache(_SharedPrefix):
         """k_pages, v_pages: 16-bit tensors (int16 view) [sum(n_pages)*32, Hkv, D],
         sequence-major; k_tail, v_tail: [B, Hkv, 32, D] with tails[b] valid rows.
         page_order: optional permutation of the allocated ids (shuffled block table)."""
+        self._host_plans()
         n_pages = np.asarray(n_pages, np.int64)
         tails = np.zeros(self.B, np.int64) if tails is None else np.asarray(tails, np.int64)
         tot = int(n_pages.sum())
@@ -304,6 +381,7 @@ class LayerCache(_SharedPrefix):
     def plan_flush(self) -> np.ndarray:
         """Host decision for the next append: a fresh page id for each sequence whose
         tail completes a page, -1 elsewhere; advances the host mirror."""
+        self._host_plans()
         fl = np.full(self.B, -1, np.int32)
         full = np.nonzero(self.h_tail + 1 == PAGE)[0]
         full = full[self.h_pages[full] < self.max_pages]
@@ -371,6 +449,34 @@ class LayerCache(_SharedPrefix):
                                self.num_pages, self.tail_k, self.tail_v, self.tail_len, sm, out,
                                workspace=self.workspace, status=self.status, stream=stream)
 
+    def attend_tree(self, q, k, v, seq_start, visible, max_nodes: int, out, sm_scale=None, stream=None):
+        """Drafted tokens q [n, Hq, 128], rotated at their positions, attend to their sequences'
+        tokens, the shared prefix among them, and to the drafted k, v [n, Hkv, 128] that they see
+        (kitty.tree_attention).  Nothing is stored."""
+        sm, more = self._tree_call(q, max_nodes, sm_scale)
+        kitty.tree_attention(self.cfg, q, k, v, seq_start, visible, max_nodes, self.pool, self.pool_pages,
+                             self.block_table, self.num_pages, self.tail_k, self.tail_v, self.tail_len,
+                             sm, out, stream=stream, **more)
+
+    def commit_tree(self, k, v, seq_start, path, path_len, stream=None):
+        """Append each sequence's accepted drafted tokens, rows path[b, :path_len[b]] of its own in
+        k, v (kitty.tree_commit), into pages that reserve has taken for them."""
+        if self.free_ids is None:
+            raise ValueError("the cache's pages are planned on the host (pages_to_device)")
+        kitty.tree_commit(self.cfg, k, v, seq_start, path, path_len, self.tail_k, self.tail_v, self.tail_len,
+                          self.run_sum, self.run_sumsq, self.run_count, self.block_table, self.num_pages,
+                          self.pool, self.pool_pages, status=self.status, stream=stream)
+
+    def _device_lens(self):
+        return self.num_pages, self.tail_len
+
+    def _held_pages(self):
+        return self.h_pages
+
+    def _read_lens(self):
+        self.h_pages[:] = self.num_pages.cpu().numpy()
+        self.h_tail[:] = self.tail_len.cpu().numpy()
+
     def append_bytes(self, flush_ids, fused: bool = False) -> int:
         """Bytes one append must move: the new K/V token read and written into the
         tail and, per flushed (sequence, kv head), the full tail read, the page blob
@@ -386,18 +492,20 @@ class LayerCache(_SharedPrefix):
     def kv_tokens(self) -> int:
         """Cached tokens one decode call attends to, over the batch (host mirror):
         full pages and unquantized tail tokens."""
+        self._host_plans()
         return int(self.h_pages.sum()) * PAGE + int(self.h_tail.sum()) + self._prefix_tokens()
 
     def algorithmic_bytes(self) -> int:
         """Bytes one decode call must move: packed pages + tails + Q + O + block
         table entries (host mirror of the current lengths)."""
+        self._host_plans()
         Hkv, Hq = self.cfg.num_kv_heads, self.cfg.num_q_heads
         pages = int(self.h_pages.sum())
         return (pages * Hkv * self.blob + int(self.h_tail.sum()) * Hkv * D * 2 * 2
                 + self.B * Hq * D * 2 * 2 + pages * 4 + self._prefix_bytes())
 
 
-class F16LayerCache(_SharedPrefix):
+class F16LayerCache(_DraftedTrees, _SharedPrefix):
     """The unquantized 16-bit paged KV cache of one layer (the paper's comparison
     layout for its same-budget claims, Abstract), with the same decode-loop
     interface as LayerCache: every token lives in a 32-token page (no tail), a
@@ -405,6 +513,8 @@ class F16LayerCache(_SharedPrefix):
     the host mirrors every length."""
 
     _shared_bytes = staticmethod(kitty.f16kv_shared_workspace_bytes)
+    _tree_bytes = staticmethod(kitty.f16kv_tree_workspace_bytes)
+    _partial = True
 
     def __init__(self, cfg: kitty.Config, B: int, max_pages: int, pool_pages: int,
                  device="cuda"):
@@ -426,6 +536,7 @@ class F16LayerCache(_SharedPrefix):
         """As LayerCache.prefill: n_pages[b] full pages (k_pages, v_pages 16-bit
         [sum(n_pages)*32, Hkv, D], sequence-major) and tails[b] more tokens
         (k_tail, v_tail [B, Hkv, 32, D]), which go to a last, partial page."""
+        self._host_plans()
         n_pages = np.asarray(n_pages, np.int64)
         tails = np.zeros(self.B, np.int64) if tails is None else np.asarray(tails, np.int64)
         tot = int(n_pages.sum())
@@ -461,6 +572,7 @@ class F16LayerCache(_SharedPrefix):
     def plan_flush(self) -> np.ndarray:
         """Host decision for the next append: a fresh page id for each sequence whose
         next token starts a page, -1 elsewhere; advances the host mirror."""
+        self._host_plans()
         fl = np.full(self.B, -1, np.int32)
         new = np.nonzero(self.h_len % PAGE == 0)[0]
         new = new[self.h_len[new] // PAGE < self.max_pages]
@@ -481,6 +593,7 @@ class F16LayerCache(_SharedPrefix):
         """Host decision for appending lens[b] tokens to each sequence: (new_page_ids [T],
         seq_start [B + 1]), a fresh page id at every token that begins a page; advances the
         host mirror."""
+        self._host_plans()
         lens = np.asarray(lens, np.int64)
         if lens.shape != (self.B,) or (lens < 0).any():
             raise ValueError("lens: one length for each of %d sequences" % self.B)
@@ -551,16 +664,41 @@ class F16LayerCache(_SharedPrefix):
         self.append(k_new, v_new, new_page_ids, stream=stream)
         self.attend(q, out, sm_scale, stream=stream)
 
+    def attend_tree(self, q, k, v, seq_start, visible, max_nodes: int, out, sm_scale=None, stream=None):
+        """As LayerCache.attend_tree."""
+        sm, more = self._tree_call(q, max_nodes, sm_scale)
+        kitty.f16kv_tree_attention(self.cfg, q, k, v, seq_start, visible, max_nodes, self.pool,
+                                   self.pool_pages, self.block_table, self.ctx_len, sm, out,
+                                   stream=stream, **more)
+
+    def commit_tree(self, k, v, seq_start, path, path_len, stream=None):
+        """As LayerCache.commit_tree."""
+        if self.free_ids is None:
+            raise ValueError("the cache's pages are planned on the host (pages_to_device)")
+        kitty.f16kv_tree_commit(self.cfg, k, v, seq_start, path, path_len, self.pool, self.pool_pages,
+                                self.block_table, self.ctx_len, status=self.status, stream=stream)
+
+    def _device_lens(self):
+        return None, self.ctx_len
+
+    def _held_pages(self):
+        return (self.h_len + PAGE - 1) // PAGE
+
+    def _read_lens(self):
+        self.h_len[:] = self.ctx_len.cpu().numpy()
+
     def append_bytes(self, new_page_ids, fused: bool = False) -> int:
         """The new K/V token read and written into its page."""
         return self.B * self.cfg.num_kv_heads * D * 2 * 2 * 2
 
     def kv_tokens(self) -> int:
+        self._host_plans()
         return int(self.h_len.sum()) + self._prefix_tokens()
 
     def algorithmic_bytes(self) -> int:
         """Bytes one decode call must move: the K and V rows of every cached token,
         Q, O and the block-table entries (host mirror of the lengths)."""
+        self._host_plans()
         Hkv, Hq = self.cfg.num_kv_heads, self.cfg.num_q_heads
         pages = int(((self.h_len + PAGE - 1) // PAGE).sum())
         return (int(self.h_len.sum()) * Hkv * D * 2 * 2 + self.B * Hq * D * 2 * 2 + pages * 4

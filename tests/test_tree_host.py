@@ -133,3 +133,30 @@ def test_tensors_are_checked(K, monkeypatch):
         K._path(i32(1, 8), i32(2), 2, -1)
     with pytest.raises(ValueError, match="path_len"):
         K._path(i32(2, 8), i32(1), 2, -1)
+
+
+@pytest.mark.parametrize("kind", ["LayerCache", "F16LayerCache"])
+def test_pages_are_planned_in_one_place(K, kind):
+    """While the device plans the pages, what the host plans is refused, and the other way round."""
+    import numpy as np
+    import torch
+    from mixed_precision_bit_gb300 import cache
+    c = getattr(cache, kind)(K.Config(num_kv_heads=2, num_q_heads=4), 3, 4, 11, device="cpu")
+    with pytest.raises(ValueError, match="on the host"):
+        c.reserve(1)
+    with pytest.raises(ValueError, match="on the host"):
+        c.commit_tree(None, None, None, None, None)
+    with pytest.raises(ValueError, match="on the host"):
+        c.pages_to_host()
+    mine = c.alloc.alloc(2)
+    c.pages_to_device()
+    assert c.free_count.tolist() == [9] and c.held.tolist() == [0, 0, 0] and c.alloc.free_count == 0
+    ids = c.free_ids.tolist()
+    assert sorted(ids[:9] + list(mine)) == list(range(11)) and ids[9:] == [-1, -1]
+    for call in (c.plan_flush, c.clear, c.drop_prefix, c.kv_tokens, c.algorithmic_bytes, c.pages_to_device,
+                 lambda: c.prefill(None, None, np.zeros(3)), lambda: c.share_prefix(torch.zeros(32, 2, 128), None)):
+        with pytest.raises(ValueError, match="on the device"):
+            call()
+    if kind == "F16LayerCache":
+        with pytest.raises(ValueError, match="on the device"):
+            c.plan_extend([1, 1, 1])
