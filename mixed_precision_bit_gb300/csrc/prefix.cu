@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       uint4 v[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int x = sh.row[32 * wid + 2 * k + (lane >> 4)];
-        v[k] = x >= 0 ? *reinterpret_cast<const uint4*>(p.q + (size_t)x * kD + 8 * c) : make_uint4(0, 0, 0, 0);
+        const int x = sh.row[32 * wid + 2 * k + (lane >> 4)], seq = x / p.Hq;
+        v[k] = x >= 0 ? *reinterpret_cast<const uint4*>(p.q + seq * p.q_stride + (size_t)(x - seq * p.Hq) * kD + 8 * c) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int k = 0; k < 16; ++k) {

@@ -10,7 +10,8 @@
 namespace kitty {
 
 struct PrefixArgs {
-  const uint16_t* q;            // [B][Hq][128]
+  const uint16_t* q;            // [B][Hq][128], a row q_stride behind the other
+  size_t q_stride;
   const uint8_t* pool;
   const int32_t* table;         // [n_prefix] page ids
   const int32_t* prefix_pages;  // [B] or null: all share the whole prefix

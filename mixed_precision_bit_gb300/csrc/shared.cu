@@ -189,6 +189,7 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
   p.n_prefix = n_prefix;
   p.B = B;
   p.Hq = cfg->num_q_heads;
+  p.q_stride = (size_t)p.Hq * kD;
   p.Hkv = cfg->num_kv_heads;
   p.g = p.Hq / p.Hkv;
   p.n_hi = cfg->n_hi;

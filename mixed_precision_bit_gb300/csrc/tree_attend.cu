@@ -90,7 +90,9 @@ struct TreeParams {
   float sm_log2;
   uint32_t wait_polls;
   int n_tokens, max_nodes, pool_pages, n_prefix, max_pages, B, Hq, Hkv, g, n_hi, blob, in_dtype, out_dtype;
-  int units, splits, raw_stages;
+  const float* pre;  // the prefix kernel's partials, if it has attended the prefix
+  int units, splits, slots, raw_stages;  // slots: of them, a row
+  int direct;  // one partial a row: it is the output
 };
 
 // Packed pages: Key planes of W bits, Values of V bits; N rows.
@@ -560,7 +562,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   const Held hd = held_of<F::kPacked>(p, b);
   const int R = min(N, hd.n * p.g - unit * N);  // rows of this block
   if (hd.code != KITTY_ST_OK && unit == 0 && split == 0 && kvh == 0 && tid == 0) set_status(p.d_status, hd.code);
-  if (!hd.ok || R <= 0) return;
+  // behind a prefix kernel, which may still run: the last block ends after it, and so does this grid
+  auto end_behind = [&] {
+    if (p.slots > 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) grid_wait();
+  };
+  if (!hd.ok || R <= 0) {
+    end_behind();
+    return;
+  }
   const int pages = hd.prefix + hd.pages, tiles = (pages + kTilePages - 1) / kTilePages + 1;
   const int t0 = (int)((long)tiles * split / p.splits), n = (int)((long)tiles * (split + 1) / p.splits) - t0;
   // row x of the block: output row; node
@@ -570,6 +579,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
   };
   if (n == 0) {
     if (tid < R) p.ws[((size_t)out_row(tid) * p.splits + split) * kPartialFloats] = -INFINITY;
+    end_behind();
     return;
   }
   const bool has_loose = t0 + n == tiles;
@@ -856,7 +866,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           float o = 0.f;
           if (w0 != 0.f) o = (__uint_as_float(x[k]) * scale + (F::kPacked ? sh.mid[0][g][y] : 0.f)) * w0;
           if (w1 != 0.f) o += (__uint_as_float(x1[k]) * scale + (F::kPacked ? sh.mid[1][g][y] : 0.f)) * w1;
-          if (p.splits == 1) {
+          if (p.direct) {
             const float v = l != 0.f ? o / l : 0.f;
             const size_t at = (size_t)row * kD + ch;
             if (p.out_dtype == KITTY_F32) static_cast<float*>(p.out)[at] = v;
@@ -1334,41 +1344,60 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  end_behind();
 }
 
-// ------------------------------------------------------------- merge of the splits
-// A warp a row (query head of a drafted token), four channels a lane; eight partials requested at
-// once, with the row's maxima, a lane a split.
+// ------------------------------------------------------------- merge of the partials
+// What each drafted token sees of a prefix that not all sequences see whole, as the prefix kernel
+// takes it.  (Rows of no sequence: 0, set before.)
+template <bool PACKED>
+__global__ void __launch_bounds__(kMaxNodes) tree_prefix_rows_kernel(const TreeParams p, int32_t* rows) {
+  const Held hd = held_of<PACKED>(p, blockIdx.x);
+  if (hd.ok && (int)threadIdx.x < hd.n) rows[hd.first + threadIdx.x] = hd.prefix;
+  if (hd.code != KITTY_ST_OK && threadIdx.x == 0) set_status(p.d_status, hd.code);
+}
+
+// A warp a row (query head of a drafted token), four channels a lane; the maxima of 32 partials, a
+// lane a partial, and the outputs of eight requested at once.
 template <bool PACKED>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   const int b = blockIdx.y, lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5);
   const Held hd = held_of<PACKED>(p, b);
   if (!hd.ok || i >= hd.n * p.Hq) return;
   const size_t row = (size_t)hd.first * p.Hq + i;
-  const float* part = p.ws + row * p.splits * kPartialFloats;
+  const float *pre = p.pre + row * p.slots * kPartialFloats, *own = p.ws + row * p.splits * kPartialFloats;
+  const int n = p.slots + p.splits;
+  auto part = [&](int x) { return x < p.slots ? pre + (size_t)x * kPartialFloats : own + (size_t)(x - p.slots) * kPartialFloats; };
   grid_wait();
-  const float2 ml = lane < p.splits ? *reinterpret_cast<const float2*>(part + lane * kPartialFloats) : make_float2(-INFINITY, 0.f);
-  float m = ml.x;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  const float e = ml.x == -INFINITY ? 0.f : ex2a(ml.x - m);
-  float l = e == 0.f ? 0.f : ml.y * e;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < p.splits; s0 += 8) {
-    float4 x[8];
+  for (int x0 = 0; x0 < n; x0 += 32) {
+    const float2 ml = x0 + lane < n ? *reinterpret_cast<const float2*>(part(x0 + lane)) : make_float2(-INFINITY, 0.f);
+    float top = fmaxf(m, ml.x);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      x[k] = s0 + k < p.splits ? reinterpret_cast<const float4*>(part + (s0 + k) * kPartialFloats + 4)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (top == -INFINITY) continue;
+    const float f = m == -INFINITY ? 0.f : ex2a(m - top), e = ml.x == -INFINITY ? 0.f : ex2a(ml.x - top);
+    float more = e == 0.f ? 0.f : ml.y * e;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float w = __shfl_sync(0xFFFFFFFFu, e, (s0 + k) & 31);
-      if (s0 + k < p.splits && w != 0.f) {
-        o.x = fmaf(x[k].x, w, o.x);
-        o.y = fmaf(x[k].y, w, o.y);
-        o.z = fmaf(x[k].z, w, o.z);
-        o.w = fmaf(x[k].w, w, o.w);
+    for (int d = 16; d > 0; d >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, d);
+    l = l * f + more;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    m = top;
+    for (int s0 = x0; s0 < min(n, x0 + 32); s0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = s0 + k < n ? reinterpret_cast<const float4*>(part(s0 + k) + 4)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = __shfl_sync(0xFFFFFFFFu, e, (s0 + k) & 31);
+        if (w != 0.f) {  // (0 behind the last)
+          o.x = fmaf(x[k].x, w, o.x);
+          o.y = fmaf(x[k].y, w, o.y);
+          o.z = fmaf(x[k].z, w, o.z);
+          o.w = fmaf(x[k].w, w, o.w);
+        }
       }
     }
   }
@@ -1400,17 +1429,21 @@ static_assert(2 * kTilePages * 7296 <= staged_room<PackedTree<4, 4, 64>>() && 2 
 
 struct TreePlan {
   int rows, units, splits;  // rows of a block, blocks of a (sequence, kv head), splits of its tiles
+  double us;                // about how long that takes
+  PrefixPlan pre;           // of the prefix kernel, where it attends the prefix (splits: 0: it does not)
 };
 
 // Rows of a block: the least of 16, 32, 64 that holds the largest tree's.
 // Splits: a block has an SM to itself, so as many as make the last round of blocks end soonest, with
-// a block's time its tiles' and a fixed part.
-TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int n_prefix, int max_pages) {
+// a block's time its tiles' and a fixed part (us, measured on one block an SM: 2048 and 8192 tokens of
+// 4, 8, 16 nodes x 4 heads, packed 33 and 79, 39 and 87, 52 and 111; 16-bit 38 and 99, 42 and 103, 53 and
+// 126.  A fixed part of 4 or 10 instead chose the same or, on 16-bit pages, 8% more time).
+TreePlan list_plan(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int n_prefix, int max_pages) {
   const int rows = max_nodes * (cfg->num_q_heads / cfg->num_kv_heads);
-  TreePlan pl = {16, 1, 1};
+  TreePlan pl = {16, 1, 1, 0.0, {0, 0, 0}};
   while (pl.rows < rows && pl.rows < 64) pl.rows *= 2;
   pl.units = (rows + pl.rows - 1) / pl.rows;
-  const double tile_us = packed ? (pl.rows <= 32 ? 0.8 : 1.2) : 1.5, fixed_us = 4.0;
+  const double tile_us = packed ? (pl.rows <= 32 ? 1.0 : 1.3) : (pl.rows <= 32 ? 1.3 : 1.6), fixed_us = 7.0;
   const double own = cfg->decode_total_pages > 0 && B > 0 ? (double)cfg->decode_total_pages / B : max_pages;
   const int tiles = (int)((n_prefix + std::min(own, (double)max_pages) + kTilePages - 1) / kTilePages) + 1;
   const long blocks = (long)pl.units * cfg->num_kv_heads * B;
@@ -1421,13 +1454,39 @@ TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int max_nodes, i
     if (cost < best - 1e-9) {
       best = cost;
       pl.splits = s;
+      pl.us = cost;
     }
   }
   return pl;
 }
 
+// A shared prefix is either part of every sequence's tiles, or attended by the prefix kernel for all
+// drafted tokens at once, 256 rows a block, and merged.  The second prepares a page's operands for
+// four times the rows, and costs the prefix kernel's start and end and a launch or two more: its
+// blocks' time (as its own plan has it) is weighed here.  Sequences of 12 nodes x 4 heads behind 4096
+// tokens, tiles against prefix kernel, us: 1 sequence 42 against 56, 4 42 against 62, 8 54 against 69,
+// 16 75 against 84, 32 136 against 105.
+TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int n_tokens, int max_nodes, int n_prefix, int max_pages) {
+  TreePlan all = list_plan(cfg, packed, B, max_nodes, n_prefix, max_pages);
+  if (n_prefix == 0) return all;
+  TreePlan own = list_plan(cfg, packed, B, max_nodes, 0, max_pages);
+  own.pre = prefix_plan(cfg, packed, n_tokens, n_prefix, 0);
+  const long blocks = (long)own.pre.units * own.pre.splits, sms = sm_count();
+  const int pages = packed ? 3 : 4, tiles = (n_prefix + pages - 1) / pages;
+  const double tile_us = n_tokens * (cfg->num_q_heads / cfg->num_kv_heads) > 128 ? 1.8 : 0.9;
+  own.us += (double)((blocks + sms - 1) / sms) * ((tiles + own.pre.splits - 1) / own.pre.splits + 7) * tile_us + 6.0;
+  return own.us < all.us ? own : all;
+}
+
+size_t own_bytes(const kitty_cfg* cfg, const TreePlan& pl, int n_tokens) {
+  return pl.splits > 1 || pl.pre.splits > 0 ? (size_t)n_tokens * cfg->num_q_heads * pl.splits * kPartialFloats * sizeof(float) : 0;
+}
+// The prefix's partials, then the own ones, then what each token sees of the prefix.
+size_t prefix_bytes(const kitty_cfg* cfg, const TreePlan& pl, int n_tokens) {
+  return (size_t)n_tokens * cfg->num_q_heads * pl.pre.slots * kPartialFloats * sizeof(float);
+}
 size_t partial_bytes(const kitty_cfg* cfg, const TreePlan& pl, int n_tokens) {
-  return pl.splits > 1 ? (size_t)n_tokens * cfg->num_q_heads * pl.splits * kPartialFloats * sizeof(float) : 0;
+  return prefix_bytes(cfg, pl, n_tokens) + own_bytes(cfg, pl, n_tokens) + (pl.pre.splits > 0 ? (size_t)n_tokens * sizeof(int32_t) : 0);
 }
 
 bool rows_ok(const void* p, int64_t stride, int heads) {
@@ -1446,7 +1505,7 @@ int workspace(const kitty_cfg* cfg, bool packed, int B, int n_tokens, int max_no
   const int rc = check_tree(cfg, B, n_tokens, max_nodes, n_prefix, max_pages);
   if (rc != KITTY_OK) return rc;
   if (!bytes) return KITTY_ERR_INVALID_ARG;
-  *bytes = B == 0 || n_tokens == 0 ? 0 : partial_bytes(cfg, tree_plan_of(cfg, packed, B, max_nodes, n_prefix, max_pages), n_tokens);
+  *bytes = B == 0 || n_tokens == 0 ? 0 : partial_bytes(cfg, tree_plan_of(cfg, packed, B, n_tokens, max_nodes, n_prefix, max_pages), n_tokens);
   return KITTY_OK;
 }
 
@@ -1474,8 +1533,8 @@ int launch_tree(TreeParams& p, const CUtensorMap& map, cudaStream_t s) {
     opted_in.fetch_or(bit);
   }
   cudaError_t e = launch_behind(tree_kernel<F>, dim3((unsigned)(p.units * p.Hkv) * (unsigned)p.B, (unsigned)p.splits), kTreeThreads,
-                                (size_t)smem, s, false, p, map);
-  if (e == cudaSuccess && p.splits > 1)
+                                (size_t)smem, s, p.slots > 0, p, map);
+  if (e == cudaSuccess && !p.direct)
     e = launch_dependent(tree_merge_kernel<F::kPacked>, dim3((unsigned)((p.max_nodes * p.Hq + 3) / 4), (unsigned)p.B), 128, 0, s, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? KITTY_OK : KITTY_ERR_CUDA;
 }
@@ -1508,7 +1567,7 @@ int tree_params(const kitty_cfg* cfg, const void* q, int64_t q_stride, const voi
                 const uint64_t* visible, int32_t max_nodes, const void* pool, int32_t pool_pages,
                 const int32_t* prefix_table, int32_t n_prefix, const int32_t* prefix_pages,
                 const int32_t* block_table, int32_t max_pages, float sm_scale, void* out, int32_t out_dtype,
-                void* ws, size_t ws_bytes, int32_t B, int32_t* d_status, bool packed, int* rows, TreeParams* p) {
+                void* ws, size_t ws_bytes, int32_t B, int32_t* d_status, bool packed, TreePlan* plan, TreeParams* p) {
   const int rc = check_tree(cfg, B, n_tokens, max_nodes, n_prefix, max_pages);
   if (rc != KITTY_OK) return rc;
   if (pool_pages < 0 || (out_dtype != KITTY_F32 && out_dtype != KITTY_BF16 && out_dtype != KITTY_F16))
@@ -1521,14 +1580,18 @@ int tree_params(const kitty_cfg* cfg, const void* q, int64_t q_stride, const voi
       (max_pages > 0 && (!block_table || !pool)) || (n_prefix > 0 && (!prefix_table || !pool)) ||
       (pool && !aligned16(pool)))
     return KITTY_ERR_INVALID_ARG;
-  const TreePlan pl = tree_plan_of(cfg, packed, B, max_nodes, n_prefix, max_pages);
+  const TreePlan pl = tree_plan_of(cfg, packed, B, n_tokens, max_nodes, n_prefix, max_pages);
   const size_t need = partial_bytes(cfg, pl, n_tokens);
   if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return KITTY_ERR_WORKSPACE;
-  if ((uint64_t)pl.units * Hkv * B > 0x7FFFFFFFull || B > 65535) return KITTY_ERR_UNSUPPORTED;
-  *rows = pl.rows;
+  if ((uint64_t)pl.units * Hkv * B > 0x7FFFFFFFull || B > 65535 || (uint64_t)n_tokens * Hq > 0x7FFFFFFFull)
+    return KITTY_ERR_UNSUPPORTED;
+  *plan = pl;
   p->units = pl.units;
   p->splits = pl.splits;
-  p->ws = static_cast<float*>(ws);
+  p->slots = pl.pre.slots;
+  p->direct = pl.splits == 1 && pl.pre.slots == 0;
+  p->pre = static_cast<float*>(ws);
+  p->ws = static_cast<float*>(ws) + prefix_bytes(cfg, pl, n_tokens) / sizeof(float);
   p->wait_polls = cfg->decode_wait_polls > 0 ? (uint32_t)cfg->decode_wait_polls : kTreeWaitPolls;
   p->q = static_cast<const uint16_t*>(q);
   p->k = static_cast<const uint16_t*>(k);
@@ -1561,6 +1624,46 @@ int tree_params(const kitty_cfg* cfg, const void* q, int64_t q_stride, const voi
   return KITTY_OK;
 }
 
+// The prefix's partials by the prefix kernel, if the plan has it so: p goes on without a prefix.
+template <bool PACKED>
+int attend_prefix(const kitty_cfg* cfg, const TreePlan& pl, TreeParams& p, cudaStream_t s) {
+  if (pl.pre.splits == 0) return KITTY_OK;
+  int32_t* rows = nullptr;
+  if (p.prefix_pages != nullptr) {
+    rows = reinterpret_cast<int32_t*>(p.ws + own_bytes(cfg, pl, p.n_tokens) / sizeof(float));
+    if (cudaMemsetAsync(rows, 0, (size_t)p.n_tokens * sizeof(int32_t), s) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return KITTY_ERR_CUDA;
+    }
+    const cudaError_t e = launch_behind(tree_prefix_rows_kernel<PACKED>, dim3((unsigned)p.B), kMaxNodes, 0, s, false, p, rows);
+    if (e != cudaSuccess) return KITTY_ERR_CUDA;
+  }
+  PrefixArgs a = {};
+  a.q = p.q;
+  a.q_stride = p.q_stride;
+  a.pool = p.pool;
+  a.table = p.prefix_table;
+  a.prefix_pages = rows;
+  a.ws = const_cast<float*>(p.pre);
+  a.d_status = p.d_status;
+  a.sm_log2 = p.sm_log2;
+  a.wait_polls = cfg->decode_wait_polls > 0 ? (uint32_t)cfg->decode_wait_polls : 1u << 22;
+  a.pool_pages = p.pool_pages;
+  a.n_prefix = p.n_prefix;
+  a.B = p.n_tokens;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.g = p.g;
+  a.n_hi = p.n_hi;
+  a.blob = p.blob;
+  a.in_dtype = p.in_dtype;
+  a.splits = pl.pre.splits;
+  a.slots = pl.pre.slots;
+  p.n_prefix = 0;
+  p.prefix_pages = nullptr;
+  return prefix_launch(cfg, PACKED, a, pl.pre, s);
+}
+
 }  // namespace
 }  // namespace kitty
 
@@ -1587,10 +1690,10 @@ extern "C" int kitty_tree_attention(const kitty_cfg* cfg, const void* q, int64_t
                                     int32_t out_dtype, void* workspace, size_t workspace_bytes, int32_t B,
                                     int32_t* d_status, void* stream) {
   TreeParams p = {};
-  int rows = 0;
-  const int rc = tree_params(cfg, q, q_stride, k, k_stride, v, v_stride, n_tokens, seq_start, visible, max_nodes,
+  TreePlan pl = {};
+  int rc = tree_params(cfg, q, q_stride, k, k_stride, v, v_stride, n_tokens, seq_start, visible, max_nodes,
                              pool, pool_pages, prefix_table, n_prefix, prefix_pages, block_table, max_pages,
-                             sm_scale, out, out_dtype, workspace, workspace_bytes, B, d_status, true, &rows, &p);
+                             sm_scale, out, out_dtype, workspace, workspace_bytes, B, d_status, true, &pl, &p);
   if (rc != KITTY_OK) return rc == 1 ? KITTY_OK : rc;
   if (!num_pages || !tail_len || !tail_k || !tail_v || !aligned16(tail_k) || !aligned16(tail_v))
     return KITTY_ERR_INVALID_ARG;
@@ -1599,8 +1702,10 @@ extern "C" int kitty_tree_attention(const kitty_cfg* cfg, const void* q, int64_t
   p.tail_k = static_cast<const uint16_t*>(tail_k);
   p.tail_v = static_cast<const uint16_t*>(tail_v);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cfg->lo_bit == 2) return launch_packed<2, 2>(p, rows, s);
-  return v_bits(cfg) == 2 ? launch_packed<4, 2>(p, rows, s) : launch_packed<4, 4>(p, rows, s);
+  rc = attend_prefix<true>(cfg, pl, p, s);
+  if (rc != KITTY_OK) return rc;
+  if (cfg->lo_bit == 2) return launch_packed<2, 2>(p, pl.rows, s);
+  return v_bits(cfg) == 2 ? launch_packed<4, 2>(p, pl.rows, s) : launch_packed<4, 4>(p, pl.rows, s);
 }
 
 extern "C" int kitty_f16kv_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_stride, const void* k,
@@ -1612,13 +1717,15 @@ extern "C" int kitty_f16kv_tree_attention(const kitty_cfg* cfg, const void* q, i
                                           float sm_scale, void* out, int32_t out_dtype, void* workspace,
                                           size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream) {
   TreeParams p = {};
-  int rows = 0;
-  const int rc = tree_params(cfg, q, q_stride, k, k_stride, v, v_stride, n_tokens, seq_start, visible, max_nodes,
+  TreePlan pl = {};
+  int rc = tree_params(cfg, q, q_stride, k, k_stride, v, v_stride, n_tokens, seq_start, visible, max_nodes,
                              pool, pool_pages, prefix_table, n_prefix, prefix_pages, block_table, max_pages,
-                             sm_scale, out, out_dtype, workspace, workspace_bytes, B, d_status, false, &rows, &p);
+                             sm_scale, out, out_dtype, workspace, workspace_bytes, B, d_status, false, &pl, &p);
   if (rc != KITTY_OK) return rc == 1 ? KITTY_OK : rc;
   if (!ctx_len) return KITTY_ERR_INVALID_ARG;
   p.ctx_len = ctx_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cfg->in_dtype == KITTY_BF16 ? launch_plain<true>(p, rows, s) : launch_plain<false>(p, rows, s);
+  rc = attend_prefix<false>(cfg, pl, p, s);
+  if (rc != KITTY_OK) return rc;
+  return cfg->in_dtype == KITTY_BF16 ? launch_plain<true>(p, pl.rows, s) : launch_plain<false>(p, pl.rows, s);
 }
