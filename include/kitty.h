@@ -526,8 +526,9 @@ int kitty_f16kv_decode_shared(const kitty_cfg* cfg, const void* q, const void* p
  * Rows.  Sequence b's nodes are the rows seq_start[b] .. seq_start[b+1] - 1 of n_tokens
  * (seq_start device int32 [B + 1], rising from 0), at most KITTY_TREE_MAX_NODES of them, in
  * any order that puts parents before children; none is fine.  Rows from seq_start[B] on are
- * padding, neither read nor written.  A sequence whose starts are out of order or beyond
- * n_tokens sets KITTY_ST_BAD_SEQ, one with too many nodes KITTY_ST_BAD_LEN; it is skipped. */
+ * padding: nothing of theirs is written, and what their inputs hold has no effect.  A sequence
+ * whose starts are out of order or beyond n_tokens sets KITTY_ST_BAD_SEQ, one with too many
+ * nodes KITTY_ST_BAD_LEN; it is skipped. */
 #define KITTY_TREE_MAX_NODES 64
 
 /* Ancestor masks and positions.
@@ -593,12 +594,17 @@ int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32
  *   prefix_table, n_prefix, prefix_pages  as in kitty_decode_attention_shared; n_prefix = 0
  *              without a shared prefix
  *   out        device [n_tokens][Hq][128] of out_dtype, dense, 16-byte aligned
- *   workspace  device, >= kitty_tree_workspace_bytes of the same sizes, 16-byte aligned; calls
- *              that may overlap need one each
- * Other arguments, layouts and status codes as for kitty_decode_attention; g = Hq/Hkv <= 32.
- * The tensor cores take fp16: a query, or a tail's or a node's key or value that a query sees,
- * beyond its range sets KITTY_ST_RANGE (NaN or Inf: KITTY_ST_NONFINITE), and the outputs of the
- * rows that see it are then undefined; rows that do not see it are not affected. */
+ *   workspace  device, >= kitty_tree_workspace_bytes of the same configuration (its planning
+ *              hint, too) and sizes, 16-byte aligned; calls that may overlap need one each
+ * Other arguments, layouts and status codes as for kitty_decode_attention; g = Hq/Hkv <= 32,
+ * B <= 65535, n_tokens * Hq < 2^31 (else KITTY_ERR_UNSUPPORTED).
+ * The tensor cores take fp16: a query, or a tail's or a node's key that a query sees, beyond its
+ * range, or such a value beyond 16376, sets KITTY_ST_RANGE (NaN or Inf: KITTY_ST_NONFINITE), and
+ * the outputs of the rows that see it are then undefined; rows that do not see it are not
+ * affected.  So does a page whose Key step is 4096 or more or whose Value step is 8192 or more
+ * (tails of values below about 12000 never make one).
+ * Rounded are each probability and the middle of a group of 32 Values to fp16 (2^-11 of them)
+ * and, for 8-bit boosted Keys, step * code; the sum is that of the rounded probabilities. */
 int kitty_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
                                int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
                                size_t* bytes);
@@ -613,7 +619,9 @@ int kitty_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_stride, 
                          size_t workspace_bytes, int32_t B, int32_t* d_status, void* stream);
 
 /* The same over 16-bit pages: sequence b's cache holds ctx_len[b] tokens (behind the prefix).
- * Everything is taken in the input type; g <= 32. */
+ * Everything is taken in the input type, a probability as two halves of it; g <= 32,
+ * pool_pages * Hkv * 64 < 2^31.  A node's key or value that is not a number sets
+ * KITTY_ST_NONFINITE and counts as 0. */
 int kitty_f16kv_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
                                      int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
                                      size_t* bytes);

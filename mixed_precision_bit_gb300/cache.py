@@ -147,8 +147,9 @@ class _SharedPrefix:
 class _DraftedTrees:
     """Trees of drafted tokens behind the sequences of a layer's cache, and the pages of their
     accepted ones.  What both caches keep of it: _device_lens (device lengths: num_pages or None,
-    and tokens behind them), _partial (whether a last, partial page is one), _read_lens (host
-    mirrors from the device's lengths)."""
+    and tokens behind them), _partial (whether a last, partial page is one), _held_pages (of each
+    sequence, by the host), _read_lens (host mirrors from the device's lengths), _mirrored (whether they
+    are the same)."""
 
     free_ids = None    # device int32 [pool_pages]: a stack of free pages; None: the host plans
     free_count = None  # device int32 [1]: its height
@@ -162,8 +163,10 @@ class _DraftedTrees:
     def pages_to_device(self):
         """Hand the free pages to the device: from now on reserve takes them, lengths change by
         commit_tree, and what the host plans (prefill, plan_flush, plan_extend, prefixes, clear)
-        is refused, until pages_to_host.  On the current stream."""
+        is refused, until pages_to_host.  On the current stream; synchronises."""
         self._host_plans()
+        if not self._mirrored():
+            raise ValueError("lengths on the device are not the host's: a planned append has not been made")
         dev = self.pool.device
         ids = np.full(self.pool_pages, -1, np.int32)
         held = torch.from_numpy(self._held_pages().astype(np.int32)).to(dev)
@@ -477,6 +480,10 @@ class LayerCache(_DraftedTrees, _SharedPrefix):
         self.h_pages[:] = self.num_pages.cpu().numpy()
         self.h_tail[:] = self.tail_len.cpu().numpy()
 
+    def _mirrored(self):
+        return (np.array_equal(self.h_pages, self.num_pages.cpu().numpy())
+                and np.array_equal(self.h_tail, self.tail_len.cpu().numpy()))
+
     def append_bytes(self, flush_ids, fused: bool = False) -> int:
         """Bytes one append must move: the new K/V token read and written into the
         tail and, per flushed (sequence, kv head), the full tail read, the page blob
@@ -686,6 +693,9 @@ class F16LayerCache(_DraftedTrees, _SharedPrefix):
 
     def _read_lens(self):
         self.h_len[:] = self.ctx_len.cpu().numpy()
+
+    def _mirrored(self):
+        return np.array_equal(self.h_len, self.ctx_len.cpu().numpy())
 
     def append_bytes(self, new_page_ids, fused: bool = False) -> int:
         """The new K/V token read and written into its page."""

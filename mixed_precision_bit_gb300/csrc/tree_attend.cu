@@ -20,9 +20,9 @@
 // the block is the rate at which their instructions come: it was 3400 cycles a tile of 64 rows with
 // the loops unrolled (120 KB of code) and is 2500 with loops of a few dozen instructions
 // (94 KB, most of it run once; scores 16 columns at a time, a page's Keys in quarters).
-// Measured, 8 kv heads of 2-bit pages: 64 sequences x 8192 tokens x 16 nodes x 4 heads 335 us (411
-// TFLOP/s, 1.3 TB/s), 8 x 32768 x 64 nodes x 8 heads 863 us (638 TFLOP/s); of 16-bit pages: 32 x
-// 8192 x 16 x 4 210 us (5.1 TB/s).
+// Measured, 8 kv heads, contexts spread below the given lengths; 2-bit pages: 64 sequences x 8192 tokens x
+// 16 nodes x 4 heads 340 us (298 MB, 90 GFLOP: 270 TFLOP/s), 8 x 32768 x 64 nodes x 8 heads 863 us
+// (361 GFLOP: 420 TFLOP/s); 16-bit pages: 32 x 8192 x 16 x 4 210 us (715 MB: 3.4 TB/s).
 //
 // Packed pages (four to a tile) are staged whole by bulk copies and dequantized straight into
 // tensor memory: the planes' fragment order is that of 16-row stores of 128 bits, whose
@@ -1497,7 +1497,8 @@ int check_tree(const kitty_cfg* cfg, int B, int n_tokens, int max_nodes, int n_p
   const int rc = check_cfg(cfg, 32);
   if (rc != KITTY_OK) return rc;
   if (B < 0 || n_tokens < 0 || n_prefix < 0 || max_pages < 0 || max_nodes < 1) return KITTY_ERR_INVALID_ARG;
-  return max_nodes > kMaxNodes ? KITTY_ERR_UNSUPPORTED : KITTY_OK;
+  // (rows are counted in 32 bits)
+  return max_nodes > kMaxNodes || (uint64_t)n_tokens * cfg->num_q_heads > 0x7FFFFFFFull ? KITTY_ERR_UNSUPPORTED : KITTY_OK;
 }
 
 int workspace(const kitty_cfg* cfg, bool packed, int B, int n_tokens, int max_nodes, int n_prefix, int max_pages,
@@ -1583,8 +1584,7 @@ int tree_params(const kitty_cfg* cfg, const void* q, int64_t q_stride, const voi
   const TreePlan pl = tree_plan_of(cfg, packed, B, n_tokens, max_nodes, n_prefix, max_pages);
   const size_t need = partial_bytes(cfg, pl, n_tokens);
   if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return KITTY_ERR_WORKSPACE;
-  if ((uint64_t)pl.units * Hkv * B > 0x7FFFFFFFull || B > 65535 || (uint64_t)n_tokens * Hq > 0x7FFFFFFFull)
-    return KITTY_ERR_UNSUPPORTED;
+  if ((uint64_t)pl.units * Hkv * B > 0x7FFFFFFFull || B > 65535) return KITTY_ERR_UNSUPPORTED;
   *plan = pl;
   p->units = pl.units;
   p->splits = pl.splits;

@@ -160,3 +160,16 @@ def test_pages_are_planned_in_one_place(K, kind):
     if kind == "F16LayerCache":
         with pytest.raises(ValueError, match="on the device"):
             c.plan_extend([1, 1, 1])
+    # an append that was planned and not made: its page is in no table yet
+    c = getattr(cache, kind)(K.Config(num_kv_heads=2, num_q_heads=4), 3, 4, 11, device="cpu")
+    c.plan_flush()
+    with pytest.raises(ValueError, match="has not been made"):
+        c.pages_to_device()
+
+
+@pytest.mark.parametrize("name", ["kitty_tree_workspace_bytes", "kitty_f16kv_tree_workspace_bytes"])
+def test_rows_are_counted_in_32_bits(K, name):
+    cfg, n = K.Config(num_kv_heads=2, num_q_heads=4), ctypes.c_size_t()
+    f = getattr(K.load(), name)
+    assert f(cfg.ref(), 65535, (1 << 29) - 1, 64, 300, 8, ctypes.byref(n)) == 0
+    assert f(cfg.ref(), 65535, 1 << 29, 64, 300, 8, ctypes.byref(n)) == -2
