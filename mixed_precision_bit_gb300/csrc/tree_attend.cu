@@ -546,6 +546,7 @@ struct alignas(16) Shared {
   float weight[2][N], total[N];      // of the two pipelines' outputs; a row's sum
   int row[N];                  // output row (token, query head); -1: none
   unsigned long long sees[N];
+  uint32_t by[kMaxNodes][2];   // rows that see a node
 };
 
 template <class F>
@@ -642,6 +643,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     const int code = mag_code(mag, F::kPacked, p.in_dtype);
     if (split == 0 && code != KITTY_ST_OK) set_status(p.d_status, code);
   }
+  // the ids of this block's first eight tiles of pages, for the warps that request them
+  int first_ids = -1;
+  if (wid == kFetchWarp || (!F::kPacked && wid == kBiasWarp)) {
+    const int x = t0 * kTilePages + lane;
+    if (x < pages && lane / kTilePages < n)
+      first_ids = x < hd.prefix ? p.prefix_table[x] : p.block_table[(size_t)b * p.max_pages + x - hd.prefix];
+  }
   if (tid < N) {
     sh.row[tid] = tid < R ? out_row(tid) : -1;
     sh.m[0][tid] = sh.m[1][tid] = kFloor;
@@ -667,6 +675,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
         else set_status(p.d_status, KITTY_ST_BAD_PAGE);
       }
       sh.loose = there;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMaxNodes / (kTreeThreads / 32); ++k) {  // a row a lane
+      const int j = wid * (kMaxNodes / (kTreeThreads / 32)) + k;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int x = 32 * half + lane;
+        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, x < N && ((sh.sees[x % N] >> j) & 1ull) != 0);
+        if (lane == 0) sh.by[j][half] = rows;
+      }
     }
     __syncthreads();
   }
@@ -710,7 +729,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       const uint32_t prow = prow0 + at4(i) * Z::kP;
       tc_fence_after();
       const bool special = has_loose && i == n - 1;
-      const bool there = (there_of(i) >> g) & 1, masks = special && there, in = lane < loose_count(g);
+      const bool there = (there_of(i) >> g) & 1, masks = special && there;
+      uint32_t see[2] = {~0u, ~0u};  // rows that see this thread's token
+      if (masks && (g > 0 || lane >= hd.loose)) {
+        see[0] = g > 0 ? sh.by[node][0] : 0;
+        see[1] = g > 0 ? sh.by[node][1] : 0;
+      }
       const float scl = special ? sc : sc_page;
       // U rows' scores from tensor memory: scaled, shifted, masked
       auto scores = [&](int c0, uint32_t (&x)[U]) {
@@ -723,9 +747,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
           fma2(x[c + 2], x[c + 3], scl2, s4.z, s4.w);
         }
         if (masks) {
+          const uint32_t on = (c0 < 32 ? see[0] : see[1]) >> (c0 & 31);
 #pragma unroll
           for (int c = 0; c < U; ++c)
-            if (!in || (g > 0 && ((sh.sees[c0 + c] >> node) & 1ull) == 0)) x[c] = __float_as_uint(-INFINITY);
+            if (((on >> c) & 1u) == 0) x[c] = __float_as_uint(-INFINITY);
         }
       };
       bool moves = false, leave = false;
@@ -941,35 +966,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
             if (code != KITTY_ST_OK && loose_seen(g, lane)) set_status(p.d_status, code);
           }
         } else {
-          // a thread a channel; what no one sees, or fp16 cannot hold, is 0
+          // a thread a channel; what no one sees, or fp16 cannot hold (beyond 16376), is 0
           const float up = pow2(value_exp<F>(lane));
-          int code = KITTY_ST_OK;
+          const uint32_t most = p.in_dtype == KITTY_BF16 ? 0x467Fu : 0x73FFu;
+          uint32_t top = 0;  // the largest, as bits
 #pragma unroll 1
-          for (int x = 0; x < 3; ++x) {
-            const int count = loose_count(x);
+          for (int x = 0; x < 6; ++x) {  // 16 tokens
+            const int part = x >> 1, count = loose_count(part);
             if (count == 0) continue;
-            const uint32_t seen = x == 0 ? 0xFFFFFFFFu : sh.any[x - 1];
-            const uint32_t src = loose + (kLoose + 32 * x) * kLoosePitch + 2 * (32 * g + lane);
-            uint32_t w[16];
+            const uint32_t seen = (part == 0 ? 0xFFFFFFFFu : sh.any[part - 1]) & (count < 32 ? (1u << count) - 1 : 0xFFFFFFFFu);
+            const uint32_t on = seen >> (16 * (x & 1)), src = loose + (kLoose + 16 * x) * kLoosePitch + 2 * (32 * g + lane);
+            uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
               float f[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int t = 2 * k + e;
-                const bool on = t < count && ((seen >> t) & 1u) != 0;
-                f[e] = on ? bits16_to_f32((uint16_t)lds16(src + t * kLoosePitch), p.in_dtype) : 0.f;
-                if (!(fabsf(f[e]) <= 16376.f)) {
-                  if (code != KITTY_ST_NONFINITE) code = fabsf(f[e]) <= 3.4028235e38f ? KITTY_ST_RANGE : KITTY_ST_NONFINITE;
-                  f[e] = 0.f;
-                }
+                const uint32_t v = ((on >> (2 * k + e)) & 1u) != 0 ? lds16(src + (2 * k + e) * kLoosePitch) : 0u;
+                top = max(top, v & 0x7FFFu);
+                f[e] = (v & 0x7FFFu) <= most ? bits16_to_f32((uint16_t)v, p.in_dtype) : 0.f;
               }
               w[k] = h2_bits(__floats2half2_rn(f[0] * up, f[1] * up));
             }
-            tmem_st16(to + 16 * x, w);
-            if (lane < 4) sts128(mids + at4(i) * 1024 + 256 * x + 64 * g + 16 * lane, make_uint4(0, 0, 0, 0));
+            tmem_st8(to + 8 * x, w);
+            if (lane < 4) sts128(mids + at4(i) * 1024 + 256 * part + 64 * g + 16 * lane, make_uint4(0, 0, 0, 0));
           }
-          if (code != KITTY_ST_OK) set_status(p.d_status, code);
+          if (top > most)
+            set_status(p.d_status, top >= (p.in_dtype == KITTY_BF16 ? 0x7F80u : 0x7C00u) ? KITTY_ST_NONFINITE : KITTY_ST_RANGE);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1112,7 +1135,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       }
       if ((i & 7) == 0) {
         const int x = (t0 + i) * kTilePages + lane;
-        ids = x >= pages ? -1 : x < hd.prefix ? p.prefix_table[x] : p.block_table[(size_t)b * p.max_pages + x - hd.prefix];
+        ids = i == 0 ? first_ids : x >= pages ? -1 : x < hd.prefix ? p.prefix_table[x] : p.block_table[(size_t)b * p.max_pages + x - hd.prefix];
         if (ids < 0 || ids >= p.pool_pages) {
           if (!values && x < min(pages, (t0 + n) * kTilePages)) set_status(p.d_status, KITTY_ST_BAD_PAGE);
           ids = -1;
@@ -1165,7 +1188,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
       if (i == 0 || i - ids_at >= 8) {  // page ids of eight tiles
         ids_at = i;
         const int x = (t0 + i) * kTilePages + lane;
-        ids = x >= pages || (i + lane / 4) >= n ? -1 : x < hd.prefix ? p.prefix_table[x] : p.block_table[(size_t)b * p.max_pages + x - hd.prefix];
+        ids = i == 0 ? first_ids : x >= pages || (i + lane / 4) >= n ? -1 : x < hd.prefix ? p.prefix_table[x] : p.block_table[(size_t)b * p.max_pages + x - hd.prefix];
       }
       const int id = __shfl_sync(0xFFFFFFFFu, ids, 4 * (i - ids_at) + (lane & 3));
       const bool in = id >= 0 && id < p.pool_pages;
