@@ -5,6 +5,10 @@
 // What bounds them.  A few kilobytes each, but for the commits' rows: the latency of a launch and of
 // the loads that depend on one another.  So each takes one launch where it can, and loads what
 // does not depend on other loads together.
+// Measured in a CUDA graph (a launch alone is 2 us): masks and positions of 512 x 64 nodes 4.1 us; page
+// tables of a step of 64 sequences 6.2 us, of 256 prompts with slot maps 11.3 (a block, because a
+// sequence's pages depend on what those before it take); paths of 64 sequences into packed tails 8.2 us,
+// of 128 into 16-bit pages 6.2.
 #include "grid_dep.cuh"
 #include "host_common.h"
 #include "quant_tile.cuh"

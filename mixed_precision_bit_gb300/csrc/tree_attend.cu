@@ -21,8 +21,9 @@
 // the loops unrolled (120 KB of code) and is 2500 with loops of a few dozen instructions
 // (94 KB, most of it run once; scores 16 columns at a time, a page's Keys in quarters).
 // Measured, 8 kv heads, contexts spread below the given lengths; 2-bit pages: 64 sequences x 8192 tokens x
-// 16 nodes x 4 heads 340 us (298 MB, 90 GFLOP: 270 TFLOP/s), 8 x 32768 x 64 nodes x 8 heads 863 us
-// (361 GFLOP: 420 TFLOP/s); 16-bit pages: 32 x 8192 x 16 x 4 210 us (715 MB: 3.4 TB/s).
+// 16 nodes x 4 heads 330 us (298 MB, 90 GFLOP: 270 TFLOP/s), 8 x 32768 x 64 nodes x 8 heads 887 us
+// (361 GFLOP: 410 TFLOP/s), 4 x 1024 chains of 5 18 us; 16-bit pages: 32 x 8192 x 16 x 4 206 us (715 MB:
+// 3.5 TB/s).
 //
 // Packed pages (four to a tile) are staged whole by bulk copies and dequantized straight into
 // tensor memory: the planes' fragment order is that of 16-row stores of 128 bits, whose
@@ -1459,8 +1460,8 @@ struct TreePlan {
 // Rows of a block: the least of 16, 32, 64 that holds the largest tree's.
 // Splits: a block has an SM to itself, so as many as make the last round of blocks end soonest, with
 // a block's time its tiles' and a fixed part (us, measured on one block an SM: 2048 and 8192 tokens of
-// 4, 8, 16 nodes x 4 heads, packed 33 and 79, 39 and 87, 52 and 111; 16-bit 38 and 99, 42 and 103, 53 and
-// 126.  A fixed part of 4 or 10 instead chose the same or, on 16-bit pages, 8% more time).
+// 4, 8, 16 nodes x 4 heads, packed 34 and 82, 37 and 86, 47 and 111; 16-bit 37 and 98, 40 and 100, 50 and
+// 128.  A fixed part of 4 or 10 instead chose the same or, on 16-bit pages, 8% more time).
 TreePlan list_plan(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int n_prefix, int max_pages) {
   const int rows = max_nodes * (cfg->num_q_heads / cfg->num_kv_heads);
   TreePlan pl = {16, 1, 1, 0.0, {0, 0, 0}};
@@ -1486,9 +1487,9 @@ TreePlan list_plan(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int 
 // A shared prefix is either part of every sequence's tiles, or attended by the prefix kernel for all
 // drafted tokens at once, 256 rows a block, and merged.  The second prepares a page's operands for
 // four times the rows, and costs the prefix kernel's start and end and a launch or two more: its
-// blocks' time (as its own plan has it) is weighed here.  Sequences of 12 nodes x 4 heads behind 4096
-// tokens, tiles against prefix kernel, us: 1 sequence 42 against 56, 4 42 against 62, 8 54 against 69,
-// 16 75 against 84, 32 136 against 105.
+// blocks' time (as its own plan has it) is weighed here; what the two grids overlap pays for the rest.
+// Sequences of 12 nodes x 4 heads behind 4096 tokens, tiles against prefix kernel, us: 1 sequence 28
+// against 36, 4 38 against 44, 8 50 against 50, 16 73 against 60, 32 130 against 85, 64 250 against 147.
 TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int n_tokens, int max_nodes, int n_prefix, int max_pages) {
   TreePlan all = list_plan(cfg, packed, B, max_nodes, n_prefix, max_pages);
   if (n_prefix == 0) return all;
@@ -1497,7 +1498,7 @@ TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int n_tokens, in
   const long blocks = (long)own.pre.units * own.pre.splits, sms = sm_count();
   const int pages = packed ? 3 : 4, tiles = (n_prefix + pages - 1) / pages;
   const double tile_us = n_tokens * (cfg->num_q_heads / cfg->num_kv_heads) > 128 ? 1.8 : 0.9;
-  own.us += (double)((blocks + sms - 1) / sms) * ((tiles + own.pre.splits - 1) / own.pre.splits + 7) * tile_us + 6.0;
+  own.us += (double)((blocks + sms - 1) / sms) * ((tiles + own.pre.splits - 1) / own.pre.splits + 7) * tile_us;
   return own.us < all.us ? own : all;
 }
 
