@@ -155,6 +155,7 @@ class _DraftedTrees:
     free_count = None  # device int32 [1]: its height
     held = None        # device int32 [B]: pages in each row of the block table
     tree_workspace = None
+    _on_device = None  # those three tensors, kept: captured steps use them after the next pages_to_device, too
 
     def _host_plans(self):
         if self.free_ids is not None:
@@ -167,14 +168,15 @@ class _DraftedTrees:
         self._host_plans()
         if not self._mirrored():
             raise ValueError("lengths on the device are not the host's: a planned append has not been made")
-        dev = self.pool.device
+        if self._on_device is None:
+            self._on_device = tuple(torch.empty(n, dtype=torch.int32, device=self.pool.device)
+                                    for n in (self.pool_pages, 1, self.B))
         ids = np.full(self.pool_pages, -1, np.int32)
-        held = torch.from_numpy(self._held_pages().astype(np.int32)).to(dev)
         n = self.alloc.free_count
         ids[:n] = self.alloc.alloc(n)[::-1]  # the stack's top is the page that the host would take
-        self.free_count = torch.tensor([n], dtype=torch.int32, device=dev)
-        self.held = held
-        self.free_ids = torch.from_numpy(ids).to(dev)
+        for mine, value in zip(self._on_device, (ids, [n], self._held_pages())):
+            mine.copy_(torch.from_numpy(np.asarray(value, np.int32)))
+        self.free_ids, self.free_count, self.held = self._on_device
 
     def pages_to_host(self):
         """Give back what no token needs, and let the host plan again: synchronises."""
@@ -204,7 +206,8 @@ class _DraftedTrees:
                           status=self.status, stream=stream)
 
     def _tree_call(self, q, max_nodes, sm_scale):
-        """(scale, keywords) of a call for q [n, Hq, 128], with a workspace that its plan fits."""
+        """(scale, keywords) of a call for q [n, Hq, 128], with a workspace that its plan fits: the
+        cache's own, so one call at a time."""
         need = self._tree_bytes(self.cfg, self.B, q.shape[0], max_nodes, self.max_pages,
                                 0 if self.prefix is None else self.prefix.numel())
         self.tree_workspace = self._grown(self.tree_workspace, max(need, 16))

@@ -173,3 +173,16 @@ def test_steps_of_drafting(kind, rank, shared, graph):
         c.step_rope(rope, q[b:b + 1], k[b:b + 1].contiguous(), v[b:b + 1].contiguous(), torch.from_numpy(c.plan_flush()).cuda(),
                     one[:1], mine)
         assert (got[b] - mine[0]).abs().max().item() <= 4e-3 * mine.square().mean().sqrt().item()
+    if captured is None:
+        return
+    # the captured step after another hand-over: the last paths once more, behind what the host appended
+    before = [int(x) for x in (a.h_len if kind == "plain" else a.h_pages * P + a.h_tail)]
+    a.pages_to_device()
+    captured.replay()
+    a.pages_to_host()
+    after = [int(x) for x in (a.h_len if kind == "plain" else a.h_pages * P + a.h_tail)]
+    assert after == [x + len(y) for x, y in zip(before, paths)] and int(a.status.item()) == 0
+    held = a.h_pages if kind == "packed" else (a.h_len + P - 1) // P
+    assert a.alloc.free_count == a.pool_pages - shared - int(held.sum())
+    ids = np.concatenate([a.block_table[b, :held[b]].cpu().numpy() for b in range(B)])
+    assert (ids >= 0).all() and np.unique(ids).size == ids.size
