@@ -592,7 +592,8 @@ int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32
  *              every tree is a chain (node i sees the nodes 0 .. i)
  *   max_nodes  most nodes of a tree, 1 .. KITTY_TREE_MAX_NODES
  *   prefix_table, n_prefix, prefix_pages  as in kitty_decode_attention_shared; n_prefix = 0
- *              without a shared prefix
+ *              without a shared prefix; behind one q_stride is at most 2^29 (else
+ *              KITTY_ERR_UNSUPPORTED)
  *   out        device [n_tokens][Hq][128] of out_dtype, dense, 16-byte aligned
  *   workspace  device, >= kitty_tree_workspace_bytes of the same configuration (its planning
  *              hint, too) and sizes, 16-byte aligned; calls that may overlap need one each

@@ -502,6 +502,11 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
     if (p.prefix_pages != nullptr) my_pages = p.prefix_pages[b];
   }
   if (tid < kRows) sh.row[tid] = real ? (int)part_row : -1;
+  // the row's queries, 16 bytes a step behind those of its warp's first sequence (a division beside
+  // the loads below spilled the softmax's registers: 202 us against 177 at 128 sequences x 32768)
+  const int b0 = __shfl_sync(0xFFFFFFFFu, b, 0);
+  const uint32_t from = real ? (uint32_t)(b - b0) * (uint32_t)(p.q_stride / 8) + (uint32_t)(kvh * p.g + in_unit - b * p.g) * (kD / 8) : ~0u;
+  const uint4* q0 = reinterpret_cast<const uint4*>(p.q + b0 * p.q_stride);
   if (F::kPacked && tid < kStages * F::kPages * 4) {  // the row of ones behind each slab's middles
     const uint32_t at = vst + (tid / (4 * F::kPages)) * F::kVBytes + (tid / 4 % F::kPages) * F::kSlab + (kD + 4) * 64;
     sts128(at + 16 * (tid & 3), make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u));
@@ -553,8 +558,8 @@ __global__ void __launch_bounds__(threads_of<F>(), 1) prefix_kernel(const Prefix
       uint4 v[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const int x = sh.row[32 * wid + 2 * k + (lane >> 4)], seq = x / p.Hq;
-        v[k] = x >= 0 ? *reinterpret_cast<const uint4*>(p.q + seq * p.q_stride + (size_t)(x - seq * p.Hq) * kD + 8 * c) : make_uint4(0, 0, 0, 0);
+        const uint32_t x = __shfl_sync(0xFFFFFFFFu, from, 2 * k + (lane >> 4));
+        v[k] = x != ~0u ? q0[x + c] : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
@@ -984,7 +989,7 @@ namespace {
 
 template <class F>
 int launch(const PrefixArgs& a, const PrefixPlan& pl, const CUtensorMap& map, cudaStream_t s) {
-  static_assert(smem_of<F>() <= 227 * 1024 - 1024, "fits beside the static part");
+  static_assert(smem_of<F>() + (int)sizeof(Shared) <= 227 * 1024, "fits beside the static part");
   static_assert(2 * (F::kS + F::kO) <= 512, "fits tensor memory");
   static std::atomic<uint64_t> opted_in{0};
   int dev = 0;

@@ -11,7 +11,7 @@ namespace kitty {
 
 struct PrefixArgs {
   const uint16_t* q;            // [B][Hq][128], a row q_stride behind the other
-  size_t q_stride;
+  size_t q_stride;              // at most kPrefixMaxStride
   const uint8_t* pool;
   const int32_t* table;         // [n_prefix] page ids
   const int32_t* prefix_pages;  // [B] or null: all share the whole prefix
@@ -22,6 +22,9 @@ struct PrefixArgs {
   int pool_pages, n_prefix, B, Hq, Hkv, g, n_hi, blob, in_dtype;
   int splits, slots;            // of the prefix's tiles; partials a row
 };
+
+// A warp's 32 rows lie within 32 bits of 16-byte steps.
+constexpr size_t kPrefixMaxStride = size_t(1) << 29;
 
 struct PrefixPlan {
   int units;   // (kv head, 256 rows) blocks of a split

@@ -171,6 +171,7 @@ int shared_attention(const kitty_cfg* cfg, bool packed, const void* q, const voi
   if (n_prefix > 0 && (!prefix_table || !pool || !aligned16(pool))) return KITTY_ERR_INVALID_ARG;
   if (B == 0) return KITTY_OK;
   if (q && !aligned16(q)) return KITTY_ERR_INVALID_ARG;
+  if ((size_t)cfg->num_q_heads * kD > kPrefixMaxStride) return KITTY_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PrefixCall call = {cfg, packed, {}, prefix_plan(cfg, packed, B, n_prefix, max_pages), s};
   const size_t mine = prefix_bytes(cfg, call.plan, B);

@@ -1606,6 +1606,7 @@ int tree_params(const kitty_cfg* cfg, const void* q, int64_t q_stride, const voi
       (pool && !aligned16(pool)))
     return KITTY_ERR_INVALID_ARG;
   const TreePlan pl = tree_plan_of(cfg, packed, B, n_tokens, max_nodes, n_prefix, max_pages);
+  if (pl.pre.splits > 0 && (size_t)q_stride > kPrefixMaxStride) return KITTY_ERR_UNSUPPORTED;
   const size_t need = partial_bytes(cfg, pl, n_tokens);
   if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return KITTY_ERR_WORKSPACE;
   if ((uint64_t)pl.units * Hkv * B > 0x7FFFFFFFull || B > 65535) return KITTY_ERR_UNSUPPORTED;
