@@ -643,26 +643,28 @@ int kitty_f16kv_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_st
  * table holds at num_pages[b] already (kitty_page_tables).
  *   path       device int32 [B][path_width], places in the tree; path_width <=
  *              KITTY_TREE_MAX_NODES
- *   path_len   device int32 [B], 0 .. path_width
+ *   path_len   device int32 [B], 0 .. path_width.  With counted = 0 a sequence that is refused gets
+ *              0 there: what was appended, for the caller and for the layers that follow
  *   counted    0: tail_len and num_pages advance.  1: they count the accepted tokens already
- *              and are left as they are (layers that share one set of lengths)
+ *              and are left as they are: the layers behind the first of a model whose layers
+ *              share one set of lengths, with the path_len that the first one's call left
  * A sequence is appended to whole or not at all: KITTY_ST_BAD_TREE for a path entry outside its
  * tree or a path_len out of range, KITTY_ST_TABLE_FULL and KITTY_ST_BAD_PAGE for the pages of
  * its full tails, KITTY_ST_BAD_LEN for lengths out of range (a tail that is full already among
  * them).  Values out of range are reported as by kitty_append_token. */
 int kitty_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
-                      const int32_t* path, int32_t path_width, const int32_t* path_len,
+                      const int32_t* path, int32_t path_width, int32_t* path_len,
                       void* tail_k, void* tail_v, int32_t* tail_len, float* run_sum,
                       float* run_sumsq, int32_t* run_count, const int32_t* block_table,
                       int32_t max_pages, int32_t* num_pages, void* pool, int32_t pool_pages,
                       int32_t counted, int32_t B, int32_t* d_status, void* stream);
 
 /* The same into the 16-bit pages, at positions ctx_len[b] .. of the pages that the block table
- * holds; counted as above, of ctx_len. */
+ * holds; path_len and counted as above, of ctx_len. */
 int kitty_f16kv_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
                             int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
-                            const int32_t* path, int32_t path_width, const int32_t* path_len,
+                            const int32_t* path, int32_t path_width, int32_t* path_len,
                             void* pool, int32_t pool_pages, const int32_t* block_table,
                             int32_t max_pages, int32_t* ctx_len, int32_t counted, int32_t B,
                             int32_t* d_status, void* stream);

@@ -466,7 +466,8 @@ class LayerCache(_DraftedTrees, _SharedPrefix):
 
     def commit_tree(self, k, v, seq_start, path, path_len, stream=None):
         """Append each sequence's accepted drafted tokens, rows path[b, :path_len[b]] of its own in
-        k, v (kitty.tree_commit), into pages that reserve has taken for them."""
+        k, v (kitty.tree_commit), into pages that reserve has taken for them.  A sequence that has no
+        room for its path is not appended to, and its path_len becomes 0."""
         if self.free_ids is None:
             raise ValueError("the cache's pages are planned on the host (pages_to_device)")
         kitty.tree_commit(self.cfg, k, v, seq_start, path, path_len, self.tail_k, self.tail_v, self.tail_len,

@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(256) slots_kernel(const PageParams p) {
 struct CommitParams {
   const uint16_t *k, *v;
   size_t k_stride, v_stride;
-  const int32_t *seq_start, *path, *path_len, *block_table;
+  const int32_t *seq_start, *path, *block_table;
+  int32_t* path_len;  // of a refused sequence, set to 0 where the lengths advance
   uint16_t *tail_k, *tail_v;  // packed cache
   int32_t *tail_len, *num_pages;
   float *run_sum, *run_sumsq;
@@ -415,14 +416,20 @@ __global__ void __launch_bounds__(128) f16kv_tree_commit_kernel(const CommitPara
   }
 }
 
-// Lengths, once every head of a sequence has used the old ones: a block a sequence.
+// Lengths, once every head of a sequence has used the old ones: a block a sequence.  One that is refused
+// leaves a path of no tokens: layers that find the lengths counted already would take its last cached
+// tokens for the path's otherwise, and write over them.
 template <bool PACKED>
 __global__ void __launch_bounds__(kMaxNodes) tree_commit_finish(const CommitParams p) {
   __shared__ int rows[kMaxNodes];
   grid_wait();
   const int b = blockIdx.x;
   const Accepted a = accepted<PACKED>(p, b, false, rows);
-  if (!a.ok || threadIdx.x != 0) return;
+  if (threadIdx.x != 0) return;
+  if (!a.ok) {
+    p.path_len[b] = 0;
+    return;
+  }
   const long after = a.before + a.n;
   if (PACKED) {
     p.num_pages[b] = (int)(after / kPage);
@@ -439,7 +446,7 @@ bool rows_ok(const void* p, int64_t stride, int heads) {
 // Checks common to the commits; 1: nothing to do.
 int commit_params(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                   int32_t n_tokens, const int32_t* seq_start, const int32_t* path, int32_t path_width,
-                  const int32_t* path_len, const int32_t* block_table, int32_t max_pages, void* pool,
+                  int32_t* path_len, const int32_t* block_table, int32_t max_pages, void* pool,
                   int32_t pool_pages, int32_t counted, int32_t B, int32_t* d_status, CommitParams* p) {
   const int rc = check_cfg(cfg);
   if (rc != KITTY_OK) return rc;
@@ -526,7 +533,7 @@ extern "C" int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, 
 
 extern "C" int kitty_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
                                  int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
-                                 const int32_t* path, int32_t path_width, const int32_t* path_len,
+                                 const int32_t* path, int32_t path_width, int32_t* path_len,
                                  void* tail_k, void* tail_v, int32_t* tail_len, float* run_sum,
                                  float* run_sumsq, int32_t* run_count, const int32_t* block_table,
                                  int32_t max_pages, int32_t* num_pages, void* pool, int32_t pool_pages,
@@ -559,7 +566,7 @@ extern "C" int kitty_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_
 
 extern "C" int kitty_f16kv_tree_commit(const kitty_cfg* cfg, const void* k, int64_t k_stride, const void* v,
                                        int64_t v_stride, int32_t n_tokens, const int32_t* seq_start,
-                                       const int32_t* path, int32_t path_width, const int32_t* path_len,
+                                       const int32_t* path, int32_t path_width, int32_t* path_len,
                                        void* pool, int32_t pool_pages, const int32_t* block_table,
                                        int32_t max_pages, int32_t* ctx_len, int32_t counted, int32_t B,
                                        int32_t* d_status, void* stream) {

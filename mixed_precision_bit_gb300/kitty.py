@@ -803,7 +803,9 @@ def tree_commit(cfg: Config, k, v, seq_start, path, path_len, tail_k, tail_v, ta
                 status=None, stream=None):
     """The accepted drafted tokens, rows path[b, :path_len[b]] of each sequence's in k, v
     [n, Hkv, 128], into the packed cache (kitty_tree_commit); full tails are quantized into the
-    pages that the block table holds behind num_pages already (page_tables)."""
+    pages that the block table holds behind num_pages already (page_tables).  path_len of a sequence
+    that is refused becomes 0.  counted: lengths shared by several layers, which the first layer's
+    call has advanced: the later layers', with the path_len that it left."""
     dev, n, B, dt = _device(), k.shape[0], tail_len.numel(), cfg.in_dtype
     kp, ks = _rows(k, n, cfg.num_kv_heads, dev, dt)
     vp, vs = _rows(v, n, cfg.num_kv_heads, dev, dt)
