@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
     }
     fence_async_shared();
     const int code = mag_code(mag, F::kPacked, p.in_dtype);
-    if (split == 0 && code != KITTY_ST_OK) set_status(p.d_status, code);
+    // (by the split that takes the loose tokens: it alone has tiles in every sequence, however short)
+    if (has_loose && code != KITTY_ST_OK) set_status(p.d_status, code);
   }
   // the ids of this block's first eight tiles of pages, for the warps that request them
   int first_ids = -1;
