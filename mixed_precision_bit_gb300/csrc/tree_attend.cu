@@ -1388,7 +1388,12 @@ template <bool PACKED>
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
   const int b = blockIdx.y, lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5);
   const Held hd = held_of<PACKED>(p, b);
-  if (!hd.ok || i >= hd.n * p.Hq) return;
+  if (!hd.ok || i >= hd.n * p.Hq) {
+    // the call ends with this grid, so it waits for those before it even if no sequence has a row: the
+    // prefix kernel attends rows of padding, too, and writes their partials
+    grid_wait();
+    return;
+  }
   const size_t row = (size_t)hd.first * p.Hq + i;
   const float *pre = p.pre + row * p.slots * kPartialFloats, *own = p.ws + row * p.splits * kPartialFloats;
   const int n = p.slots + p.splits;
