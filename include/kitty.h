@@ -621,8 +621,8 @@ int kitty_tree_attention(const kitty_cfg* cfg, const void* q, int64_t q_stride, 
 
 /* The same over 16-bit pages: sequence b's cache holds ctx_len[b] tokens (behind the prefix).
  * Everything is taken in the input type, a probability as two halves of it; g <= 32,
- * pool_pages * Hkv * 64 < 2^31.  A node's key or value that is not a number sets
- * KITTY_ST_NONFINITE and counts as 0. */
+ * pool_pages * Hkv * 64 < 2^31.  An element of a node's key or value that is not a number (NaN
+ * or Inf) sets KITTY_ST_NONFINITE if a query sees the node, and counts as 0, that element alone. */
 int kitty_f16kv_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
                                      int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
                                      size_t* bytes);

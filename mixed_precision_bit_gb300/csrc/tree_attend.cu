@@ -521,6 +521,11 @@ __device__ __forceinline__ int mag_code(uint32_t m, bool packed, int in_dtype) {
   return KITTY_ST_OK;
 }
 
+// Two 16-bit values a word, 0 for those that are not numbers.
+__device__ __forceinline__ uint32_t numbers2(uint32_t x, int in_dtype) {
+  return x & __vcmpltu2(x & 0x7FFF7FFFu, in_dtype == KITTY_BF16 ? two(0x7F80) : two(0x7C00));
+}
+
 struct Bars {  // by tile parity
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];  // operands
   uint64_t sfull[2], sempty[2];
@@ -1029,11 +1034,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeParams 
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const int at = k0 + 256 * k + (tid & 255), t = at >> 4, c = at & 15;
-            if (t >= 32) {  // not a number: reported, and kept from those that do not see it
+            if (t >= 32) {  // elements that are not numbers: reported, and 0, so that they reach no one
               const int e = mag_code(mag2(mag2(mag2(mag2(0, v[k].x), v[k].y), v[k].z), v[k].w), false, p.in_dtype);
               if (e != KITTY_ST_OK) {
                 code = e;
-                v[k] = make_uint4(0, 0, 0, 0);
+                v[k] = make_uint4(numbers2(v[k].x, p.in_dtype), numbers2(v[k].y, p.in_dtype), numbers2(v[k].z, p.in_dtype),
+                                  numbers2(v[k].w, p.in_dtype));
               }
             }
             if (t < kLoose) sts128(to + (c >> 3) * Z::kHalf16 + t * 128 + (((c & 7) ^ (t & 7)) << 4), v[k]);
