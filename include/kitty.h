@@ -552,8 +552,9 @@ int kitty_tree_plan(const int32_t* parents, const int32_t* seq_start, int32_t n_
  * Sequence b is to have pages for
  *   n_b = 32 * num_pages[b] + lens[b] + (seq_start[b+1] - seq_start[b]) + extra   tokens,
  * ceil(n_b / 32) of them (partial = 1: a page that is begun counts, as in the 16-bit cache) or
- * floor(n_b / 32) (partial = 0: full pages only, as in the packed cache).  held[b] is how many
- * its row of the block table has.
+ * floor(n_b / 32) (partial = 0: full pages only, as in the packed cache), but no more than
+ * max_pages for the sake of `extra`, which are tokens that may come.  held[b] is how many its row
+ * of the block table has.
  *   more     pages are taken from the top of the stack, in order of sequences and of places
  *            in the row.  The sequences are served in order until one does not fit: that
  *            one and all later ones that need pages get none (KITTY_ST_NO_PAGES)
@@ -571,9 +572,9 @@ int kitty_tree_plan(const int32_t* parents, const int32_t* seq_start, int32_t n_
  *              there); rows from seq_start[B] on are left as they are
  *   new_page_ids device int32 [n_tokens] or NULL (needs seq_start): the page id where the token
  *              begins a page, else -1, as kitty_f16kv_append_rope takes them
- * A sequence that needs more than max_pages (KITTY_ST_TABLE_FULL), whose lengths are negative or
- * whose held is outside [0, max_pages] (KITTY_ST_BAD_LEN), or that would give back an id out of
- * range (KITTY_ST_BAD_PAGE) keeps its row.  A free_count outside [0, pool_pages] sets
+ * A sequence that needs more than max_pages without them (KITTY_ST_TABLE_FULL), whose lengths are
+ * negative or whose held is outside [0, max_pages] (KITTY_ST_BAD_LEN), or that would give back an
+ * id out of range (KITTY_ST_BAD_PAGE) keeps its row.  A free_count outside [0, pool_pages] sets
  * KITTY_ST_BAD_LEN and nothing changes. */
 int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32_t* seq_start,
                       int32_t n_tokens, int32_t extra, int32_t partial, int32_t shrink,

@@ -196,8 +196,8 @@ class _DraftedTrees:
                         pos_base=self.pos_base, status=self.status, stream=stream)
 
     def reserve(self, extra: int, stream=None):
-        """Pages for `extra` more tokens of each sequence, as many as a path may be long, on the
-        device; pages beyond them go back to the stack."""
+        """Pages for `extra` more tokens of each sequence, as many as a path may be long and its row of
+        the block table has room for, on the device; pages beyond them go back to the stack."""
         if self.free_ids is None:
             raise ValueError("the cache's pages are planned on the host (pages_to_device)")
         num_pages, lens = self._device_lens()

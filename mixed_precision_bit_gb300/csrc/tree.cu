@@ -109,7 +109,7 @@ struct PageParams {
 // Pages that sequence b is to have, or -1 (reported) when it keeps what it has; `have`: what it has.
 __device__ __forceinline__ int pages_wanted(const PageParams& p, int b, int& have) {
   have = p.held[b];
-  long n = (long)p.lens[b] + p.extra + (p.num_pages != nullptr ? (long)kPage * p.num_pages[b] : 0);
+  long n = (long)p.lens[b] + min(p.extra, 0) + (p.num_pages != nullptr ? (long)kPage * p.num_pages[b] : 0);
   bool bad = p.lens[b] < 0 || (p.num_pages != nullptr && p.num_pages[b] < 0) || have < 0 || have > p.max_pages;
   if (p.seq_start != nullptr) {
     int first, count;
@@ -121,12 +121,13 @@ __device__ __forceinline__ int pages_wanted(const PageParams& p, int b, int& hav
     set_status(p.d_status, KITTY_ST_BAD_LEN);
     return -1;
   }
-  const long want = (p.partial ? n + kPage - 1 : n) / kPage;
-  if (want > p.max_pages) {
+  const int begun = p.partial ? kPage - 1 : 0;
+  if ((n + begun) / kPage > p.max_pages) {
     set_status(p.d_status, KITTY_ST_TABLE_FULL);
     return -1;
   }
-  return (int)want;
+  // tokens that may come: as many as the row has room for
+  return (int)min((n + max(p.extra, 0) + begun) / kPage, (long)p.max_pages);
 }
 
 // Inclusive sum over the block's threads.  `sums`: 32 entries.

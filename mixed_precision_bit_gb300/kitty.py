@@ -715,9 +715,10 @@ def page_tables(lens, held, block_table, free_ids, free_count, num_pages=None, s
                 extra: int = 0, partial: bool = True, shrink: bool = False, slots=None,
                 new_page_ids=None, status=None, stream=None):
     """Pages for 32 * num_pages + lens tokens of each sequence, the new ones that seq_start [B + 1]
-    marks and `extra` more, from the stack free_ids[:free_count] on the device into the block
-    table, whose rows hold `held` pages; shrink: those beyond go back (kitty_page_tables).  slots
-    (64-bit) and new_page_ids (int32), one entry a new token, may be None."""
+    marks and `extra` more (of these as many as the row has room for), from the stack
+    free_ids[:free_count] on the device into the block table, whose rows hold `held` pages; shrink:
+    those beyond go back (kitty_page_tables).  slots (64-bit) and new_page_ids (int32), one entry a
+    new token, may be None."""
     dev, B = _device(), lens.numel()
     table, max_pages = _table(block_table, B, dev)
     n = max((t.numel() for t in (slots, new_page_ids) if t is not None), default=0)
