@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kPThreads) page_tables_kernel(const PageParams
           }
         }
         bad = __syncthreads_or(bad) != 0;
-        if (!bad && top + total <= p.pool_pages) {
+        if (!bad && total <= p.pool_pages - top) {  // (their sum may pass 32 bits)
           for (int j = tid; j < total; j += kPThreads) {
             const int s = owner(ends, kPThreads, j);
             const int col = base[s] + j - (s > 0 ? ends[s - 1] : 0);
