@@ -721,9 +721,8 @@ def page_tables(lens, held, block_table, free_ids, free_count, num_pages=None, s
     new token, may be None."""
     dev, B = _device(), lens.numel()
     table, max_pages = _table(block_table, B, dev)
-    n = max((t.numel() for t in (slots, new_page_ids) if t is not None), default=0)
-    if seq_start is not None and n == 0:
-        n = 0x7FFFFFFF  # no rows are written: any starts will do
+    # without a map no rows are written: any starts will do
+    n = max((t.numel() for t in (slots, new_page_ids) if t is not None), default=0 if seq_start is None else 0x7FFFFFFF)
     _chk("kitty_page_tables", load().kitty_page_tables(
         _ints("num_pages", num_pages, B, dev), _ints("lens", lens, B, dev),
         _ints("seq_start", seq_start, B + 1, dev), n, extra, int(partial), int(shrink),

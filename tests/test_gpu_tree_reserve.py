@@ -79,3 +79,16 @@ def test_the_last_paths_of_a_full_row(kind):
     assert int(c.status.item()) == kitty.ST["TABLE_FULL"] and total() == [most, most, 64]
     c.pages_to_host()
     assert c.alloc.free_count == 0
+
+
+def test_a_step_without_new_tokens():
+    """Slot maps without an entry: pages as without them."""
+    from mixed_precision_bit_gb300 import kitty
+    import torch
+    for empty in (dict(slots=torch.zeros(0, dtype=torch.int64, device="cuda")), dict(new_page_ids=dev32([]))):
+        t = dict(held=dev32([0, 0]), block_table=dev32([[-1] * 3] * 2), free_ids=dev32(np.arange(5)), free_count=dev32([5]))
+        st = status0()
+        kitty.page_tables(dev32([33, 0]), seq_start=dev32([0, 0, 0]), status=st, **empty, **t)
+        assert int(st.item()) == 0 and t["held"].cpu().tolist() == [2, 0] and t["block_table"].cpu().tolist()[0] == [4, 3, -1]
+        kitty.page_tables(dev32([33, 0]), seq_start=dev32([0, 0, 1]), status=st, **empty, **t)  # a token without an entry
+        assert int(st.item()) == kitty.ST["BAD_SEQ"]
