@@ -164,10 +164,13 @@ class _DraftedTrees:
     def pages_to_device(self):
         """Hand the free pages to the device: from now on reserve takes them, lengths change by
         commit_tree, and what the host plans (prefill, plan_flush, plan_extend, prefixes, clear)
-        is refused, until pages_to_host.  On the current stream; synchronises."""
+        is refused, until pages_to_host.  Refused while an append is planned and not made, as in the
+        layers of a ServingStep with graphs (cleared, or with graphs=False, they can be handed
+        over).  On the current stream; synchronises."""
         self._host_plans()
         if not self._mirrored():
-            raise ValueError("lengths on the device are not the host's: a planned append has not been made")
+            raise ValueError("lengths on the device are not the host's: a planned append has not been made (a ServingStep "
+                             "with graphs plans one step ahead: only clear() frees its layers)")
         if self._on_device is None:
             self._on_device = tuple(torch.empty(n, dtype=torch.int32, device=self.pool.device)
                                     for n in (self.pool_pages, 1, self.B))
@@ -755,7 +758,7 @@ class ServingStep:
     step are planned on the host while the graph of this one runs (the host
     mirrors of the layers run one step ahead between calls); two graphs read
     the plans from alternating pinned buffers.  Between run() calls the layers
-    must not be driven by other calls; a layer whose prefix has changed, or that was
+    must not be driven by other calls, nor their pages handed to the device; a layer whose prefix has changed, or that was
     cleared, since the graphs were captured is refused (they attend what it had then).
     graphs=False: direct calls; the flush plan of layer l is made just before
     its block goes up, so planning overlaps the kernels of the layers before it.
