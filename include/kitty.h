@@ -603,8 +603,13 @@ int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32
  * The tensor cores take fp16: a query, or a tail's or a node's key that a query sees, beyond its
  * range, or such a value beyond 16376, sets KITTY_ST_RANGE (NaN or Inf: KITTY_ST_NONFINITE), and
  * the outputs of the rows that see it are then undefined; rows that do not see it are not
- * affected.  So does a page whose Key step is 4096 or more or whose Value step is 8192 or more
- * (tails of values below about 12000 never make one).
+ * affected.  So does a page whose Key step is 4096 or more or whose Value step is 8192 or more.
+ * Steps are ranges (largest less smallest) over 3 for 2-bit codes, 15 for 4-bit ones (2-bit Keys
+ * boosted to 4 bits: 4/15, 4-bit Keys boosted to 8: 16/255), rounded up to seven bits: 2-bit Keys of
+ * magnitudes below 6096 and 2-bit Values below 12192 make none, nor do 4-bit Keys below 30480
+ * and 4-bit Values below 60960.  The pages of a shared prefix may be held to the limits of
+ * kitty_decode_attention_shared instead (steps of at most 65504 / 2^bits); which of the two goes by
+ * what is faster for the call, so steps are to be within both.
  * Rounded are each probability and the middle of a group of 32 Values to fp16 (2^-11 of them)
  * and, for 8-bit boosted Keys, step * code; the sum is that of the rounded probabilities. */
 int kitty_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
