@@ -611,7 +611,11 @@ int kitty_page_tables(const int32_t* num_pages, const int32_t* lens, const int32
  * kitty_decode_attention_shared instead (steps of at most 65504 / 2^bits); which of the two goes by
  * what is faster for the call, so steps are to be within both.
  * Rounded are each probability and the middle of a group of 32 Values to fp16 (2^-11 of them)
- * and, for 8-bit boosted Keys, step * code; the sum is that of the rounded probabilities. */
+ * and, for 8-bit boosted Keys, step * code; the sum is that of the rounded probabilities.  Near
+ * fp16's smallest numbers more is: a page's Value or a loose one is held times a power of two down
+ * to 2^-4, so each is off by up to 2^-21 once a step is below 2^-13, a bf16 Value below 2^-13 or an
+ * fp16 one below 2^-10; likewise a page's Key with a step below 2^-14 (8-bit boosted ones by up to
+ * 2^-19).  A bf16 query or loose key is off by up to 2^-25 below 2^-17. */
 int kitty_tree_workspace_bytes(const kitty_cfg* cfg, int32_t B, int32_t n_tokens,
                                int32_t max_nodes, int32_t n_prefix, int32_t max_pages,
                                size_t* bytes);

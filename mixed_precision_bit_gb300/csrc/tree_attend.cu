@@ -41,7 +41,10 @@
 // drafted ones, 32 + 64 at most, copied row by row; masks apply there alone.
 //
 // Roundings: p to fp16 (2^-11), a group's middle to fp16, for 8-bit boosted Keys step * code to
-// fp16; 16-bit pages: p to two halves.
+// fp16; 16-bit pages: p to two halves.  "Exact" above holds while the results are no subnormal fp16:
+// times 2^-4, Value steps below 2^-13 and loose Values below 2^-10 (bf16: 2^-13) lose up to 2^-21 each,
+// Key steps below 2^-14 likewise.  (A scale of the page's own would take its largest step first, and an
+// instruction a register in the loops that bound the block.)
 #include "prefix.h"
 
 #include <algorithm>

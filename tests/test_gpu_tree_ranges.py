@@ -1,5 +1,5 @@
 """How large and how small Keys and Values may be for the fp16 operands of packed pages: the limits that
-kitty.h states, from both sides."""
+kitty.h states, from both sides, and the rounding of what is near fp16's smallest numbers."""
 
 import numpy as np
 import pytest
@@ -77,3 +77,43 @@ def test_a_prefix_is_held_to_either_limit(what, lo_bit, v_bit, value, tiles, ker
         st = status0()
         c.run(status=st)
         assert int(st.item()) == code, B
+
+
+@pytest.mark.parametrize("lo_bit,v_bit", [(2, 2), (4, 4)])
+@pytest.mark.parametrize("scale", [2.0 ** -11, 2.0 ** -15, 2.0 ** -19])
+def test_small_values(scale, lo_bit, v_bit):
+    """Each off by 2^-21 at most, as the bound has it."""
+    r = np.random.default_rng(3)
+    c = PackedTree(2, 8, F16, own=[3, 1], tails=[5, 31], counts=[7, 12], n_hi=16, lo_bit=lo_bit, v_bit=v_bit, seed=2)
+    refill(c, r.standard_normal((P, D)), scale * r.standard_normal((P, D)))
+    c.tail_v = synth.to_bits(scale * synth.from_bits(c.tail_v, F16), F16)
+    c.put_cache()
+    c.rows[:, 10:] = synth.to_bits(scale * synth.from_bits(c.rows[:, 10:], F16), F16)
+    c.put_rows()
+    st = status0()
+    check(c, status=st)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("n_hi,lo_bit,v_bit", [(0, 2, 2), (16, 2, 2), (0, 4, 2), (16, 4, 4)])
+@pytest.mark.parametrize("scale", [2.0 ** -10, 2.0 ** -14, 2.0 ** -18])
+def test_small_keys(scale, n_hi, lo_bit, v_bit):
+    """A page's Key elements off by 2^-21 at most, with 8-bit boosted ones by 2^-19 (a sixteenth of a step, times a
+    low code, and two sums, each rounded at 2^-25 under 2^4): a score by that times the sum of |q|, which is as much
+    as 1/4 or 1 more in the magnitudes that the bound takes 2^-19 of."""
+    r = np.random.default_rng(3)
+    c = PackedTree(2, 8, F16, own=[3, 1], tails=[0, 0], counts=[7, 12], n_hi=n_hi, lo_bit=lo_bit, v_bit=v_bit, seed=2,
+                   q_scale=min(0.5 / scale, 2.0 ** 12))
+    refill(c, scale * r.standard_normal((P, D)), r.standard_normal((P, D)))
+    c.rows[:, 8:10] = synth.to_bits(scale * synth.from_bits(c.rows[:, 8:10], F16), F16)
+    c.put_rows()
+    held, more = c.cached, 1.0 if lo_bit == 4 and n_hi else 0.25
+
+    def cached(b, h):
+        k, v, part, size, most = held(b, h)
+        return k, v, part, size + more, most
+
+    c.cached = cached
+    st = status0()
+    check(c, status=st)
+    assert int(st.item()) == 0
