@@ -189,6 +189,7 @@ class _DraftedTrees:
         self._read_lens()
         n = int(self.free_count.item())
         self.alloc.free(self.free_ids[:n].cpu().numpy())
+        self.free_count.fill_(-1)  # a step captured before that is replayed now finds no stack: reported, no page taken
         self.free_ids = self.free_count = self.held = None
 
     def plan_trees(self, parents, seq_start, visible, positions, stream=None):
