@@ -5,10 +5,10 @@
 // What bounds them.  A few kilobytes each, but for the commits' rows: the latency of a launch and of
 // the loads that depend on one another.  So each takes one launch where it can, and loads what
 // does not depend on other loads together.
-// Measured in a CUDA graph (a launch alone is 2 us): masks and positions of 512 x 64 nodes 4.1 us; page
-// tables of a step of 64 sequences 6.2 us, of 256 prompts with slot maps 11.3 (a block, because a
-// sequence's pages depend on what those before it take); paths of 64 sequences into packed tails 8.2 us,
-// of 128 into 16-bit pages 6.2.
+// Measured, calls one after another in a CUDA graph: masks and positions of 512 x 64 nodes 1.9 us; page
+// tables of a step of 64 sequences, taken and given back, 9.7 us, of 256 prompts with slot maps 20.7 (a
+// block, because a sequence's pages depend on what those before it take); paths of 64 sequences into
+// packed tails 6.7 us, with the lengths 7.7, of 128 into 16-bit pages 3.4 and 4.1.
 #include "grid_dep.cuh"
 #include "host_common.h"
 #include "quant_tile.cuh"

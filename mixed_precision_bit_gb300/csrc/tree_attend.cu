@@ -21,8 +21,8 @@
 // the loops unrolled (120 KB of code) and is 2500 with loops of a few dozen instructions
 // (94 KB, most of it run once; scores 16 columns at a time, a page's Keys in quarters).
 // Measured, 8 kv heads, contexts spread below the given lengths; 2-bit pages: 64 sequences x 8192 tokens x
-// 16 nodes x 4 heads 330 us (298 MB, 90 GFLOP: 270 TFLOP/s), 8 x 32768 x 64 nodes x 8 heads 887 us
-// (361 GFLOP: 410 TFLOP/s), 4 x 1024 chains of 5 18 us; 16-bit pages: 32 x 8192 x 16 x 4 206 us (715 MB:
+// 16 nodes x 4 heads 322 us (298 MB, 90 GFLOP: 280 TFLOP/s), 8 x 32768 x 64 nodes x 8 heads 909 us
+// (361 GFLOP: 397 TFLOP/s), 4 x 1024 chains of 5 18 us; 16-bit pages: 32 x 8192 x 16 x 4 204 us (715 MB:
 // 3.5 TB/s).
 //
 // Packed pages (four to a tile) are staged whole by bulk copies and dequantized straight into
@@ -1503,8 +1503,9 @@ TreePlan list_plan(const kitty_cfg* cfg, bool packed, int B, int max_nodes, int 
 // drafted tokens at once, 256 rows a block, and merged.  The second prepares a page's operands for
 // four times the rows, and costs the prefix kernel's start and end and a launch or two more: its
 // blocks' time (as its own plan has it) is weighed here; what the two grids overlap pays for the rest.
-// Sequences of 12 nodes x 4 heads behind 4096 tokens, tiles against prefix kernel, us: 1 sequence 28
-// against 36, 4 38 against 44, 8 50 against 50, 16 73 against 60, 32 130 against 85, 64 250 against 147.
+// Sequences of 12 nodes x 4 heads behind 4096 tokens, tiles against prefix kernel, us: 1 sequence 29
+// against 37, 4 39 against 41, 8 51 against 47 (where the rule still takes the tiles), 16 74 against 60,
+// 32 132 against 85, 64 259 against 136.
 TreePlan tree_plan_of(const kitty_cfg* cfg, bool packed, int B, int n_tokens, int max_nodes, int n_prefix, int max_pages) {
   TreePlan all = list_plan(cfg, packed, B, max_nodes, n_prefix, max_pages);
   if (n_prefix == 0) return all;
