@@ -759,8 +759,9 @@ class ServingStep:
     step are planned on the host while the graph of this one runs (the host
     mirrors of the layers run one step ahead between calls); two graphs read
     the plans from alternating pinned buffers.  Between run() calls the layers
-    must not be driven by other calls, nor their pages handed to the device; a layer whose prefix has changed, or that was
-    cleared, since the graphs were captured is refused (they attend what it had then).
+    must not be driven by other calls, nor their pages handed to the device; a
+    layer whose prefix has changed, or that was cleared, since the graphs were
+    captured is refused (they attend what it had then).
     graphs=False: direct calls; the flush plan of layer l is made just before
     its block goes up, so planning overlaps the kernels of the layers before it.
     fused=False runs append then attend per layer.
